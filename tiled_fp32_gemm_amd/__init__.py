@@ -7,7 +7,10 @@ The functions ``sgemm``, ``sgemm_ex``, ``sgemm_ws``, ``sgemm_ws_noalloc``,
 (device pointers as integers, a HIP stream handle as an integer) and only
 marshal arguments: every step of the product runs in the HIP kernels.
 ``matmul`` is a convenience over torch tensors that derives the leading
-dimensions and the stream and calls ``sgemm_ex``.
+dimensions and the stream and calls ``sgemm_ex``.  ``epilogue`` (products
+with an epilogue and their gradients) and ``moe`` (expert routing and the experts'
+products) are the same for ``include/sgemm_linear.h`` and
+``include/sgemm_moe.h``; their functions are names of this module too.
 
 There is no fallback: if ``libsgemm.so`` has not been built, or does not load,
 importing the binding's functions raises.  Build it with
@@ -30,7 +33,11 @@ __all__ = ["sgemm", "sgemm_ex", "sgemm_plan_query", "sgemm_status_string",
            "sgemm_ladder", "sgemm_ladder_steps", "sgemm_ladder_name",
            "ladder_steps", "sgemm_ws", "sgemm_workspace_bytes",
            "sgemm_plan_query_ws", "sgemm_ws_noalloc", "ERR_SCRATCH_LIMIT",
-           "NOALLOC_MAX_BYTES"]
+           "NOALLOC_MAX_BYTES", "ACTIVATIONS", "LINEAR_SYMBOLS", "linear",
+           "linear_backward", "activation_backward", "MOE_SYMBOLS",
+           "MOE_MAX_EXPERTS", "moe_sort", "moe_permute", "moe_unpermute",
+           "moe_unpermute_backward", "grouped_linear",
+           "grouped_linear_backward"]
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_LAUNCH, ERR_SCRATCH_LIMIT = 0, 1, 2, 3, 4
 NOALLOC_MAX_BYTES = 32 << 20   # SGEMM_NOALLOC_MAX_BYTES
@@ -116,6 +123,8 @@ def load():
     lib.sgemm_workspace_bytes.restype = i64
     lib.sgemm_plan_query_ws.argtypes = common + [i64, ctypes.POINTER(SgemmPlan)]
     lib.sgemm_plan_query_ws.restype = i32
+    _epilogue.prototypes(lib)
+    _moe.prototypes(lib)
     _lib = lib
     return lib
 
@@ -298,3 +307,21 @@ def plan(A, B, out=None, algo: str | int = "auto") -> dict:
     if st != OK:
         raise SgemmError(st, "sgemm_plan_query")
     return p.as_dict()
+
+
+from . import epilogue as _epilogue  # noqa: E402  (they use the names above)
+from . import moe as _moe  # noqa: E402
+from .epilogue import (ACTIVATIONS, LINEAR_SYMBOLS, Epilogue,  # noqa: E402
+                       activation_backward, linear, linear_backward,
+                       sgemm_act_backward, sgemm_act_backward_workspace_bytes,
+                       sgemm_linear, sgemm_linear_plan_query,
+                       sgemm_linear_workspace_bytes)
+from .moe import (MOE_MAX_EXPERTS, MOE_SYMBOLS, grouped_linear,  # noqa: E402
+                  grouped_linear_backward, moe_permute, moe_sort,
+                  moe_unpermute, moe_unpermute_backward, sgemm_grouped,
+                  sgemm_grouped_act_backward,
+                  sgemm_grouped_act_backward_workspace_bytes,
+                  sgemm_grouped_wgrad, sgemm_grouped_wgrad_workspace_bytes,
+                  sgemm_grouped_workspace_bytes, sgemm_moe_permute,
+                  sgemm_moe_sort, sgemm_moe_sort_workspace_bytes,
+                  sgemm_moe_unpermute, sgemm_moe_unpermute_backward)

@@ -1,5 +1,6 @@
 """Builds libsgemm.so (the HIP kernels and the C ABI) and libsgemm_probe.so
-(the benchmark's clock probe) for gfx950 with hipcc.
+(the benchmark's clock probe) for gfx950 with hipcc.  The library's source
+files are compiled side by side and linked.
 
 ``python -m tiled_fp32_gemm_amd.build [--asm]`` compiles in-tree; ``--asm``
 also writes the device assembly next to the sources' build folder
@@ -7,10 +8,12 @@ also writes the device assembly next to the sources' build folder
 """
 from __future__ import annotations
 
+import concurrent.futures
 import glob
 import os
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -19,6 +22,7 @@ PROBE_LIB = os.path.join(HERE, "libsgemm_probe.so")
 ROOT = os.path.dirname(HERE)
 ASM_DIR = os.path.join(ROOT, "_build")
 ARCH = "gfx950"
+JOBS = 8     # compilations at once
 
 # Packed FP32 instructions are kept out of the generated code (the vector
 # kernels use single fused multiply-adds; the matrix kernels do not need them).
@@ -33,10 +37,15 @@ def sources() -> list[str]:
                   glob.glob(os.path.join(ROOT, "include", "*.h")))
 
 
-def _compile(src: str, out: str, verbose: bool) -> str:
+def library_sources() -> list[str]:
+    """The sources of libsgemm.so, the longest to compile first."""
+    names = sorted(glob.glob(os.path.join(CSRC, "*.hip")), key=os.path.getsize, reverse=True)
+    return [n for n in names if os.path.basename(n) != "probe.hip"]
+
+
+def _hipcc(args: list[str], out: str, verbose: bool) -> str:
     tmp = out + f".tmp{os.getpid()}"
-    cmd = ["hipcc", *DEVICE_FLAGS, "-fPIC", "-shared",
-           "-Wl,-rpath,/opt/rocm/lib", src, "-o", tmp]
+    cmd = ["hipcc", *DEVICE_FLAGS, "-fPIC", *args, "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
@@ -45,10 +54,16 @@ def _compile(src: str, out: str, verbose: bool) -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile ``csrc/sgemm.hip`` into ``libsgemm.so`` and ``csrc/probe.hip``
-    into ``libsgemm_probe.so`` (always recompiles)."""
-    _compile(os.path.join(CSRC, "probe.hip"), PROBE_LIB, verbose)
-    return _compile(os.path.join(CSRC, "sgemm.hip"), LIB, verbose)
+    """Compile the sources under ``csrc`` into ``libsgemm.so`` and
+    ``csrc/probe.hip`` into ``libsgemm_probe.so`` (always recompiles)."""
+    link = ["-shared", "-Wl,-rpath,/opt/rocm/lib"]
+    with tempfile.TemporaryDirectory() as objects, \
+            concurrent.futures.ThreadPoolExecutor(JOBS) as pool:
+        jobs = [pool.submit(_hipcc, ["-c", src], os.path.join(
+            objects, os.path.basename(src) + ".o"), verbose) for src in library_sources()]
+        probe = pool.submit(_hipcc, [*link, os.path.join(CSRC, "probe.hip")], PROBE_LIB, verbose)
+        probe.result()
+        return _hipcc([*link, *(j.result() for j in jobs)], LIB, verbose)
 
 
 def build_asm() -> str:

@@ -1,0 +1,344 @@
+// linear.hip -- the C ABI of include/sgemm_linear.h and the grouped products of
+// include/sgemm_moe.h: argument checks, kernel choice and launch.
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+#include <stdio.h>
+#include <string.h>
+
+#include "../../include/sgemm_linear.h"
+#include "../../include/sgemm_moe.h"
+#include "host.hpp"
+#include "kernel_act_backward.hpp"
+#include "kernel_linear_simple.hpp"
+
+namespace {
+
+using namespace sg::host;
+using sg::ActBackwardArgs;
+using sg::ProductArgs;
+
+typedef void (*ProductFn)(ProductArgs);
+
+struct Span {
+  const void* p;
+  int64_t bytes;   // 0: not touched; -1: beyond int64
+};
+
+// A span that is touched has to be there and aligned; one beyond int64 is
+// unsupported.
+int check_spans(const Span* s, int n) {
+  for (int i = 0; i < n; ++i)
+    if (s[i].bytes != 0 && (s[i].p == nullptr || ((uintptr_t)s[i].p & 3u)))
+      return SGEMM_ERR_INVALID_ARG;
+  for (int i = 0; i < n; ++i)
+    if (s[i].bytes < 0) return SGEMM_ERR_UNSUPPORTED;
+  return SGEMM_OK;
+}
+
+bool overlaps(const Span& a, const Span& b) {
+  return sg::host::overlaps(a.p, a.bytes, b.p, b.bytes);
+}
+
+int64_t at_least_one(int64_t n) { return n > 1 ? n : 1; }
+
+// Bytes of `groups` matrices of `one` bytes, `stride` floats apart.
+int64_t groups_bytes(int64_t groups, int64_t stride, int64_t one) {
+  if (groups == 0 || one <= 0) return groups == 0 ? 0 : one;
+  if (groups - 1 > (INT64_MAX / 4 - one) / at_least_one(stride)) return -1;
+  return (groups - 1) * stride * 4 + one;
+}
+
+// The operands of one call, checked.
+struct Product {
+  ProductArgs g;
+  bool trans_a, trans_b;
+  bool launch;   // false: nothing to do
+  Span a, b, c, bias, res, pre;
+};
+
+// Checks that hold for every kind: sizes, leading dimensions, epilogue,
+// pointers, overlaps.  Groups: stride_b (kRowGroups) or stride_c (kSumGroups).
+int check_product(int mode, int ta, int tb, int64_t M, int64_t N, int64_t K, int64_t groups,
+                  const int32_t* offsets, int64_t rows, const float* A, int64_t lda,
+                  const float* B, int64_t ldb, int64_t stride_b, float* C, int64_t ldc,
+                  int64_t stride_c, const sgemm_epilogue* ep, const void* ws, int64_t ws_bytes,
+                  Product& p) {
+  memset(&p, 0, sizeof(p));
+  if ((ta | tb) & ~1) return SGEMM_ERR_INVALID_ARG;
+  if (M < 0 || N < 0 || K < 0 || rows < 0 || groups < 0) return SGEMM_ERR_INVALID_ARG;
+  if (ws_bytes < 0 || (ws_bytes > 0 && ws == nullptr) || ((uintptr_t)ws & 3u))
+    return SGEMM_ERR_INVALID_ARG;
+  const int64_t ar = ta ? K : M, ac = ta ? M : K, br = tb ? N : K, bc = tb ? K : N;
+  if (lda < at_least_one(ac) || ldb < at_least_one(bc) || ldc < at_least_one(N))
+    return SGEMM_ERR_INVALID_ARG;
+  static const sgemm_epilogue none = {};
+  if (ep == nullptr) ep = &none;
+  if (ep->act < SGEMM_ACT_NONE || ep->act > SGEMM_ACT_SILU) return SGEMM_ERR_INVALID_ARG;
+  if ((ep->residual && ep->ldr < at_least_one(N)) || (ep->preact && ep->ldp < at_least_one(N)) ||
+      (mode == sg::kRowGroups && ep->bias && ep->ldbias < at_least_one(N)))
+    return SGEMM_ERR_INVALID_ARG;
+  if (groups > sg::kMaxGroups) return SGEMM_ERR_UNSUPPORTED;
+
+  const bool touch = M > 0 && N > 0 && (mode == sg::kDense || groups > 0);
+  p.launch = touch;
+  if (!touch) return SGEMM_OK;
+  const bool sums = mode == sg::kSumGroups;
+  p.a = {A, span_bytes(ar, ac, lda)};
+  p.b = {B, span_bytes(br, bc, ldb)};
+  p.c = {C, span_bytes(M, N, ldc)};
+  p.res = {ep->residual, ep->residual ? span_bytes(M, N, ep->ldr) : 0};
+  p.pre = {ep->preact, ep->preact ? span_bytes(M, N, ep->ldp) : 0};
+  p.bias = {ep->bias, !ep->bias ? 0 : mode == sg::kRowGroups
+                                          ? groups_bytes(groups, ep->ldbias, N * 4) : N * 4};
+  p.g.a_bytes = p.a.bytes;
+  p.g.b_bytes = p.b.bytes;
+  p.g.c_bytes = p.c.bytes;
+  if (mode == sg::kRowGroups) {
+    if (p.b.bytes > 0 && groups > 1 && stride_b < p.b.bytes / 4) return SGEMM_ERR_INVALID_ARG;
+    p.b.bytes = groups_bytes(groups, stride_b, p.b.bytes);
+  }
+  if (sums) {
+    if (p.c.bytes > 0 && groups > 1 && stride_c < p.c.bytes / 4) return SGEMM_ERR_INVALID_ARG;
+    p.c.bytes = groups_bytes(groups, stride_c, p.c.bytes);
+  }
+  const Span off = {offsets, mode == sg::kDense ? 0 : (groups + 1) * 4};
+  const Span all[] = {p.a, p.b, p.c, p.bias, p.res, p.pre, off};
+  const int st = check_spans(all, 7);
+  if (st != SGEMM_OK) return st;
+  if (M > kMaxDim || N > kMaxDim || K > kMaxDim || rows > kMaxDim) return SGEMM_ERR_UNSUPPORTED;
+  const bool in_place = ep->residual == C && ep->ldr == ldc;
+  if (overlaps(p.c, p.a) || overlaps(p.c, p.b) || overlaps(p.c, p.bias) ||
+      overlaps(p.c, p.pre) || overlaps(p.c, off) || (!in_place && overlaps(p.c, p.res)) ||
+      overlaps(p.pre, p.a) || overlaps(p.pre, p.b) || overlaps(p.pre, p.bias) ||
+      overlaps(p.pre, p.res) || overlaps(p.pre, off))
+    return SGEMM_ERR_INVALID_ARG;
+
+  ProductArgs& g = p.g;
+  p.trans_a = ta;
+  p.trans_b = tb;
+  g.A = A;
+  g.B = B;
+  g.C = C;
+  g.M = (int)M;
+  g.N = (int)N;
+  g.K = (int)K;
+  // A leading dimension only matters past the first row of an operand.
+  g.lda = (int)(ar > 1 ? lda : at_least_one(ac));
+  g.ldb = (int)(br > 1 ? ldb : at_least_one(bc));
+  g.ldc = (int)(M > 1 ? ldc : N);
+  g.bias = ep->bias;
+  g.residual = ep->residual;
+  g.preact = ep->preact;
+  g.ld_bias = ep->ldbias;
+  g.ldr = (int)(M > 1 ? ep->ldr : N);
+  g.ldp = (int)(M > 1 ? ep->ldp : N);
+  g.act = ep->act;
+  g.mode = mode;
+  g.groups = mode == sg::kDense ? 1 : (int)groups;
+  g.rows = (int)rows;
+  g.offsets = offsets;
+  g.stride_b = stride_b;
+  g.stride_c = stride_c;
+  g.splits = 1;
+  return SGEMM_OK;
+}
+
+int launch_product(ProductFn fn, const ProductArgs& g, int64_t workgroups, int threads,
+                   hipStream_t stream) {
+  ProductArgs args = g;
+  void* kargs[] = {&args};
+  const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(fn),
+                                       dim3((unsigned)workgroups), dim3(threads), kargs, 0, stream);
+  return e == hipSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH;
+}
+
+// Leading dimensions are ints in the kernels.
+bool lds_fit(const Product& p, int64_t lda, int64_t ldb, int64_t ldc, const sgemm_epilogue* ep) {
+  const int64_t lim = int64_t(1) << 29;
+  return (p.a.bytes == 0 || p.g.lda == 1 || lda < lim) && ldb < lim && ldc < lim &&
+         (!ep || !ep->residual || ep->ldr < lim) && (!ep || !ep->preact || ep->ldp < lim);
+}
+
+int run_product(Product& p, hipStream_t stream) {
+  ProductArgs& g = p.g;
+  g.tiles_n = (int)cdiv(g.N, 16);
+  g.tiles_m = (int)cdiv(g.M, 16);
+  const int64_t rows = g.mode == sg::kRowGroups
+                           ? g.tiles_m + (g.groups < g.M ? g.groups : g.M)
+                           : (int64_t)g.tiles_m * g.groups;
+  const int64_t wgs = rows * g.tiles_n;
+  if (!grid_fits(wgs, 256)) return SGEMM_ERR_UNSUPPORTED;
+  static const ProductFn table[4] = {
+      sg::product_simple_kernel<false, false>, sg::product_simple_kernel<false, true>,
+      sg::product_simple_kernel<true, false>, sg::product_simple_kernel<true, true>};
+  return launch_product(table[(p.trans_a ? 2 : 0) | (p.trans_b ? 1 : 0)], g, wgs, 256, stream);
+}
+
+// Strips of rows per group: enough workgroups for the chip, strips of 16 rows
+// or more, within the workspace.
+int64_t act_strips(int64_t M, int64_t N, int64_t groups, int64_t ws_bytes) {
+  const int64_t blocks = cdiv(N, sg::kActCols) * groups;
+  int64_t s = cdiv(8 * kCUs, blocks);
+  const int64_t most = cdiv(cdiv(M, groups), 16);
+  if (s > most) s = most;
+  const int64_t room = ws_bytes / 4 / (groups * N);
+  if (s > room) s = room;
+  return s < 1 ? 1 : s;
+}
+
+int act_backward(int64_t M, int64_t N, int64_t groups, const int32_t* offsets, bool grouped,
+                 const float* dC, int64_t lddc, const float* Z, int64_t ldz, int act, float* dZ,
+                 int64_t lddz, float* dbias, int64_t lddb, hipStream_t stream, void* ws,
+                 int64_t ws_bytes) {
+  if (M < 0 || N < 0 || groups < 0 || act < SGEMM_ACT_NONE || act > SGEMM_ACT_SILU)
+    return SGEMM_ERR_INVALID_ARG;
+  if (ws_bytes < 0 || (ws_bytes > 0 && ws == nullptr) || ((uintptr_t)ws & 3u))
+    return SGEMM_ERR_INVALID_ARG;
+  const int64_t n1 = at_least_one(N);
+  if (act == SGEMM_ACT_NONE) Z = nullptr;
+  if (lddc < n1 || (act != SGEMM_ACT_NONE && ldz < n1) || (dZ && lddz < n1) ||
+      (grouped && dbias && lddb < n1))
+    return SGEMM_ERR_INVALID_ARG;
+  if (groups > sg::kMaxGroups) return SGEMM_ERR_UNSUPPORTED;
+  if (N == 0 || groups == 0 || (!dZ && !dbias) || (M == 0 && !dbias)) return SGEMM_OK;
+  const Span c = {dC, span_bytes(M, N, lddc)};
+  const Span z = {Z, act != SGEMM_ACT_NONE ? span_bytes(M, N, ldz) : 0};
+  const Span d = {dZ, dZ ? span_bytes(M, N, lddz) : 0};
+  const Span b = {dbias, !dbias ? 0 : grouped ? groups_bytes(groups, lddb, N * 4) : N * 4};
+  const Span off = {offsets, grouped ? (groups + 1) * 4 : 0};
+  const Span all[] = {c, z, d, b, off};
+  const int st = check_spans(all, 5);
+  if (st != SGEMM_OK) return st;
+  if (M > kMaxDim || N > kMaxDim) return SGEMM_ERR_UNSUPPORTED;
+  const bool on_c = dZ == dC && lddz == lddc, on_z = Z && dZ == Z && lddz == ldz;
+  if ((!on_c && overlaps(d, c)) || (!on_z && overlaps(d, z)) || overlaps(b, c) ||
+      overlaps(b, z) || overlaps(b, d) || overlaps(off, d) || overlaps(off, b))
+    return SGEMM_ERR_INVALID_ARG;
+
+  ActBackwardArgs a;
+  a.dC = dC;
+  a.Z = Z;
+  a.dZ = dZ;
+  a.dbias = dbias;
+  a.W = static_cast<float*>(ws);
+  a.lddc = lddc;
+  a.ldz = ldz;
+  a.lddz = lddz;
+  a.lddb = grouped ? lddb : 0;
+  a.offsets = grouped ? offsets : nullptr;
+  a.M = (int)M;
+  a.N = (int)N;
+  a.groups = (int)groups;
+  a.act = act;
+  a.blocks_n = (int)cdiv(N, sg::kActCols);
+  // Without sums the strips need no room.
+  const int64_t strips = act_strips(M, N, groups, dbias ? ws_bytes : INT64_MAX);
+  a.strips = (int)strips;
+  if (dbias && strips > 1) {
+    const Span w = {ws, strips * groups * N * 4};
+    if (overlaps(w, c) || overlaps(w, z) || overlaps(w, d) || overlaps(w, b) || overlaps(w, off))
+      return SGEMM_ERR_INVALID_ARG;
+  }
+  const int64_t wgs = a.blocks_n * strips * groups, sums = cdiv(N, 64) * groups;
+  if (!grid_fits(wgs, 64 * sg::kActWaves) || !grid_fits(sums, 256)) return SGEMM_ERR_UNSUPPORTED;
+  void* kargs[] = {&a};
+  const void* fn = Z ? reinterpret_cast<const void*>(sg::act_backward_kernel<true>)
+                     : reinterpret_cast<const void*>(sg::act_backward_kernel<false>);
+  hipError_t e = hipLaunchKernel(fn, dim3((unsigned)wgs), dim3(64 * sg::kActWaves), kargs, 0,
+                                 stream);
+  if (e == hipSuccess && dbias && strips > 1)
+    e = hipLaunchKernel(reinterpret_cast<const void*>(sg::column_sum_kernel),
+                        dim3((unsigned)sums), dim3(256), kargs, 0, stream);
+  return e == hipSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH;
+}
+
+}  // namespace
+
+extern "C" {
+
+int sgemm_linear(int trans_a, int trans_b, int64_t M, int64_t N, int64_t K, const float* A,
+                 int64_t lda, const float* B, int64_t ldb, float* C, int64_t ldc,
+                 const sgemm_epilogue* epilogue, hipStream_t stream, void* workspace,
+                 int64_t workspace_bytes) {
+  Product p;
+  const int st = check_product(sg::kDense, trans_a, trans_b, M, N, K, 0, nullptr, 0, A, lda, B,
+                               ldb, 0, C, ldc, 0, epilogue, workspace, workspace_bytes, p);
+  if (st != SGEMM_OK || !p.launch) return st;
+  if (!lds_fit(p, lda, ldb, ldc, epilogue)) return SGEMM_ERR_UNSUPPORTED;
+  return run_product(p, stream);
+}
+
+int64_t sgemm_linear_workspace_bytes(int, int, int64_t, int64_t, int64_t) { return 0; }
+
+int sgemm_linear_plan_query(int trans_a, int trans_b, int64_t M, int64_t N, int64_t K,
+                            int64_t workspace_bytes, sgemm_plan* plan) {
+  if (plan == nullptr || workspace_bytes < 0 || M < 0 || N < 0 || K < 0 ||
+      ((trans_a | trans_b) & ~1))
+    return SGEMM_ERR_INVALID_ARG;
+  memset(plan, 0, sizeof(*plan));
+  plan->splits = 1;
+  return SGEMM_OK;
+}
+
+int sgemm_act_backward(int64_t M, int64_t N, const float* dC, int64_t lddc, const float* preact,
+                       int64_t ldp, int act, float* dZ, int64_t lddz, float* dbias,
+                       hipStream_t stream, void* workspace, int64_t workspace_bytes) {
+  return act_backward(M, N, 1, nullptr, false, dC, lddc, preact, ldp, act, dZ, lddz, dbias, 0,
+                      stream, workspace, workspace_bytes);
+}
+
+int64_t sgemm_act_backward_workspace_bytes(int64_t M, int64_t N) {
+  return sgemm_grouped_act_backward_workspace_bytes(M, N, 1);
+}
+
+int sgemm_grouped(int trans_b, int64_t M, int64_t N, int64_t K, int64_t groups,
+                  const int32_t* offsets, const float* A, int64_t lda, const float* B,
+                  int64_t ldb, int64_t stride_b, float* C, int64_t ldc,
+                  const sgemm_epilogue* epilogue, hipStream_t stream, void* workspace,
+                  int64_t workspace_bytes) {
+  Product p;
+  const int st = check_product(sg::kRowGroups, 0, trans_b, M, N, K, groups, offsets, M, A, lda, B,
+                               ldb, stride_b, C, ldc, 0, epilogue, workspace, workspace_bytes, p);
+  if (st != SGEMM_OK || !p.launch) return st;
+  if (!lds_fit(p, lda, ldb, ldc, epilogue)) return SGEMM_ERR_UNSUPPORTED;
+  return run_product(p, stream);
+}
+
+int64_t sgemm_grouped_workspace_bytes(int, int64_t, int64_t, int64_t, int64_t) { return 0; }
+
+// dB_g of K x N is a product of K x rows (A transposed) and rows x N; its
+// transpose one of N x rows and rows x K.
+int sgemm_grouped_wgrad(int trans_b, int64_t M, int64_t N, int64_t K, int64_t groups,
+                        const int32_t* offsets, const float* A, int64_t lda, const float* dZ,
+                        int64_t lddz, float* dB, int64_t lddb, int64_t stride_db,
+                        hipStream_t stream, void* workspace, int64_t workspace_bytes) {
+  if (trans_b & ~1) return SGEMM_ERR_INVALID_ARG;
+  Product p;
+  const int st = check_product(sg::kSumGroups, 1, 0, trans_b ? N : K, trans_b ? K : N, M, groups,
+                               offsets, M, trans_b ? dZ : A, trans_b ? lddz : lda,
+                               trans_b ? A : dZ, trans_b ? lda : lddz, 0, dB, lddb, stride_db,
+                               nullptr, workspace, workspace_bytes, p);
+  if (st != SGEMM_OK || !p.launch) return st;
+  if (!lds_fit(p, lda, lddz, lddb, nullptr)) return SGEMM_ERR_UNSUPPORTED;
+  return run_product(p, stream);
+}
+
+int64_t sgemm_grouped_wgrad_workspace_bytes(int, int64_t, int64_t, int64_t, int64_t) { return 0; }
+
+int sgemm_grouped_act_backward(int64_t M, int64_t N, int64_t groups, const int32_t* offsets,
+                               const float* dC, int64_t lddc, const float* preact, int64_t ldp,
+                               int act, float* dZ, int64_t lddz, float* dbias, int64_t lddbias,
+                               hipStream_t stream, void* workspace, int64_t workspace_bytes) {
+  return act_backward(M, N, groups, offsets, true, dC, lddc, preact, ldp, act, dZ, lddz, dbias,
+                      lddbias, stream, workspace, workspace_bytes);
+}
+
+int64_t sgemm_grouped_act_backward_workspace_bytes(int64_t M, int64_t N, int64_t groups) {
+  if (M <= 0 || N <= 0 || groups <= 0 || M > kMaxDim || N > kMaxDim || groups > sg::kMaxGroups)
+    return 0;
+  const int64_t s = act_strips(M, N, groups, INT64_MAX);
+  return s > 1 ? s * groups * N * 4 : 0;
+}
+
+}  // extern "C"

@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "../../include/sgemm.h"
+#include "host.hpp"
 #include "kernel_fma.hpp"
 #include "kernel_ladder.hpp"
 #include "kernel_mfma.hpp"
@@ -19,13 +20,8 @@
 namespace {
 
 using sg::GemmArgs;
+using namespace sg::host;
 
-// The kernels address each operand from the corner of their own tile with
-// 32-bit byte offsets below 2^31 (kOob = 2^31 marks an element outside the
-// matrix), so what is bounded is one tile's span, not an operand's size.
-constexpr int64_t kMaxSpanBytes = sg::kRsrcMax;
-// Tile origins and sizes are 32-bit ints in the kernels.
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1024;
 // The split partials are addressed as one resource from their first byte.
 constexpr int64_t kMaxWorkspaceBytes = sg::kRsrcMax;
 
@@ -33,21 +29,6 @@ struct Checked {
   int64_t a_bytes = 0, b_bytes = 0, c_bytes = 0;
   bool launch = false;  // false: M == 0 or N == 0, nothing to do
 };
-
-// Bytes spanned by a rows x cols row-major operand with leading dimension ld
-// (0 when empty); -1 when the span does not fit in int64.
-int64_t span_bytes(int64_t rows, int64_t cols, int64_t ld) {
-  if (rows == 0 || cols == 0) return 0;
-  const int64_t lim = INT64_MAX / 4;
-  if (rows - 1 > (lim - cols) / ld) return -1;
-  return ((rows - 1) * ld + cols) * 4;
-}
-
-bool overlaps(const void* p, int64_t pb, const void* q, int64_t qb) {
-  if (pb == 0 || qb == 0) return false;
-  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-  return a < b + (uintptr_t)qb && b < a + (uintptr_t)pb;
-}
 
 int check(int64_t M, int64_t N, int64_t K, const float* A, int64_t lda,
           const float* B, int64_t ldb, const float* C, int64_t ldc, int algo,
@@ -78,20 +59,6 @@ int check(int64_t M, int64_t N, int64_t K, const float* A, int64_t lda,
   return SGEMM_OK;
 }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-// True when rows x width floats with leading dimension ld (the first row
-// starting at offset 0) end below kMaxSpanBytes: ((rows - 1) ld + width) 4
-// bytes, formed without overflow.
-bool span_fits(int64_t rows, int64_t width, int64_t ld) {
-  if (rows <= 0 || width <= 0) return true;
-  const int64_t lim = kMaxSpanBytes / 4;  // floats
-  if (width >= lim) return false;
-  if (rows == 1) return true;
-  if (ld > (lim - 1 - width) / (rows - 1)) return false;
-  return (rows - 1) * ld + width < lim;
-}
-
 // Whether a kernel with BM x BN tiles and BK-deep slabs can address this
 // product: one tile's rows of A (all K columns, or BK if more) and of C, and
 // one slab's rows of B (BN columns past the tile's first), each within
@@ -102,11 +69,6 @@ bool tile_fits(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb,
   if (K > 0 && !span_fits(M < bm ? M : bm, K > bk ? K : bk, lda)) return false;
   if (K > 0 && !span_fits(K < bk ? K : bk, bn, ldb)) return false;
   return span_fits(M < bm ? M : bm, bn, ldc);
-}
-
-// The grid's work-items, workgroups x threads, must fit in 32 bits.
-bool grid_fits(int64_t workgroups, int threads) {
-  return workgroups >= 0 && workgroups < ((int64_t(1) << 32) / threads);
 }
 
 typedef void (*KernelFn)(GemmArgs);
@@ -196,42 +158,9 @@ const Candidate* mfma_candidates(bool direct, int& n) {
   return direct ? lds : reg;
 }
 
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-constexpr int kCUs = 256;                      // MI355X compute units
-constexpr double kPeakPerCU = 157.3e12 / kCUs;  // FP32 matrix flop/s per CU
-constexpr double kSaturate = 1.28;   // waves per SIMD that keep the pipes busy
-constexpr double kSlabFloor = 0.61e-6;  // s: a slab's wait for its loads
-constexpr double kRoundCost = 4.4e-6;   // s: fill and drain of one round
-constexpr double kWriteBW = 4.52e12;    // B/s: C stores of a final round
-
-// Estimated seconds of variant c on an M x N x K product.  Workgroups are
-// spread evenly over the CUs, so the busiest CU computes n = ceil(tiles /
-// CUs) tiles (charging partial-tile padding and the idle CUs of the last
-// round, i.e. wave quantisation), in rounds of up to occ resident ones.  In a
-// round of r tiles every slab takes the longer of its compute (r tiles'
-// flops at eff of the CU's peak, in proportion below kSaturate waves per
-// SIMD) and the latency of its loads; each round adds a fixed cost; and the
-// C tiles of the final round, which all CUs store at once, are charged at
-// the chip's write bandwidth.
 double estimate_grid(const Candidate& c, int64_t tiles, int64_t K) {
-  const Variant& v = c.v;
-  const int64_t n = cdiv(tiles, kCUs);
-  const int64_t slabs = K > v.tile_k ? cdiv(K, v.tile_k) : 1;
-  const double waves = v.threads / 64.0;
-  const double slab_flops = 2.0 * v.tile_m * v.tile_n * v.tile_k;
-  auto round = [&](int64_t r) {
-    const double simd = r * waves / 4.0;
-    const double busy = simd >= kSaturate ? 1.0 : simd / kSaturate;
-    const double compute = r * slab_flops / (kPeakPerCU * c.eff * busy);
-    return (double)slabs * (compute > kSlabFloor ? compute : kSlabFloor) + kRoundCost;
-  };
-  const int64_t full = n / c.occ, rest = n % c.occ;
-  double t = (double)full * round(c.occ) + (rest > 0 ? round(rest) : 0.0);
-  const int64_t last = rest > 0 ? rest : c.occ;
-  const int64_t cus = tiles < kCUs ? tiles : kCUs;
-  t += (double)last * cus * v.tile_m * v.tile_n * 4.0 / kWriteBW;
-  return t;
+  const TileCost cost = {c.v.tile_m, c.v.tile_n, c.v.tile_k, c.v.threads, c.eff, c.occ};
+  return estimate_grid(cost, tiles, K);
 }
 
 double estimate(const Candidate& c, int64_t M, int64_t N, int64_t K) {

@@ -10,7 +10,8 @@
 #include "../../include/sgemm_moe.h"
 #include "host.hpp"
 #include "kernel_act_backward.hpp"
-#include "kernel_linear_simple.hpp"
+#include "kernel_product_reduce.hpp"
+#include "product_variants.hpp"
 
 namespace {
 
@@ -18,7 +19,7 @@ using namespace sg::host;
 using sg::ActBackwardArgs;
 using sg::ProductArgs;
 
-typedef void (*ProductFn)(ProductArgs);
+using sg::ProductVariant;
 
 struct Span {
   const void* p;
@@ -91,9 +92,6 @@ int check_product(int mode, int ta, int tb, int64_t M, int64_t N, int64_t K, int
   p.pre = {ep->preact, ep->preact ? span_bytes(M, N, ep->ldp) : 0};
   p.bias = {ep->bias, !ep->bias ? 0 : mode == sg::kRowGroups
                                           ? groups_bytes(groups, ep->ldbias, N * 4) : N * 4};
-  p.g.a_bytes = p.a.bytes;
-  p.g.b_bytes = p.b.bytes;
-  p.g.c_bytes = p.c.bytes;
   if (mode == sg::kRowGroups) {
     if (p.b.bytes > 0 && groups > 1 && stride_b < p.b.bytes / 4) return SGEMM_ERR_INVALID_ARG;
     p.b.bytes = groups_bytes(groups, stride_b, p.b.bytes);
@@ -144,15 +142,6 @@ int check_product(int mode, int ta, int tb, int64_t M, int64_t N, int64_t K, int
   return SGEMM_OK;
 }
 
-int launch_product(ProductFn fn, const ProductArgs& g, int64_t workgroups, int threads,
-                   hipStream_t stream) {
-  ProductArgs args = g;
-  void* kargs[] = {&args};
-  const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(fn),
-                                       dim3((unsigned)workgroups), dim3(threads), kargs, 0, stream);
-  return e == hipSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH;
-}
-
 // Leading dimensions are ints in the kernels.
 bool lds_fit(const Product& p, int64_t lda, int64_t ldb, int64_t ldc, const sgemm_epilogue* ep) {
   const int64_t lim = int64_t(1) << 29;
@@ -160,19 +149,159 @@ bool lds_fit(const Product& p, int64_t lda, int64_t ldb, int64_t ldc, const sgem
          (!ep || !ep->residual || ep->ldr < lim) && (!ep || !ep->preact || ep->ldp < lim);
 }
 
-int run_product(Product& p, hipStream_t stream) {
+const ProductVariant* variants(bool trans_a, bool trans_b) {
+  if (trans_a) return trans_b ? sg::product_variants_sf() : sg::product_variants_ss();
+  return trans_b ? sg::product_variants_ff() : sg::product_variants_fs();
+}
+
+// Whether a variant's 32-bit offsets reach its tile's part of every operand:
+// with k running along the rows all of k, with k from row to row one slab.
+bool variant_fits(const Product& p, const ProductVariant& v) {
+  const ProductArgs& g = p.g;
+  const sg::host::TileCost& c = v.cost;
+  const int64_t K = g.mode == sg::kSumGroups ? c.tile_k : g.K;
+  auto fits = [&](bool k_fast, int64_t extent, int tile, int64_t ld) {
+    if (K == 0) return true;
+    return k_fast ? span_fits(extent < tile ? extent : tile, K > c.tile_k ? K : c.tile_k, ld)
+                  : span_fits(K < c.tile_k ? K : c.tile_k, tile, ld);
+  };
+  const int64_t rows = g.M < c.tile_m ? g.M : c.tile_m;
+  return fits(!p.trans_a, g.M, c.tile_m, g.lda) && fits(p.trans_b, g.N, c.tile_n, g.ldb) &&
+         span_fits(rows, c.tile_n, g.ldc) &&
+         (!g.residual || span_fits(rows, c.tile_n, g.ldr)) &&
+         (!g.preact || span_fits(rows, c.tile_n, g.ldp)) && span_fits(rows, c.tile_n, g.N);
+}
+
+struct Choice {
+  const ProductVariant* v;
+  int splits, k_split;
+  int64_t workgroups;   // of the grid
+};
+
+// Groups that can have rows.
+int64_t live_groups(const ProductArgs& g) { return g.groups < g.M ? g.groups : g.M; }
+
+// Workgroups of one split: exactly the tiles, except over row groups, whose
+// tiles only the device can count; this is the most there can be.
+int64_t grid_tiles(const ProductArgs& g, const sg::host::TileCost& c) {
+  const int64_t tn = cdiv(g.N, c.tile_n);
+  if (g.mode == sg::kRowGroups) {
+    const int64_t live = live_groups(g);
+    return ((g.M - live) / c.tile_m + live) * tn;
+  }
+  return cdiv(g.M, c.tile_m) * tn * g.groups;
+}
+
+// Tiles with work, row groups taken as equal.
+int64_t likely_tiles(const ProductArgs& g, const sg::host::TileCost& c) {
+  if (g.mode != sg::kRowGroups) return grid_tiles(g, c);
+  const int64_t live = live_groups(g);
+  return live * cdiv(cdiv(g.M, live), c.tile_m) * cdiv(g.N, c.tile_n);
+}
+
+// The variant, and the split of K, with the least estimated time (the model
+// of host.hpp; the costs of a split are those sgemm_ws was fitted with).  A
+// null v: no variant can address this product.
+Choice choose(const Product& p, int64_t ws_bytes) {
+  const ProductArgs& g = p.g;
+  const ProductVariant* table = variants(p.trans_a, p.trans_b);
+  // kSumGroups: the sum's length, groups taken as equal.
+  const int64_t K = g.mode == sg::kSumGroups ? cdiv(g.rows, at_least_one(g.groups)) : g.K;
+  const int64_t out = (int64_t)g.M * g.N * (g.mode == sg::kSumGroups ? g.groups : 1);
+  Choice one = {nullptr, 1, 0, 0}, split = one;
+  double t_one = 0, t_split = 0;
+  static const int kSplits[] = {2, 3, 4, 6, 8, 12, 16, 24, 32};
+  for (int i = 0; i < sg::kProductVariants; ++i) {
+    const ProductVariant& v = table[i];
+    const sg::host::TileCost& c = v.cost;
+    const int64_t grid = grid_tiles(g, c), likely = likely_tiles(g, c);
+    if (!variant_fits(p, v) || !grid_fits(grid, c.threads)) continue;
+    const double t = estimate_grid(c, likely, K);
+    if (one.v == nullptr || t < t_one * 0.995) {
+      one = {&v, 1, 0, grid};
+      t_one = t;
+    }
+    for (int S : kSplits) {
+      const int64_t ks = cdiv(cdiv(K, S), c.tile_k) * c.tile_k;
+      const int64_t se = g.mode == sg::kSumGroups ? S : cdiv(K, ks);
+      if (se < 2 || K < 2 * c.tile_k || se * out > ws_bytes / 4 ||
+          !grid_fits(grid * se, c.threads) ||
+          !grid_fits(out / g.N * cdiv(g.N, sg::kProductReduceCols), 64))
+        continue;
+      const double ts = 0.95 * estimate_grid(c, likely * se, ks) + 3.0e-6 +
+                        (double)(se + 1) * out * 4.0 / 5.0e12;
+      if (split.v == nullptr || ts < t_split) {
+        split = {&v, (int)se, (int)ks, grid * se};
+        t_split = ts;
+      }
+    }
+  }
+  return split.v != nullptr && t_split < t_one * 0.97 ? split : one;
+}
+
+int64_t split_bytes(const ProductArgs& g, const Choice& ch) {
+  if (ch.v == nullptr || ch.splits == 1) return 0;
+  return (int64_t)ch.splits * g.M * g.N * (g.mode == sg::kSumGroups ? g.groups : 1) * 4;
+}
+
+int run_product(Product& p, const int32_t* offsets, hipStream_t stream, void* ws,
+                int64_t ws_bytes) {
   ProductArgs& g = p.g;
-  g.tiles_n = (int)cdiv(g.N, 16);
-  g.tiles_m = (int)cdiv(g.M, 16);
-  const int64_t rows = g.mode == sg::kRowGroups
-                           ? g.tiles_m + (g.groups < g.M ? g.groups : g.M)
-                           : (int64_t)g.tiles_m * g.groups;
-  const int64_t wgs = rows * g.tiles_n;
-  if (!grid_fits(wgs, 256)) return SGEMM_ERR_UNSUPPORTED;
-  static const ProductFn table[4] = {
-      sg::product_simple_kernel<false, false>, sg::product_simple_kernel<false, true>,
-      sg::product_simple_kernel<true, false>, sg::product_simple_kernel<true, true>};
-  return launch_product(table[(p.trans_a ? 2 : 0) | (p.trans_b ? 1 : 0)], g, wgs, 256, stream);
+  const Choice ch = choose(p, ws_bytes);
+  if (ch.v == nullptr) return SGEMM_ERR_UNSUPPORTED;
+  const sg::host::TileCost& c = ch.v->cost;
+  g.tiles_m = (int)cdiv(g.M, c.tile_m);
+  g.tiles_n = (int)cdiv(g.N, c.tile_n);
+  g.group_m = g.tiles_m < 8 ? g.tiles_m : 8;
+  g.splits = ch.splits;
+  g.k_split = ch.k_split;
+  if (ch.splits > 1) {
+    g.W = static_cast<float*>(ws);
+    const Span w = {ws, split_bytes(g, ch)};
+    const Span off = {offsets, offsets ? (int64_t)(g.groups + 1) * 4 : 0};
+    if (overlaps(w, p.a) || overlaps(w, p.b) || overlaps(w, p.c) || overlaps(w, p.bias) ||
+        overlaps(w, p.res) || overlaps(w, p.pre) || overlaps(w, off))
+      return SGEMM_ERR_INVALID_ARG;
+  }
+  void* kargs[] = {&g};
+  hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(ch.v->fn),
+                                 dim3((unsigned)ch.workgroups), dim3(c.threads), kargs, 0, stream);
+  if (e == hipSuccess && ch.splits > 1) {
+    const int64_t rows = (int64_t)g.M * (g.mode == sg::kSumGroups ? g.groups : 1);
+    e = hipLaunchKernel(reinterpret_cast<const void*>(sg::product_reduce_kernel),
+                        dim3((unsigned)(rows * cdiv(g.N, sg::kProductReduceCols))), dim3(64),
+                        kargs, 0, stream);
+  }
+  return e == hipSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH;
+}
+
+// A product with no operands, for the questions about plans.
+Product shape_only(int mode, bool ta, bool tb, int64_t M, int64_t N, int64_t K, int64_t groups,
+                   int64_t rows) {
+  Product p;
+  memset(&p, 0, sizeof(p));
+  p.trans_a = ta;
+  p.trans_b = tb;
+  p.launch = M > 0 && N > 0 && groups > 0;
+  p.g.M = (int)M;
+  p.g.N = (int)N;
+  p.g.K = (int)K;
+  p.g.lda = (int)at_least_one(ta ? M : K);
+  p.g.ldb = (int)at_least_one(tb ? K : N);
+  p.g.ldc = (int)N;
+  p.g.mode = mode;
+  p.g.groups = (int)groups;
+  p.g.rows = (int)rows;
+  return p;
+}
+
+bool sizes_ok(int64_t a, int64_t b, int64_t c) {
+  return a >= 0 && b >= 0 && c >= 0 && a <= kMaxDim && b <= kMaxDim && c <= kMaxDim;
+}
+
+int64_t plan_workspace(const Product& p) {
+  if (!p.launch) return 0;
+  return split_bytes(p.g, choose(p, INT64_MAX));
 }
 
 // Strips of rows per group: enough workgroups for the chip, strips of 16 rows
@@ -266,18 +395,40 @@ int sgemm_linear(int trans_a, int trans_b, int64_t M, int64_t N, int64_t K, cons
                                ldb, 0, C, ldc, 0, epilogue, workspace, workspace_bytes, p);
   if (st != SGEMM_OK || !p.launch) return st;
   if (!lds_fit(p, lda, ldb, ldc, epilogue)) return SGEMM_ERR_UNSUPPORTED;
-  return run_product(p, stream);
+  return run_product(p, p.g.offsets, stream, workspace, workspace_bytes);
 }
 
-int64_t sgemm_linear_workspace_bytes(int, int, int64_t, int64_t, int64_t) { return 0; }
+int64_t sgemm_linear_workspace_bytes(int trans_a, int trans_b, int64_t M, int64_t N, int64_t K) {
+  if (!sizes_ok(M, N, K) || ((trans_a | trans_b) & ~1)) return 0;
+  return plan_workspace(shape_only(sg::kDense, trans_a, trans_b, M, N, K, 1, 0));
+}
 
 int sgemm_linear_plan_query(int trans_a, int trans_b, int64_t M, int64_t N, int64_t K,
                             int64_t workspace_bytes, sgemm_plan* plan) {
   if (plan == nullptr || workspace_bytes < 0 || M < 0 || N < 0 || K < 0 ||
       ((trans_a | trans_b) & ~1))
     return SGEMM_ERR_INVALID_ARG;
+  if (!sizes_ok(M, N, K)) return SGEMM_ERR_UNSUPPORTED;
   memset(plan, 0, sizeof(*plan));
   plan->splits = 1;
+  const Product p = shape_only(sg::kDense, trans_a, trans_b, M, N, K, 1, 0);
+  if (!p.launch) return SGEMM_OK;
+  const Choice ch = choose(p, workspace_bytes);
+  if (ch.v == nullptr) return SGEMM_ERR_UNSUPPORTED;
+  const sg::host::TileCost& c = ch.v->cost;
+  plan->algo = SGEMM_ALGO_MFMA_DIRECT;
+  plan->tile_m = c.tile_m;
+  plan->tile_n = c.tile_n;
+  plan->tile_k = c.tile_k;
+  plan->threads = c.threads;
+  plan->vec_a = plan->vec_b = 1;
+  plan->workgroups = ch.workgroups;
+  plan->lds_bytes = ch.v->lds_bytes;
+  plan->wg_per_cu = c.occ;
+  plan->splits = ch.splits;
+  plan->workspace_bytes = split_bytes(p.g, ch);
+  snprintf(plan->kernel, sizeof(plan->kernel), "product_%c%c_%s", trans_a ? 's' : 'f',
+           trans_b ? 'f' : 's', ch.v->name);
   return SGEMM_OK;
 }
 
@@ -302,10 +453,14 @@ int sgemm_grouped(int trans_b, int64_t M, int64_t N, int64_t K, int64_t groups,
                                ldb, stride_b, C, ldc, 0, epilogue, workspace, workspace_bytes, p);
   if (st != SGEMM_OK || !p.launch) return st;
   if (!lds_fit(p, lda, ldb, ldc, epilogue)) return SGEMM_ERR_UNSUPPORTED;
-  return run_product(p, stream);
+  return run_product(p, p.g.offsets, stream, workspace, workspace_bytes);
 }
 
-int64_t sgemm_grouped_workspace_bytes(int, int64_t, int64_t, int64_t, int64_t) { return 0; }
+int64_t sgemm_grouped_workspace_bytes(int trans_b, int64_t M, int64_t N, int64_t K,
+                                      int64_t groups) {
+  if (!sizes_ok(M, N, K) || groups < 0 || groups > sg::kMaxGroups || (trans_b & ~1)) return 0;
+  return plan_workspace(shape_only(sg::kRowGroups, false, trans_b, M, N, K, groups, M));
+}
 
 // dB_g of K x N is a product of K x rows (A transposed) and rows x N; its
 // transpose one of N x rows and rows x K.
@@ -321,10 +476,15 @@ int sgemm_grouped_wgrad(int trans_b, int64_t M, int64_t N, int64_t K, int64_t gr
                                nullptr, workspace, workspace_bytes, p);
   if (st != SGEMM_OK || !p.launch) return st;
   if (!lds_fit(p, lda, lddz, lddb, nullptr)) return SGEMM_ERR_UNSUPPORTED;
-  return run_product(p, stream);
+  return run_product(p, p.g.offsets, stream, workspace, workspace_bytes);
 }
 
-int64_t sgemm_grouped_wgrad_workspace_bytes(int, int64_t, int64_t, int64_t, int64_t) { return 0; }
+int64_t sgemm_grouped_wgrad_workspace_bytes(int trans_b, int64_t M, int64_t N, int64_t K,
+                                            int64_t groups) {
+  if (!sizes_ok(M, N, K) || groups < 0 || groups > sg::kMaxGroups || (trans_b & ~1)) return 0;
+  return plan_workspace(shape_only(sg::kSumGroups, true, false, trans_b ? N : K, trans_b ? K : N,
+                                   M, groups, M));
+}
 
 int sgemm_grouped_act_backward(int64_t M, int64_t N, int64_t groups, const int32_t* offsets,
                                const float* dC, int64_t lddc, const float* preact, int64_t ldp,

@@ -18,7 +18,6 @@ struct ProductArgs {
   const float* A;
   const float* B;
   float* C;
-  int64_t a_bytes, b_bytes, c_bytes;   // spans (b, c: of one group's matrix)
   int M, N, K;                         // kSumGroups: K is unused
   int lda, ldb, ldc;
   // Epilogue.

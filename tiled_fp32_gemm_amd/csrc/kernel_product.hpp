@@ -341,18 +341,21 @@ product_kernel(ProductArgs g) {
             stage + 4 * ((r >> 4) * (16 * CPR) + (r & 15) + 16 * (4 * sub + 2 * lh + h)));
       }
     } else {
+      // One lane offset (two for R = 32, whose xor moves to the neighbouring
+      // row), so that the k steps are immediates of the reads.
+      const int col = T == 2 ? w0 + 2 * li : w0 + li;
+      const int q = R >= 64 ? (col >> 2) ^ (lh ? 8 : 0) : col >> 2;
+      const float* const p = stage + 4 * (8 * lh * (R / 4) + q) + (col & 3);
+      const int flip = R >= 64 ? 0 : lh * R;
 #pragma unroll
       for (int pp = 0; pp < 4; ++pp) {
-        const int k = 16 * sub + 8 * lh + 4 * h + pp;
-        auto at = [&](int col) {
-          return 4 * ((k * (R / 4) + (col >> 2)) ^ (lh ? 8 : 0)) + (col & 3);
-        };
+        const float* const at = p + (16 * sub + 4 * h + pp) * R + (pp & 1 ? -flip : flip);
         if (T == 2) {
-          const f32x2 v = *reinterpret_cast<const f32x2*>(stage + at(w0 + 2 * li));
+          const f32x2 v = *reinterpret_cast<const f32x2*>(at);
           out[0][pp] = v[0];
           out[T - 1][pp] = v[1];
         } else {
-          out[0][pp] = stage[at(w0 + li)];
+          out[0][pp] = *at;
         }
       }
     }

@@ -9,7 +9,8 @@ automatically: ``linear_backward`` is a call of its own.
 from __future__ import annotations
 
 import ctypes
-from contextlib import contextmanager
+
+import torch
 
 import tiled_fp32_gemm_amd as sg
 
@@ -73,7 +74,9 @@ def sgemm_act_backward_workspace_bytes(M, N) -> int:
     return sg.load().sgemm_act_backward_workspace_bytes(M, N)
 
 
-# Checks and marshalling shared with the grouped products.
+# Checks and marshalling shared with the routing calls.  They run before every
+# launch and cost as much as a small kernel, so each tensor is asked once for
+# what is needed of it.
 
 def _act(activation) -> int:
     try:
@@ -83,60 +86,84 @@ def _act(activation) -> int:
                          f"got {activation!r}") from None
 
 
-def _float(t, name: str, device, shape=None):
-    """A float32 tensor on `device`, of `shape` where one is given."""
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
-        raise ValueError(f"{name} must be a float32 tensor")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}: got {tuple(t.shape)}")
+def _device(t, name: str) -> int:
+    """The index of the GPU an operand is on."""
+    try:
+        dev = t.get_device()
+    except AttributeError:
+        dev = -1
+    if dev < 0:
+        raise ValueError(f"{name} must be a tensor on a GPU")
+    return dev
+
+
+def _float(t, name: str, dev: int):
+    """A float32 tensor on GPU `dev`."""
+    try:
+        good = t.dtype is torch.float32 and t.get_device() == dev
+    except AttributeError:
+        good = False
+    if not good:
+        raise ValueError(f"{name} must be a float32 tensor on cuda:{dev}")
     return t
 
 
-def _gpu(t, name: str):
-    """The device of an operand that has to be on a GPU."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a tensor on a GPU")
-    return t.device
+def _matrix(t, name: str, dev: int) -> tuple[int, int, int]:
+    """Rows, columns and leading dimension of a row-major float32 matrix."""
+    _float(t, name, dev)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    r, c = t.shape
+    ld, unit = t.stride()
+    if unit != 1 and c > 1:
+        raise ValueError(f"{name} must have unit column stride (row-major)")
+    return r, c, ld if r > 1 else max(c, 1)
 
 
-def _unit(t, name: str) -> int:
-    """The address of a 1-D tensor with unit stride."""
-    if t.dim() != 1 or (t.numel() > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be 1-D with unit stride")
+def _sized(t, name: str, dev: int, rows: int, cols: int) -> int:
+    """The leading dimension of a rows x cols float32 matrix."""
+    r, c, ld = _matrix(t, name, dev)
+    if r != rows or c != cols:
+        raise ValueError(f"{name} must be {rows} x {cols}: got {r} x {c}")
+    return ld
+
+
+def _vector(t, name: str, dev: int, n: int) -> int:
+    """The address of n floats with unit stride."""
+    if _float(t, name, dev).shape != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be 1-D of {n} with unit stride")
     return t.data_ptr()
 
 
-def _workspace(workspace, device) -> tuple[int, int]:
-    import torch
+def _workspace(workspace, dev: int) -> tuple[int, int]:
     if workspace is None:
         return 0, 0
-    if (not isinstance(workspace, torch.Tensor) or workspace.device != device
-            or not workspace.is_contiguous()):
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    try:
+        good = workspace.get_device() == dev and workspace.is_contiguous()
+    except AttributeError:
+        good = False
+    if not good:
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
     n = workspace.numel() * workspace.element_size()
     return (workspace.data_ptr(), n) if n else (0, 0)
 
 
-@contextmanager
-def _on(device, stream):
-    """`device` current, and `stream` (default: the device's current one) the
-    stream that tensors made inside belong to; yields the stream's handle."""
-    import torch
+def _empty(dev: int, *shape, dtype=None):
+    return torch.empty(shape, dtype=dtype or torch.float32, device=dev)
+
+
+def _on(dev: int, stream, body):
+    """``body(handle)`` with GPU `dev` current and `stream` (default: its
+    current one) the stream that tensors made inside belong to."""
     if stream is None:
-        if torch.cuda.current_device() == device.index:
-            yield torch.cuda.current_stream().cuda_stream
-            return
-        with torch.cuda.device(device):
-            yield torch.cuda.current_stream().cuda_stream
-        return
-    if stream.device != device:
-        raise ValueError(f"stream must be of {device}")
-    with torch.cuda.device(device), torch.cuda.stream(stream):
-        yield stream.cuda_stream
+        if torch.cuda.current_device() == dev:
+            return body(torch._C._cuda_getCurrentRawStream(dev))
+        with torch.cuda.device(dev):
+            return body(torch._C._cuda_getCurrentRawStream(dev))
+    if stream.device.index != dev:
+        raise ValueError(f"stream must be of cuda:{dev}")
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        return body(stream.cuda_stream)
 
 
 def _check(status: int, what: str) -> None:
@@ -144,26 +171,26 @@ def _check(status: int, what: str) -> None:
         raise sg.SgemmError(status, what)
 
 
-def _op_shape(t, name: str, transposed: bool) -> tuple[int, int]:
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D")
-    r, c = t.shape
-    return (c, r) if transposed else (r, c)
-
-
-def _epilogue(act, bias, ld_bias, residual, preact):
+def _epilogue(act, bias, ld_bias, residual, ldr, preact, ldp):
     """``Epilogue`` of checked tensors, or None for an empty one."""
     if not act and bias is None and residual is None and preact is None:
         return None
-    e = Epilogue()
-    e.act = act
-    if bias is not None:
-        e.bias, e.ldbias = bias.data_ptr(), ld_bias
-    if residual is not None:
-        e.residual, e.ldr = residual.data_ptr(), sg._ld(residual, "residual")
-    if preact is not None:
-        e.preact, e.ldp = preact.data_ptr(), sg._ld(preact, "preact")
-    return e
+    return Epilogue(act, None if bias is None else bias.data_ptr(), ld_bias,
+                    None if residual is None else residual.data_ptr(), ldr,
+                    None if preact is None else preact.data_ptr(), ldp)
+
+
+def _inner(A, B, dev: int, transpose_a, transpose_b):
+    """M, N, K and the leading dimensions of op(A) and op(B)."""
+    M, K, lda = _matrix(A, "A", dev)
+    K2, N, ldb = _matrix(B, "B", dev)
+    if transpose_a:
+        M, K = K, M
+    if transpose_b:
+        K2, N = N, K2
+    if K2 != K:
+        raise ValueError(f"shape mismatch: op(A) is {M} x {K}, op(B) is {K2} x {N}")
+    return M, N, K, lda, ldb
 
 
 def linear(A, B, bias=None, activation="none", residual=None, *, transpose_a=False,
@@ -178,31 +205,25 @@ def linear(A, B, bias=None, activation="none", residual=None, *, transpose_a=Fal
     split, see ``sgemm_linear_workspace_bytes``.  Raises ``ValueError`` on bad
     tensors and ``SgemmError`` on a library error.
     """
-    import torch
     act = _act(activation)
-    dev = _gpu(A, "A")
-    M, K = _op_shape(_float(A, "A", dev), "A", transpose_a)
-    K2, N = _op_shape(_float(B, "B", dev), "B", transpose_b)
-    if K2 != K:
-        raise ValueError(f"shape mismatch: op(A) is {M} x {K}, op(B) is {K2} x {N}")
-    lda, ldb = sg._ld(A, "A"), sg._ld(B, "B")
+    dev = _device(A, "A")
+    M, N, K, lda, ldb = _inner(A, B, dev, transpose_a, transpose_b)
     if bias is not None:
-        _unit(_float(bias, "bias", dev, (N,)), "bias")
-    if residual is not None:
-        _float(residual, "residual", dev, (M, N))
-    if preact is not None:
-        _float(preact, "preact", dev, (M, N))
-    epilogue = _epilogue(act, bias, N, residual, preact)
+        _vector(bias, "bias", dev, N)
+    ldr = 1 if residual is None else _sized(residual, "residual", dev, M, N)
+    ldp = 1 if preact is None else _sized(preact, "preact", dev, M, N)
+    epilogue = _epilogue(act, bias, N, residual, ldr, preact, ldp)
     ws, ws_bytes = _workspace(workspace, dev)
-    if out is not None:
-        _float(out, "out", dev, (M, N))
-    with _on(dev, stream) as s:
-        if out is None:
-            out = torch.empty((M, N), dtype=torch.float32, device=dev)
-        st = sgemm_linear(transpose_a, transpose_b, M, N, K, A.data_ptr(), lda, B.data_ptr(),
-                          ldb, out.data_ptr(), sg._ld(out, "out"), epilogue, s, ws, ws_bytes)
-    _check(st, "sgemm_linear")
-    return out
+    ldc = max(N, 1) if out is None else _sized(out, "out", dev, M, N)
+
+    def call(s):
+        c = _empty(dev, M, N) if out is None else out
+        st = sg.load().sgemm_linear(bool(transpose_a), bool(transpose_b), M, N, K, A.data_ptr(),
+                                    lda, B.data_ptr(), ldb, c.data_ptr(), ldc, epilogue, s, ws,
+                                    ws_bytes)
+        _check(st, "sgemm_linear")
+        return c
+    return _on(dev, stream, call)
 
 
 def activation_backward(dC, activation="none", preact=None, *, bias_grad=True, out=None,
@@ -213,29 +234,28 @@ def activation_backward(dC, activation="none", preact=None, *, bias_grad=True, o
     ``out`` receives dZ and may be ``dC`` or ``preact``.  For activation
     "none" dZ is dC: unless ``out`` asks for a copy, dC itself is returned.
     """
-    import torch
     act = _act(activation)
-    dev = _gpu(dC, "dC")
-    M, N = _op_shape(_float(dC, "dC", dev), "dC", False)
-    lddc, z, ldz = sg._ld(dC, "dC"), 0, 1
+    dev = _device(dC, "dC")
+    M, N, lddc = _matrix(dC, "dC", dev)
+    z, ldz = 0, 1
     if act:
         if preact is None:
             raise ValueError(f"activation {activation!r} needs preact")
-        z, ldz = _float(preact, "preact", dev, (M, N)).data_ptr(), sg._ld(preact, "preact")
-    if out is not None:
-        _float(out, "out", dev, (M, N))
+        ldz = _sized(preact, "preact", dev, M, N)
+        z = preact.data_ptr()
+    lddz = max(N, 1) if out is None else _sized(out, "out", dev, M, N)
     ws, ws_bytes = _workspace(workspace, dev)
-    with _on(dev, stream) as s:
-        dz = out
-        if dz is None and act:
-            dz = torch.empty((M, N), dtype=torch.float32, device=dev)
-        dbias = torch.empty(N, dtype=torch.float32, device=dev) if bias_grad else None
-        st = sgemm_act_backward(M, N, dC.data_ptr(), lddc, z, ldz, act,
-                                0 if dz is None else dz.data_ptr(),
-                                1 if dz is None else sg._ld(dz, "out"),
-                                dbias.data_ptr() if bias_grad else 0, s, ws, ws_bytes)
-    _check(st, "sgemm_act_backward")
-    return (dC if dz is None else dz), dbias
+
+    def call(s):
+        dz = _empty(dev, M, N) if out is None and act else out
+        dbias = _empty(dev, N) if bias_grad else None
+        st = sg.load().sgemm_act_backward(M, N, dC.data_ptr(), lddc, z, ldz, act,
+                                          None if dz is None else dz.data_ptr(), lddz,
+                                          dbias.data_ptr() if bias_grad else None, s, ws,
+                                          ws_bytes)
+        _check(st, "sgemm_act_backward")
+        return (dC if dz is None else dz), dbias
+    return _on(dev, stream, call)
 
 
 def linear_backward(dC, A, B, activation="none", preact=None, *, transpose_a=False,
@@ -245,13 +265,11 @@ def linear_backward(dC, A, B, activation="none", preact=None, *, transpose_a=Fal
     ``bias_grad``.  ``preact`` is what ``linear`` stored (not needed for
     activation "none").  The residual's gradient is ``dC``.
     """
-    dev = _gpu(dC, "dC")
-    M, K = _op_shape(_float(A, "A", dev), "A", transpose_a)
-    K2, N = _op_shape(_float(B, "B", dev), "B", transpose_b)
-    if K2 != K:
-        raise ValueError(f"shape mismatch: op(A) is {M} x {K}, op(B) is {K2} x {N}")
-    _float(dC, "dC", dev, (M, N))
-    with _on(dev, stream):   # dZ, when it is made here, belongs to the stream
+    dev = _device(dC, "dC")
+    M, N, _, _, _ = _inner(A, B, dev, transpose_a, transpose_b)
+    _sized(dC, "dC", dev, M, N)
+
+    def call(_):   # dZ, when it is made here, belongs to the stream
         dZ, dbias = activation_backward(dC, activation, preact, bias_grad=bias_grad,
                                         workspace=workspace)
         if transpose_a:
@@ -262,4 +280,5 @@ def linear_backward(dC, A, B, activation="none", preact=None, *, transpose_a=Fal
             dB = linear(dZ, A, transpose_a=True, transpose_b=transpose_a, workspace=workspace)
         else:
             dB = linear(A, dZ, transpose_a=not transpose_a, workspace=workspace)
-    return dA, dB, dbias
+        return dA, dB, dbias
+    return _on(dev, stream, call)

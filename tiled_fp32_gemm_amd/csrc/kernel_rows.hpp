@@ -1,0 +1,233 @@
+// kernel_rows.hpp -- the epilogue products for a few rows (one token of a
+// decoder, or an expert's few tokens): op(B) is read once, straight into
+// registers, and multiplied with vector FMAs.
+//
+// Such a product is bound by reading B (2 R flop a float for R rows, where the
+// chip has 32 flop for each float of HBM bandwidth), so what counts is bytes in
+// flight: a workgroup of four waves takes a few columns and splits K over its
+// threads, each with several 16-byte groups in flight, and the partial sums
+// meet once at the end, first within the waves, then through LDS in wave order.
+// No second launch and no workspace.  A (R rows) comes from the caches.
+//
+//   rows_fast_kernel   B is N x K: a wave takes four columns (four rows of B),
+//                      its lanes 256 consecutive k at a time.  KW = 1: each of
+//                      the four waves has columns of its own and all of K.
+//                      KW = 4: they share the columns and take K by turns, for
+//                      N too small to fill the chip otherwise.
+//   rows_slow_kernel   B is K x N: LC lanes take 4 LC consecutive columns of
+//                      four consecutive k rows, the others further k.
+//
+// Measured on MI355X (kernel trace; B of 64 MiB, 4096 x 4096, from HBM, one row
+// with bias and SILU): fast 13.4 us = 5.0 TB/s (KW = 4: 16.2), slow 15.4 us at
+// 16 columns a workgroup (32: 17.6, 64: 29: too few workgroups); product_kernel
+// with its second launch takes 20.4 and 21.9 us.  2, 4 and 8 rows cost 13 to
+// 16 us.
+//
+// Both take rows in chunks of R (more rows than R are further workgroups), of
+// one product or of groups, and A stored M x K.
+#pragma once
+
+#include "kernel_product.hpp"
+
+namespace sg {
+
+constexpr int kRowsThreads = 256;
+
+// Sums v[0 .. N-1] over the lanes of a wave that differ in bits D, D/2, ..,
+// LAST: halves are exchanged while there are several values, so that a lane
+// ends with N / (lanes summed) of them, v[0] on, or one.  Returns the number of
+// the first.
+template <int D, int LAST, int N, int V>
+__device__ __forceinline__ int spread_sum(float (&v)[V], int lane) {
+  if constexpr (D < LAST) {
+    return 0;
+  } else if constexpr (N > 1) {
+    const bool up = (lane & D) != 0;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const float give = up ? v[i] : v[i + N / 2];
+      const float keep = up ? v[i + N / 2] : v[i];
+      v[i] = keep + __shfl_xor(give, D);
+    }
+    return (up ? N / 2 : 0) + spread_sum<D / 2, LAST, N / 2, V>(v, lane);
+  } else {
+    v[0] += __shfl_xor(v[0], D);
+    return spread_sum<D / 2, LAST, 1, V>(v, lane);
+  }
+}
+
+// The chunk of rows and the block of columns of this workgroup.
+struct RowsPlace {
+  int row0, rows, group, block;
+};
+
+template <int R>
+__device__ __forceinline__ bool rows_place(const ProductArgs& g, RowsPlace& p) {
+  if (g.mode == kRowGroups) {
+    RowTile t;
+    if (!row_group_tile<R>(g, (int)threadIdx.x & 63, t)) return false;
+    p.group = __builtin_amdgcn_readfirstlane(t.group);
+    p.row0 = __builtin_amdgcn_readfirstlane(t.first + t.tm * R);
+    p.rows = min(R, __builtin_amdgcn_readfirstlane(t.end) - p.row0);
+    p.block = __builtin_amdgcn_readfirstlane(t.tn);
+    return true;
+  }
+  int tm, tn;
+  tile_order(xcd_order((int)blockIdx.x, (int)gridDim.x), g.tiles_m, g.tiles_n, g.group_m, tm, tn);
+  p.group = 0;
+  p.row0 = tm * R;
+  p.rows = min(R, g.M - p.row0);
+  p.block = tn;
+  return true;
+}
+
+__device__ __forceinline__ void finish_one(const ProductArgs& g, const RowsPlace& p, int r, int col,
+                                           float z) {
+  const int64_t row = p.row0 + r;
+  if (g.bias) z += g.bias[p.group * g.ld_bias + col];
+  if (g.preact) g.preact[row * g.ldp + col] = z;
+  z = activate(g.act, z);
+  if (g.residual) z += g.residual[row * g.ldr + col];
+  g.C[row * g.ldc + col] = z;
+}
+
+template <int R, int NC, int KW>
+__global__ void __launch_bounds__(kRowsThreads) rows_fast_kernel(ProductArgs g) {
+  constexpr int V = R * NC;
+  constexpr int STEP = 256 * KW;            // k taken at a time
+  constexpr int U = V >= 16 ? 1 : 2;        // of these in flight
+  __shared__ float part[4][V];
+  const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+  RowsPlace p;
+  if (!rows_place<R>(g, p)) return;
+  // Waves that split k share their columns.
+  const int n0 = (p.block * (4 / KW) + (KW == 4 ? 0 : wave)) * NC;
+  const float* a[R];
+  const float* b[NC];
+  // Rows and columns past the end repeat the last one; their sums are dropped.
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    a[r] = g.A + (int64_t)(p.row0 + min(r, p.rows - 1)) * g.lda;
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+    b[c] = (g.mode == kRowGroups ? g.B + p.group * g.stride_b : g.B) +
+           (int64_t)min(n0 + c, g.N - 1) * g.ldb;
+  float acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+  auto take = [&](const f32x4 (&av)[R], const f32x4 (&bv)[NC]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          acc[r * NC + c] = fmaf(av[r][e], bv[c][e], acc[r * NC + c]);
+  };
+  int k = 4 * (KW == 4 ? (int)threadIdx.x : lane);
+  for (; k + (U - 1) * STEP + 4 <= g.K; k += U * STEP) {
+    f32x4 av[U][R], bv[U][NC];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        bv[u][c] = *reinterpret_cast<const f32x4u*>(b[c] + k + u * STEP);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        av[u][r] = *reinterpret_cast<const f32x4u*>(a[r] + k + u * STEP);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) take(av[u], bv[u]);
+  }
+  for (; k < g.K; k += STEP) {
+    f32x4 av[R], bv[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) bv[c] = load_upto(b[c] + k, g.K - k);
+#pragma unroll
+    for (int r = 0; r < R; ++r) av[r] = load_upto(a[r] + k, g.K - k);
+    take(av, bv);
+  }
+  const int which = spread_sum<32, 1, V, V>(acc, lane);
+  // Lanes that share a value hold it alike.
+  if ((lane & (64 / V - 1)) == 0) part[wave][which] = acc[0];
+  __syncthreads();
+  const int i = KW == 4 ? (int)threadIdx.x : lane;
+  if (i >= V) return;
+  const int r = i / NC, col = n0 + i % NC;
+  if (r < p.rows && col < g.N)
+    finish_one(g, p, r, col,
+               KW == 4 ? ((part[0][i] + part[1][i]) + part[2][i]) + part[3][i] : part[wave][i]);
+}
+
+template <int R, int LC>
+__global__ void __launch_bounds__(kRowsThreads) rows_slow_kernel(ProductArgs g) {
+  constexpr int V = 4 * R;
+  constexpr int KR = kRowsThreads / LC;   // groups of four k rows at a time
+  constexpr int SHARE = 64 / LC;          // of them in a wave
+  constexpr int LEFT = V > SHARE ? V / SHARE : 1;   // values a lane ends with
+  __shared__ float part[4][V * LC];
+  const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  RowsPlace p;
+  if (!rows_place<R>(g, p)) return;
+  const int cg = tid % LC;
+  const int n0 = p.block * 4 * LC;
+  const int col = n0 + 4 * cg, left = g.N - col;
+  const float* a[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    a[r] = g.A + (int64_t)(p.row0 + min(r, p.rows - 1)) * g.lda;
+  const float* const b = (g.mode == kRowGroups ? g.B + p.group * g.stride_b : g.B) + col;
+  float acc[V];   // [row][column]
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+  auto sweep = [&](auto whole) {
+    constexpr bool kWhole = decltype(whole)::value;
+    auto load = [&](int k) {
+      return kWhole ? f32x4(*reinterpret_cast<const f32x4u*>(b + (int64_t)k * g.ldb))
+                    : load_upto(b + (int64_t)k * g.ldb, left);
+    };
+    constexpr int kTwice = R == 8 ? 1 : 2;   // groups of rows in flight
+    int k = 4 * (tid / LC);
+#pragma unroll kTwice
+    for (; k + 4 <= g.K; k += 4 * KR) {
+      f32x4 av[R], bv[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) bv[e] = load(k + e);
+#pragma unroll
+      for (int r = 0; r < R; ++r) av[r] = *reinterpret_cast<const f32x4u*>(a[r] + k);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            acc[r * 4 + c] = fmaf(av[r][e], bv[e][c], acc[r * 4 + c]);
+    }
+    for (; k < g.K; ++k) {   // the last, partial group of four: one thread's
+      const f32x4 bv = load(k);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[r * 4 + c] = fmaf(a[r][k], bv[c], acc[r * 4 + c]);
+    }
+  };
+  if (left >= 4) sweep(std::true_type());
+  else if (left > 0) sweep(std::false_type());
+  // Over the wave's SHARE lanes of a column group.
+  const int first = spread_sum<32, LC, V, V>(acc, lane);
+  if (V >= SHARE || lane / LC % (SHARE / V > 0 ? SHARE / V : 1) == 0) {
+#pragma unroll
+    for (int i = 0; i < LEFT; ++i) part[wave][(first + i) * LC + cg] = acc[i];
+  }
+  __syncthreads();
+  for (int i = tid; i < V * LC; i += kRowsThreads) {
+    // Consecutive threads take consecutive columns of a row.
+    const int r = i / (4 * LC), c = i % (4 * LC);
+    const int at = (r * 4 + c % 4) * LC + c / 4;
+    if (r < p.rows && n0 + c < g.N) {
+      finish_one(g, p, r, n0 + c, ((part[0][at] + part[1][at]) + part[2][at]) + part[3][at]);
+    }
+  }
+}
+
+}  // namespace sg

@@ -244,10 +244,70 @@ int64_t split_bytes(const ProductArgs& g, const Choice& ch) {
   return (int64_t)ch.splits * g.M * g.N * (g.mode == sg::kSumGroups ? g.groups : 1) * 4;
 }
 
+// The kernels for a few rows (kernel_rows.hpp): rows a chunk, columns a
+// workgroup; rows 0: not for this product.
+struct RowsChoice {
+  int rows, cols;
+  int64_t workgroups;
+};
+
+// Measured on MI355X against product_kernel with a workspace (us, B from HBM;
+// N = K = 4096, and eight groups of N = 4096, K = 1024):
+//      B stored         N x K             K x N
+//      8 rows           15.8 / 19.2       16.3 / 21.8
+//      16 rows          18.0 / 20.3       24.5 / 21.8
+//      groups, avg. 1   17.7 / 24.4       18.4 / 22.8
+//      groups, avg. 4   31.8 / 35.7       29.7 / 31.4
+//      groups, avg. 8   39.5 / 37.9       36.6 / 33.7
+// Columns a workgroup: the most that still give every CU a workgroup.
+RowsChoice choose_rows(const Product& p) {
+  const ProductArgs& g = p.g;
+  RowsChoice none = {0, 0, 0};
+  if (p.trans_a || g.mode == sg::kSumGroups) return none;
+  const bool grouped = g.mode == sg::kRowGroups;
+  const int64_t live = grouped ? live_groups(g) : 1;
+  const int64_t most = grouped ? 4 * live : p.trans_b ? 2 * sg::kRowsMost : sg::kRowsMost;
+  if (g.M > most && g.M > sg::kRowsMost) return none;
+  // A chunk has room for a group of twice the average.
+  const int64_t want = grouped ? cdiv(2 * g.M, live) : g.M;
+  RowsChoice ch = {1, p.trans_b ? 16 : 64, 0};
+  while (ch.rows < sg::kRowsMost && ch.rows < want && ch.rows < g.M) ch.rows *= 2;
+  const int64_t chunks = grouped ? live : cdiv(g.M, ch.rows);
+  if (p.trans_b) {
+    if (cdiv(g.N, 16) * chunks < kCUs) ch.cols = 4;
+  } else {
+    while (ch.cols > 16 && cdiv(g.N, ch.cols) * chunks < kCUs) ch.cols /= 2;
+  }
+  const sg::host::TileCost c = {ch.rows, ch.cols, 0, 0, 0, 0};
+  ch.workgroups = grid_tiles(g, c);
+  return grid_fits(ch.workgroups, 256) ? ch : none;
+}
+
+// Few columns over a long K x N matrix leave the chip idle, where a split
+// product fills it: 1 x 1024 x 8192 takes 18.2 us by rows and 14.5 us split,
+// at K = 1024 it is 4.5 and 9.0.
+bool rather_split(const Product& p, const RowsChoice& rows, const Choice& ch) {
+  return !p.trans_b && ch.v != nullptr && ch.splits > 1 && p.g.K > 4096 &&
+         rows.workgroups < kCUs / 2;
+}
+
 int run_product(Product& p, const int32_t* offsets, hipStream_t stream, void* ws,
                 int64_t ws_bytes) {
   ProductArgs& g = p.g;
-  const Choice ch = choose(p, ws_bytes);
+  const RowsChoice rows = choose_rows(p);
+  Choice ch = {nullptr, 1, 0, 0};
+  // Only a long K asks what a split would be.
+  if (rows.rows == 0 || g.K > 4096) ch = choose(p, ws_bytes);
+  if (rows.rows > 0 && !rather_split(p, rows, ch)) {
+    g.tiles_m = (int)cdiv(g.M, rows.rows);
+    g.tiles_n = (int)cdiv(g.N, rows.cols);
+    g.group_m = g.tiles_m < 8 ? g.tiles_m : 8;
+    void* args[] = {&g};
+    const hipError_t e = hipLaunchKernel(
+        reinterpret_cast<const void*>(sg::rows_kernel(p.trans_b, rows.rows, rows.cols)),
+        dim3((unsigned)rows.workgroups), dim3(256), args, 0, stream);
+    return e == hipSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH;
+  }
   if (ch.v == nullptr) return SGEMM_ERR_UNSUPPORTED;
   const sg::host::TileCost& c = ch.v->cost;
   g.tiles_m = (int)cdiv(g.M, c.tile_m);
@@ -301,7 +361,9 @@ bool sizes_ok(int64_t a, int64_t b, int64_t c) {
 
 int64_t plan_workspace(const Product& p) {
   if (!p.launch) return 0;
-  return split_bytes(p.g, choose(p, INT64_MAX));
+  const Choice ch = choose(p, INT64_MAX);
+  const RowsChoice rows = choose_rows(p);
+  return rows.rows > 0 && !rather_split(p, rows, ch) ? 0 : split_bytes(p.g, ch);
 }
 
 // Strips of rows per group: enough workgroups for the chip, strips of 16 rows
@@ -414,6 +476,18 @@ int sgemm_linear_plan_query(int trans_a, int trans_b, int64_t M, int64_t N, int6
   const Product p = shape_only(sg::kDense, trans_a, trans_b, M, N, K, 1, 0);
   if (!p.launch) return SGEMM_OK;
   const Choice ch = choose(p, workspace_bytes);
+  const RowsChoice rows = choose_rows(p);
+  if (rows.rows > 0 && !rather_split(p, rows, ch)) {
+    plan->algo = SGEMM_ALGO_FMA;
+    plan->tile_m = rows.rows;
+    plan->tile_n = rows.cols;
+    plan->threads = 256;
+    plan->vec_a = plan->vec_b = 1;
+    plan->workgroups = rows.workgroups;
+    snprintf(plan->kernel, sizeof(plan->kernel), "rows_%s_%dx%d", trans_b ? "fast" : "slow",
+             rows.rows, rows.cols);
+    return SGEMM_OK;
+  }
   if (ch.v == nullptr) return SGEMM_ERR_UNSUPPORTED;
   const sg::host::TileCost& c = ch.v->cost;
   plan->algo = SGEMM_ALGO_MFMA_DIRECT;

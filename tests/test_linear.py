@@ -411,7 +411,7 @@ def test_act_backward_refuses(lib, args):
 
 
 def test_act_backward_refuses_a_bad_workspace(lib):
-    a = (400, 8, BIG, 8, FAR, 8, 1, FAR * 2, 8, FAR * 3)
+    a = (400000, 8, BIG, 8, FAR, 8, 1, FAR * 2, 8, FAR * 3)
     for ws, n in ((0, 4096), (FAR * 4 + 2, 4096), (FAR * 4, -4), (BIG, 4096), (FAR, 4096),
                   (FAR * 2, 4096), (FAR * 3, 4096)):
         assert sg.sgemm_act_backward(*a, 0, ws, n) == sg.ERR_INVALID_ARG, (ws, n)

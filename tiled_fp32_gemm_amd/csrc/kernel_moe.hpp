@@ -60,39 +60,55 @@ __global__ void __launch_bounds__(64 * WAVES) moe_sort_kernel(SortArgs a) {
   constexpr int NT = 64 * WAVES;
   __shared__ int next[WAVES][kMaxExperts];   // each wave's count, then its next row
   __shared__ int total[kMaxExperts];         // of all chunks, then the first row
+  __shared__ int before[kMaxExperts];        // of the chunks before this one
   __shared__ int kept;
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int b = (int)blockIdx.x;
-  for (int e = tid; e < a.E; e += NT)
+  for (int e = tid; e < a.E; e += NT) {
+    total[e] = before[e] = 0;
     for (int w = 0; w < WAVES; ++w) next[w][e] = 0;
+  }
   __syncthreads();
   const int64_t first = (int64_t)b * a.chunk;
   const int last = (int)min(first + a.chunk, (int64_t)a.n);
   const int per = ((a.chunk + WAVES - 1) / WAVES + 63) / 64 * 64;   // a wave's part
   const int64_t w0 = first + (int64_t)wave * per;
   const int64_t w1 = min(w0 + per, (int64_t)last);
+#pragma unroll 4
   for (int64_t i = w0 + lane; i < w1; i += 64) {
     const int e = expert_of<Id>(a.experts, (int)i, a.E);
     if (e >= 0) atomicAdd(&next[wave][e], 1);
   }
   __syncthreads();
-  // Each wave's count becomes the rows of its expert before it: in this chunk
-  // here, in the chunks before below.
-  for (int e = tid; e < a.E; e += NT) {
-    int before = 0, all = 0;
-    if (a.chunks > 1) {
-      for (int c = 0; c < a.chunks; ++c) {
-        const int v = a.counts[(int64_t)c * a.E + e];
-        before += c < b ? v : 0;
-        all += v;
+  if (a.chunks > 1) {   // all chunks' counts, and those of the chunks before
+    const int n = a.chunks * a.E, mine = b * a.E, skip = NT % a.E;
+    int e = tid % a.E;
+    constexpr int U = 16;   // counts in flight
+    for (int i0 = tid; i0 < n; i0 += U * NT) {
+      int v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = i0 + u * NT < n ? a.counts[i0 + u * NT] : 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (v[u] != 0) {
+          atomicAdd(&total[e], v[u]);
+          if (i0 + u * NT < mine) atomicAdd(&before[e], v[u]);
+        }
+        e += skip;
+        if (e >= a.E) e -= a.E;
       }
     }
+    __syncthreads();
+  }
+  // Each wave's count becomes the rows of its expert before it.
+  for (int e = tid; e < a.E; e += NT) {
+    int row = before[e];
     for (int w = 0; w < WAVES; ++w) {
       const int v = next[w][e];
-      next[w][e] = before;
-      before += v;
+      next[w][e] = row;
+      row += v;
     }
-    total[e] = a.chunks > 1 ? all : before;
+    if (a.chunks == 1) total[e] = row;
   }
   __syncthreads();
   if (wave == 0) {   // exclusive scan of the totals
@@ -118,10 +134,12 @@ __global__ void __launch_bounds__(64 * WAVES) moe_sort_kernel(SortArgs a) {
   }
   for (int64_t r = first + tid; r < last; r += NT)   // this chunk's share of the rows
     if (r >= kept) a.order[r] = -1;
+  int ahead = w0 + lane < w1 ? expert_of<Id>(a.experts, (int)(w0 + lane), a.E) : -1;
   for (int64_t i0 = w0; i0 < w1; i0 += 64) {
     const int64_t i = i0 + lane;
     const bool in = i < w1;
-    const int e = in ? expert_of<Id>(a.experts, (int)i, a.E) : -1;
+    const int e = ahead;
+    ahead = i + 64 < w1 ? expert_of<Id>(a.experts, (int)i + 64, a.E) : -1;
     uint64_t same = __ballot(e >= 0);
     for (int k = 0; k < a.bits; ++k) {
       const bool bit = (e >> k) & 1;
@@ -196,7 +214,7 @@ __global__ void __launch_bounds__(256) moe_unpermute_kernel(MoveArgs a) {
         const int p = a.place[c];
         if (p >= 0 && p < a.rows) {
           w[u] = a.weights ? a.weights[c] : 1.0f;
-          v[u] = load_upto(a.in + p * a.ld_in + col, n);
+          v[u] = load_upto_once(a.in + p * a.ld_in + col, n);
         }
       }
     }

@@ -366,12 +366,19 @@ int64_t plan_workspace(const Product& p) {
   return rows.rows > 0 && !rather_split(p, rows, ch) ? 0 : split_bytes(p.g, ch);
 }
 
-// Strips of rows per group: enough workgroups for the chip, strips of 16 rows
-// or more, within the workspace.
+int act_lanes(int64_t N) {
+  int lpr = 64;
+  while (lpr > 1 && 2 * N <= 4 * lpr) lpr /= 2;
+  return lpr;
+}
+
+// Strips of rows per group: enough workgroups for the chip (four a CU), at
+// least four rounds of rows each, within the workspace.
 int64_t act_strips(int64_t M, int64_t N, int64_t groups, int64_t ws_bytes) {
-  const int64_t blocks = cdiv(N, sg::kActCols) * groups;
-  int64_t s = cdiv(8 * kCUs, blocks);
-  const int64_t most = cdiv(cdiv(M, groups), 16);
+  const int lpr = act_lanes(N);
+  const int64_t blocks = cdiv(N, 4 * lpr) * groups;
+  int64_t s = cdiv(4 * kCUs, blocks);
+  const int64_t most = cdiv(cdiv(M, groups), 4 * (64 / lpr) * sg::kActWaves);
   if (s > most) s = most;
   const int64_t room = ws_bytes / 4 / (groups * N);
   if (s > room) s = room;
@@ -422,7 +429,8 @@ int act_backward(int64_t M, int64_t N, int64_t groups, const int32_t* offsets, b
   a.N = (int)N;
   a.groups = (int)groups;
   a.act = act;
-  a.blocks_n = (int)cdiv(N, sg::kActCols);
+  a.lpr = act_lanes(N);
+  a.blocks_n = (int)cdiv(N, 4 * a.lpr);
   // Without sums the strips need no room.
   const int64_t strips = act_strips(M, N, groups, dbias ? ws_bytes : INT64_MAX);
   a.strips = (int)strips;
@@ -431,8 +439,8 @@ int act_backward(int64_t M, int64_t N, int64_t groups, const int32_t* offsets, b
     if (overlaps(w, c) || overlaps(w, z) || overlaps(w, d) || overlaps(w, b) || overlaps(w, off))
       return SGEMM_ERR_INVALID_ARG;
   }
-  const int64_t wgs = a.blocks_n * strips * groups, sums = cdiv(N, 64) * groups;
-  if (!grid_fits(wgs, 64 * sg::kActWaves) || !grid_fits(sums, 256)) return SGEMM_ERR_UNSUPPORTED;
+  const int64_t wgs = a.blocks_n * strips * groups, sums = cdiv(N, sg::kSumCols) * groups;
+  if (!grid_fits(wgs, 64 * sg::kActWaves) || !grid_fits(sums, 1024)) return SGEMM_ERR_UNSUPPORTED;
   void* kargs[] = {&a};
   const void* fn = Z ? reinterpret_cast<const void*>(sg::act_backward_kernel<true>)
                      : reinterpret_cast<const void*>(sg::act_backward_kernel<false>);
@@ -440,7 +448,7 @@ int act_backward(int64_t M, int64_t N, int64_t groups, const int32_t* offsets, b
                                  stream);
   if (e == hipSuccess && dbias && strips > 1)
     e = hipLaunchKernel(reinterpret_cast<const void*>(sg::column_sum_kernel),
-                        dim3((unsigned)sums), dim3(256), kargs, 0, stream);
+                        dim3((unsigned)sums), dim3(1024), kargs, 0, stream);
   return e == hipSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH;
 }
 

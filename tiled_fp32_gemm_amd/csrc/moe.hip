@@ -17,7 +17,7 @@ using sg::SortArgs;
 // One workgroup sorts up to kSortOne choices; more are cut into chunks of
 // kSortChunk, or longer ones so that there are at most kSortChunks.
 constexpr int64_t kSortOne = 8192;
-constexpr int64_t kSortChunk = 2048;
+constexpr int64_t kSortChunk = 1024;
 constexpr int64_t kSortChunks = 512;
 
 int64_t sort_chunk(int64_t n) {

@@ -20,6 +20,11 @@ __device__ __forceinline__ f32x4 load_upto(const float* p, int n) {
   if (n > 2) v[2] = p[2];
   return v;
 }
+// load_upto for data that is read once.
+__device__ __forceinline__ f32x4 load_upto_once(const float* p, int n) {
+  if (n >= 4) return __builtin_nontemporal_load(reinterpret_cast<const f32x4u*>(p));
+  return load_upto(p, n);
+}
 __device__ __forceinline__ void store_upto(float* p, int n, f32x4 v) {
   if (n >= 4) {
     *reinterpret_cast<f32x4u*>(p) = v;

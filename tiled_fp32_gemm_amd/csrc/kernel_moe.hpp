@@ -188,10 +188,10 @@ __global__ void __launch_bounds__(256) moe_permute_kernel(MoveArgs a) {
   int col;
   if (!move_place(a, t, col)) return;
   const int n = a.H - col;
-  const f32x4 v = load_upto(a.in + t * a.ld_in + col, n);
+  const f32x4 v = load_upto_once(a.in + t * a.ld_in + col, n);
   for (int j = 0; j < a.top; ++j) {
     const int p = a.place[t * a.top + j];
-    if (p >= 0 && p < a.rows) store_upto(a.out + p * a.ld_out + col, n, v);
+    if (p >= 0 && p < a.rows) store_upto_once(a.out + p * a.ld_out + col, n, v);
   }
 }
 
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(256) moe_unpermute_kernel(MoveArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) sum[e] = fmaf(w[u], v[u][e], sum[e]);
   }
-  store_upto(a.out + t * a.ld_out + col, n, sum);
+  store_upto_once(a.out + t * a.ld_out + col, n, sum);
 }
 
 // G lanes per choice.
@@ -246,14 +246,14 @@ __global__ void __launch_bounds__(256) moe_unpermute_backward_kernel(MoveArgs a)
     const int n = a.H - col;
     f32x4 d = load_upto(g + col, n);
     if (a.dweights) {
-      const f32x4 v = load_upto(y + col, n);
+      const f32x4 v = load_upto_once(y + col, n);
 #pragma unroll
       for (int e = 0; e < 4; ++e) dot[e] = fmaf(d[e], v[e], dot[e]);
     }
     if (a.out) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) d[e] *= w;
-      store_upto(o + col, n, d);
+      store_upto_once(o + col, n, d);
     }
   }
   if (!a.dweights) return;

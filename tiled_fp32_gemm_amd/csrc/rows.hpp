@@ -35,4 +35,10 @@ __device__ __forceinline__ void store_upto(float* p, int n, f32x4 v) {
   if (n > 2) p[2] = v[2];
 }
 
+// store_upto for data that is not read back soon.
+__device__ __forceinline__ void store_upto_once(float* p, int n, f32x4 v) {
+  if (n >= 4) __builtin_nontemporal_store(f32x4u(v), reinterpret_cast<f32x4u*>(p));
+  else store_upto(p, n, v);
+}
+
 }  // namespace sg

@@ -94,12 +94,14 @@ struct RowTile {
   int tm, tn, split;
 };
 
-__device__ __forceinline__ int scan64(int v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
+// Inclusive sum over the lanes of a wave, by row shifts and row broadcasts.
+__device__ __forceinline__ int scan64(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast:31
   return v;
 }
 
@@ -121,42 +123,67 @@ __device__ __forceinline__ void tile_order(int L, int tiles_m, int tiles_n, int 
   tn = in / rows;
 }
 
-// False: no tile for this workgroup.
+// False: no tile for this workgroup.  The groups' whole tiles come first, in
+// group order, then their partial last ones, which are shorter work: the
+// launch ends with them, and each XCD has its share of both.  Every wave does
+// this for itself, 64 groups at a time, and almost always has all of them at
+// once.
 template <int BM>
 __device__ __forceinline__ bool row_group_tile(const ProductArgs& g, int lane, RowTile& t) {
-  int total = 0;
-  for (int e0 = 0; e0 < g.groups; e0 += 64) {
-    int b = 0, e = 0;
+  int b = 0, e = 0, whole = 0, upto = 0;
+  bool part = false;   // looking for partial tiles
+  auto scan = [&](int e0) {
+    b = e = 0;
     if (e0 + lane < g.groups) group_range(g.offsets, e0 + lane, g.rows, b, e);
-    total += __shfl(scan64((e - b + BM - 1) / BM, lane), 63);
+    whole = (e - b) / BM;
+    upto = scan64(part ? ((e - b) % BM != 0 ? 1 : 0) : whole);
+  };
+  auto count = [&]() {
+    scan(0);
+    int n = __builtin_amdgcn_readlane(upto, 63);
+    if (g.groups > 64) {
+      for (int e0 = 64; e0 < g.groups; e0 += 64) {
+        scan(e0);
+        n += __builtin_amdgcn_readlane(upto, 63);
+      }
+      scan(0);
+    }
+    return n * g.tiles_n;
+  };
+  int w = (int)blockIdx.x;
+  int total = count();
+  if (w >= total * g.splits) {
+    w -= total * g.splits;
+    part = true;
+    total = count();
+    if (w >= total * g.splits) return false;
   }
-  total *= g.tiles_n;
-  const int w = (int)blockIdx.x;
-  if (w >= total * g.splits) return false;
   int L = xcd_order(w, total * g.splits);
   t.split = L / total;
   L -= t.split * total;
+  const int row_tile = L / g.tiles_n;   // of all groups' row tiles
   int before = 0;
-  for (int e0 = 0; e0 < g.groups; e0 += 64) {
-    int b = 0, e = 0;
-    if (e0 + lane < g.groups) group_range(g.offsets, e0 + lane, g.rows, b, e);
-    const int tiles = (e - b + BM - 1) / BM;
-    const int upto = before + scan64(tiles, lane) * g.tiles_n;
-    const uint64_t past = __ballot(upto > L);
+  for (int e0 = 0;;) {
+    const uint64_t past = __ballot(before + upto > row_tile);
     if (past != 0) {
       const int at = __ffsll((unsigned long long)past) - 1;
-      const int tiles_m = __shfl(tiles, at);
-      L -= __shfl(upto, at) - tiles_m * g.tiles_n;
+      const int rows = __builtin_amdgcn_readlane(whole, at);
+      const int tiles_m = part ? 1 : rows;
+      L -= (before + __builtin_amdgcn_readlane(upto, at) - tiles_m) * g.tiles_n;
       t.group = e0 + at;
-      t.first = __shfl(b, at);
-      t.end = __shfl(e, at);
+      t.first = __builtin_amdgcn_readlane(b, at);
+      t.end = __builtin_amdgcn_readlane(e, at);
       tile_order(L, tiles_m, g.tiles_n, min(tiles_m, 8), t.tm, t.tn);
       // Offsets that fall could make the counts above overflow.
-      return t.tm >= 0 && t.tm < tiles_m && t.tn >= 0 && t.tn < g.tiles_n;
+      const bool good = t.tm >= 0 && t.tm < tiles_m && t.tn >= 0 && t.tn < g.tiles_n;
+      if (part) t.tm = rows;
+      return good && t.first + t.tm * BM < t.end;
     }
-    before = __shfl(upto, 63);
+    before += __builtin_amdgcn_readlane(upto, 63);
+    e0 += 64;
+    if (e0 >= g.groups) return false;
+    scan(e0);
   }
-  return false;
 }
 
 // AFAST: A is M x K.  BFAST: B is N x K.
@@ -193,13 +220,15 @@ product_kernel(ProductArgs g) {
     kb = split * g.k_split;
     K = g.splits > 1 ? min(g.k_split, g.K - kb) : g.K;
   } else {
+    // Summed groups differ in length: the XCDs share each group's tiles, rather
+    // than take whole groups.
     const int tiles = g.tiles_m * g.tiles_n;
-    int L = xcd_order((int)blockIdx.x, (int)gridDim.x);
-    split = L / (tiles * g.groups);
-    L -= split * tiles * g.groups;
-    group = L / tiles;
+    const int per_group = g.mode == kSumGroups ? tiles * g.splits : (int)gridDim.x;
+    group = (int)blockIdx.x / per_group;
+    const int L = xcd_order((int)blockIdx.x - group * per_group, per_group);
+    split = L / tiles;
     int tm, tn;
-    tile_order(L - group * tiles, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
+    tile_order(L - split * tiles, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
     row0 = tm * BM;
     m_left = g.M - row0;
     n0 = tn * BN;
@@ -422,6 +451,10 @@ product_kernel(ProductArgs g) {
       mfma_chunk(fr[1], std::false_type(), qz, qz, st, std::false_type());
     }
   };
+  // A wave whose part of the tile lies outside C only loads: its share of the
+  // matrix pipe goes to the others, so an edge tile costs what its waves with
+  // work cost.
+  const bool works = wm0 < m_left && wn0 < n_left;
   if (nslab > 0) {
     issue(rsrc_a(0), rsrc_b(0), 0);
     __builtin_amdgcn_s_waitcnt(kWaitLoads);
@@ -429,15 +462,26 @@ product_kernel(ProductArgs g) {
     __builtin_amdgcn_s_waitcnt(kWaitLds);
     asm volatile("s_barrier" ::: "memory");
     if (nslab > 1) issue(rsrc_a(BK), rsrc_b(BK), 1);
-    read_chunk(fr[0], 0, 0);
-    int t = 0;
-    for (; t + 2 < nslab; ++t) step(t, std::true_type());
-    if (t + 1 < nslab) {
-      step(t, std::false_type());
-      ++t;
+    if (works) {
+      read_chunk(fr[0], 0, 0);
+      int t = 0;
+      for (; t + 2 < nslab; ++t) step(t, std::true_type());
+      if (t + 1 < nslab) {
+        step(t, std::false_type());
+        ++t;
+      }
+      chunks(t & 1);
+      mfma_chunk(fr[1], std::false_type(), qz, qz, 0, std::false_type());
+    } else {
+      // The same waits and barriers.
+      for (int t = 0; t + 1 < nslab; ++t) {
+        __builtin_amdgcn_s_waitcnt(kWaitLoads);
+        if (k_tail && t + 2 == nslab) fix_tail(t + 1, (t + 1) & 1);
+        __builtin_amdgcn_s_waitcnt(kWaitLds);
+        asm volatile("s_barrier" ::: "memory");
+        if (t + 2 < nslab) issue(rsrc_a((t + 2) * BK), rsrc_b((t + 2) * BK), t & 1);
+      }
     }
-    chunks(t & 1);
-    mfma_chunk(fr[1], std::false_type(), qz, qz, 0, std::false_type());
   }
   // Every wave has read its last fragments before LDS is used again.
   __syncthreads();

@@ -192,11 +192,14 @@ int64_t grid_tiles(const ProductArgs& g, const sg::host::TileCost& c) {
   return cdiv(g.M, c.tile_m) * tn * g.groups;
 }
 
-// Tiles with work, row groups taken as equal.
+// Whole tiles' worth of work.  A row group's last tile has, on average, half a
+// wave's rows of padding: waves without rows leave the others their share.
 int64_t likely_tiles(const ProductArgs& g, const sg::host::TileCost& c) {
   if (g.mode != sg::kRowGroups) return grid_tiles(g, c);
   const int64_t live = live_groups(g);
-  return live * cdiv(cdiv(g.M, live), c.tile_m) * cdiv(g.N, c.tile_n);
+  const int64_t wave_rows = c.tile_m >= 256 ? 64 : 32;
+  const int64_t rows = (2 * g.M + live * wave_rows) / (2 * c.tile_m);
+  return (rows > live ? rows : live) * cdiv(g.N, c.tile_n);
 }
 
 // The variant, and the split of K, with the least estimated time (the model

@@ -58,11 +58,14 @@ constexpr double kSlabFloor = 0.61e-6;  // s: a slab's wait for its loads
 constexpr double kRoundCost = 4.4e-6;   // s: fill and drain of one round
 constexpr double kWriteBW = 4.52e12;    // B/s: C stores of a final round
 
+
 // What the time model needs to know of a tile variant.
 struct TileCost {
   int tile_m, tile_n, tile_k, threads;
   double eff;   // fraction of a CU's FP32 matrix peak with its pipes busy
   int occ;      // workgroups a CU holds at once
+  double slab_floor = kSlabFloor;   // s a slab takes however little it computes
+  double saturate = kSaturate;      // waves per SIMD that keep the pipes busy
 };
 
 // Estimated seconds of a tile variant on an M x N x K product.  Workgroups are
@@ -81,9 +84,9 @@ inline double estimate_grid(const TileCost& v, int64_t tiles, int64_t K) {
   const double slab_flops = 2.0 * v.tile_m * v.tile_n * v.tile_k;
   auto round = [&](int64_t r) {
     const double simd = r * waves / 4.0;
-    const double busy = simd >= kSaturate ? 1.0 : simd / kSaturate;
+    const double busy = simd >= v.saturate ? 1.0 : simd / v.saturate;
     const double compute = r * slab_flops / (kPeakPerCU * v.eff * busy);
-    return (double)slabs * (compute > kSlabFloor ? compute : kSlabFloor) + kRoundCost;
+    return (double)slabs * (compute > v.slab_floor ? compute : v.slab_floor) + kRoundCost;
   };
   const int64_t full = n / v.occ, rest = n % v.occ;
   double t = (double)full * round(v.occ) + (rest > 0 ? round(rest) : 0.0);

@@ -45,9 +45,9 @@
 
 namespace sg {
 
-template <int BM, int BN, int WM, int WN, int BK_, int KS_>
+template <int BM, int BN, int WM, int WN, int BK_, int KS_, int STAGES_>
 struct ProductCfg {
-  static constexpr int BK = BK_, KS = KS_;
+  static constexpr int BK = BK_, KS = KS_, STAGES = STAGES_;
   static constexpr int CPR = BK / 4;
   static constexpr int SUB_G = BK / 16 / KS;   // 16-deep sub-slabs per wave group
   static constexpr int WAVES_N = BN / WN;
@@ -55,7 +55,7 @@ struct ProductCfg {
   static constexpr int NT = 64 * SPATIAL * KS;
   static constexpr int TA = WM / 32, TB = WN / 32;
   static constexpr int A_STAGE = BM * BK, B_STAGE = BK * BN;   // floats
-  static constexpr int STAGE_FLOATS = 2 * (A_STAGE + B_STAGE);
+  static constexpr int STAGE_FLOATS = STAGES * (A_STAGE + B_STAGE);
   static constexpr int RED_FLOATS = (KS - 1) * BM * BN;
   static constexpr int OUT_FLOATS = SPATIAL * 32 * WN;
   static constexpr int max3(int a, int b, int c) {
@@ -69,9 +69,10 @@ struct ProductCfg {
   static_assert(SUB_G * KS * 16 == BK, "whole sub-slabs per wave group");
 };
 
-// s_waitcnt immediates: every vector-memory operation of this wave, and every
-// LDS access of it (the other counts at their maxima).
-constexpr int kWaitLoads = (0x7 << 4) | (0xF << 8);
+// s_waitcnt immediates for this wave's vector-memory operations and for its LDS
+// accesses (the other counts at their maxima).
+template <int n>   // at most n vector-memory operations left
+constexpr int kWaitLoads = (n & 0xF) | (0x7 << 4) | (0xF << 8) | ((n >> 4) << 14);
 constexpr int kWaitLds = 0xF | (0x7 << 4) | (0x3 << 14);
 
 // Where one operand's unit u of a slab stage comes from: for k fast the row
@@ -187,15 +188,16 @@ __device__ __forceinline__ bool row_group_tile(const ProductArgs& g, int lane, R
 }
 
 // AFAST: A is M x K.  BFAST: B is N x K.
-template <int BM, int BN, int WM, int WN, int BK_, int KS_, bool AFAST, bool BFAST>
+template <int BM, int BN, int WM, int WN, int BK_, int KS_, int STAGES_, bool AFAST, bool BFAST>
 __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN) * KS_)
 product_kernel(ProductArgs g) {
-  using Cfg = ProductCfg<BM, BN, WM, WN, BK_, KS_>;
+  using Cfg = ProductCfg<BM, BN, WM, WN, BK_, KS_, STAGES_>;
+  constexpr int S = Cfg::STAGES;
   constexpr int BK = Cfg::BK, NT = Cfg::NT, TA = Cfg::TA, TB = Cfg::TB, CPR = Cfg::CPR;
   constexpr int KS = Cfg::KS, SUB_G = Cfg::SUB_G;
   __shared__ __attribute__((aligned(16))) float lds[Cfg::LDS_FLOATS];
-  float* const As = lds;                      // [2][A_STAGE]
-  float* const Bs = lds + 2 * Cfg::A_STAGE;   // [2][B_STAGE]
+  float* const As = lds;                      // [S][A_STAGE]
+  float* const Bs = lds + S * Cfg::A_STAGE;   // [S][B_STAGE]
 
   const int tid = (int)threadIdx.x;
   const int lane = tid & 63;
@@ -426,17 +428,20 @@ product_kernel(ProductArgs g) {
                  std::integral_constant<bool, KS == 4>());
     }
   };
+  // Slab t (in stage t mod S) when a slab t + 1 follows; with LOADS slab t + S is
+  // loaded into the stage that slab t leaves, and slabs t + 2 .. t + S - 1 stay
+  // in flight across the wait.
   auto step = [&](int t, auto loads) {
     constexpr bool kLoads = decltype(loads)::value;
-    const int st = t & 1, nst = st ^ 1;
+    const int st = t % S, nst = (t + 1) % S;
     __amdgpu_buffer_rsrc_t qa = qz, qb = qz;
     if constexpr (kLoads) {
-      qa = rsrc_a((t + 2) * BK);
-      qb = rsrc_b((t + 2) * BK);
+      qa = rsrc_a((t + S) * BK);
+      qb = rsrc_b((t + S) * BK);
     }
     chunks(st);
     if constexpr (KS == 2) __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(kWaitLoads);
+    __builtin_amdgcn_s_waitcnt(kWaitLoads<kLoads ? (S - 2) * Cfg::LOADS : 0>);
     if (k_tail && t + 2 == nslab) fix_tail(t + 1, nst);
     __builtin_amdgcn_s_waitcnt(kWaitLds);
     asm volatile("s_barrier" ::: "memory");
@@ -456,30 +461,45 @@ product_kernel(ProductArgs g) {
   // work cost.
   const bool works = wm0 < m_left && wn0 < n_left;
   if (nslab > 0) {
+    // Slabs 0 .. S-2 go out at once; slab 0 is waited for (with those behind it
+    // when there are fewer), published, and slab S-1 goes out.
     issue(rsrc_a(0), rsrc_b(0), 0);
-    __builtin_amdgcn_s_waitcnt(kWaitLoads);
+#pragma unroll
+    for (int j = 1; j + 1 < S; ++j)
+      if (j < nslab) issue(rsrc_a(j * BK), rsrc_b(j * BK), j);
+    if (nslab >= S - 1)
+      __builtin_amdgcn_s_waitcnt(kWaitLoads<(S - 2) * Cfg::LOADS>);
+    else
+      __builtin_amdgcn_s_waitcnt(kWaitLoads<0>);
     if (k_tail && nslab == 1) fix_tail(0, 0);
     __builtin_amdgcn_s_waitcnt(kWaitLds);
     asm volatile("s_barrier" ::: "memory");
-    if (nslab > 1) issue(rsrc_a(BK), rsrc_b(BK), 1);
+    if (nslab > S - 1) issue(rsrc_a((S - 1) * BK), rsrc_b((S - 1) * BK), S - 1);
     if (works) {
       read_chunk(fr[0], 0, 0);
       int t = 0;
-      for (; t + 2 < nslab; ++t) step(t, std::true_type());
-      if (t + 1 < nslab) {
-        step(t, std::false_type());
-        ++t;
+      for (; t + S < nslab; ++t) step(t, std::true_type());
+      if constexpr (S == 2) {
+        if (t + 1 < nslab) {
+          step(t, std::false_type());
+          ++t;
+        }
+      } else {
+        for (; t + 1 < nslab; ++t) step(t, std::false_type());
       }
-      chunks(t & 1);
+      chunks(t % S);
       mfma_chunk(fr[1], std::false_type(), qz, qz, 0, std::false_type());
     } else {
       // The same waits and barriers.
       for (int t = 0; t + 1 < nslab; ++t) {
-        __builtin_amdgcn_s_waitcnt(kWaitLoads);
-        if (k_tail && t + 2 == nslab) fix_tail(t + 1, (t + 1) & 1);
+        if (t + S < nslab)
+          __builtin_amdgcn_s_waitcnt(kWaitLoads<(S - 2) * Cfg::LOADS>);
+        else
+          __builtin_amdgcn_s_waitcnt(kWaitLoads<0>);
+        if (k_tail && t + 2 == nslab) fix_tail(t + 1, (t + 1) % S);
         __builtin_amdgcn_s_waitcnt(kWaitLds);
         asm volatile("s_barrier" ::: "memory");
-        if (t + 2 < nslab) issue(rsrc_a((t + 2) * BK), rsrc_b((t + 2) * BK), t & 1);
+        if (t + S < nslab) issue(rsrc_a((t + S) * BK), rsrc_b((t + S) * BK), t % S);
       }
     }
   }

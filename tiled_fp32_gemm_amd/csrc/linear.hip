@@ -229,7 +229,8 @@ Choice choose(const Product& p, int64_t ws_bytes) {
       const int64_t se = g.mode == sg::kSumGroups ? S : cdiv(K, ks);
       if (se < 2 || K < 2 * c.tile_k || se * out > ws_bytes / 4 ||
           !grid_fits(grid * se, c.threads) ||
-          !grid_fits(out / g.N * cdiv(g.N, sg::kProductReduceCols), 64))
+          !grid_fits(out / g.N * cdiv(g.N, sg::kProductReduceCols),
+                     64))
         continue;
       const double ts = 0.95 * estimate_grid(c, likely * se, ks) + 3.0e-6 +
                         (double)(se + 1) * out * 4.0 / 5.0e12;
@@ -281,7 +282,7 @@ RowsChoice choose_rows(const Product& p) {
   } else {
     while (ch.cols > 16 && cdiv(g.N, ch.cols) * chunks < kCUs) ch.cols /= 2;
   }
-  const sg::host::TileCost c = {ch.rows, ch.cols, 0, 0, 0, 0};
+  const sg::host::TileCost c = {ch.rows, ch.cols, 0, 0, 0, 0, 0, 0};
   ch.workgroups = grid_tiles(g, c);
   return grid_fits(ch.workgroups, 256) ? ch : none;
 }
@@ -332,8 +333,8 @@ int run_product(Product& p, const int32_t* offsets, hipStream_t stream, void* ws
   if (e == hipSuccess && ch.splits > 1) {
     const int64_t rows = (int64_t)g.M * (g.mode == sg::kSumGroups ? g.groups : 1);
     e = hipLaunchKernel(reinterpret_cast<const void*>(sg::product_reduce_kernel),
-                        dim3((unsigned)(rows * cdiv(g.N, sg::kProductReduceCols))), dim3(64),
-                        kargs, 0, stream);
+                        dim3((unsigned)(rows * cdiv(g.N, sg::kProductReduceCols))),
+                        dim3(64), kargs, 0, stream);
   }
   return e == hipSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH;
 }

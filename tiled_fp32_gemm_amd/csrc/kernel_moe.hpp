@@ -170,17 +170,19 @@ struct MoveArgs {
   int64_t ld_in, ld_grad, ld_out;
   int64_t T;
   int top, H, rows;       // rows = T top
-  int tx, chunks;         // threads along a row, column chunks of a row
 };
 
-// A row's thread: the token and the first column of its four.
+// The token and the first of the four columns of this thread: the rows' 16-byte
+// groups are numbered through, so that every lane has one whatever H is.
 __device__ __forceinline__ bool move_place(const MoveArgs& a, int64_t& t, int& col) {
-  const int ty = 256 / a.tx;
-  const int64_t b = (int64_t)blockIdx.x / a.chunks;
-  const int chunk = (int)((int64_t)blockIdx.x - b * a.chunks);
-  t = b * ty + (int)threadIdx.x / a.tx;
-  col = 4 * (chunk * a.tx + (int)threadIdx.x % a.tx);
-  return t < a.T && col < a.H;
+  const int groups = (a.H + 3) / 4;
+  const int64_t first = (int64_t)blockIdx.x * 256;
+  const int64_t t0 = first / groups;
+  const unsigned in = (unsigned)(first - t0 * groups) + threadIdx.x;
+  const unsigned down = in / (unsigned)groups;
+  t = t0 + down;
+  col = 4 * (int)(in - down * (unsigned)groups);
+  return t < a.T;
 }
 
 __global__ void __launch_bounds__(256) moe_permute_kernel(MoveArgs a) {
@@ -242,18 +244,27 @@ __global__ void __launch_bounds__(256) moe_unpermute_backward_kernel(MoveArgs a)
   const float* y = a.in + p * a.ld_in;
   float* o = a.out + p * a.ld_out;
   f32x4 dot = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int col = 4 * lane; col < a.H; col += 4 * G) {
-    const int n = a.H - col;
-    f32x4 d = load_upto(g + col, n);
-    if (a.dweights) {
-      const f32x4 v = load_upto_once(y + col, n);
+  constexpr int U = 4;   // groups in flight
+  for (int c0 = 4 * lane; c0 < a.H; c0 += U * 4 * G) {
+    f32x4 d[U], v[U];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) dot[e] = fmaf(d[e], v[e], dot[e]);
+    for (int u = 0; u < U; ++u) {
+      const int col = c0 + u * 4 * G, n = a.H - col;
+      d[u] = v[u] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (n > 0) {
+        d[u] = load_upto(g + col, n);
+        if (a.dweights) v[u] = load_upto_once(y + col, n);
+      }
     }
-    if (a.out) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) d[e] *= w;
-      store_upto_once(o + col, n, d);
+    for (int u = 0; u < U; ++u) {
+      const int col = c0 + u * 4 * G, n = a.H - col;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        dot[e] = fmaf(d[u][e], v[u][e], dot[e]);
+        d[u][e] *= w;
+      }
+      if (a.out && n > 0) store_upto_once(o + col, n, d[u]);
     }
   }
   if (!a.dweights) return;

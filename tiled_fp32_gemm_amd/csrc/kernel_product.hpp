@@ -33,7 +33,7 @@
 // wave in its own part, no barrier), so that bias, activation and residual are
 // applied four columns a lane in a short loop and every global access is 16
 // bytes a lane along a row.  The residual's loads are issued before the
-// activation runs.  Split K (splits > 1) stores the partial sums instead;
+// activation runs, for small wave tiles before the main loop.  Split K (splits > 1) stores the partial sums instead;
 // kernel_product_reduce.hpp adds them and applies the epilogue.
 #pragma once
 
@@ -258,6 +258,39 @@ product_kernel(ProductArgs g) {
   split = __builtin_amdgcn_readfirstlane(split);
   const int n_left = g.N - n0;
 
+  // The lane's four columns and rows in the epilogue: LPR lanes take a row's
+  // 16-byte groups, so IT rounds cover 32 rows.  Small wave tiles have registers
+  // to spare and load the bias and the residual now, under the main loop; the
+  // large ones do after it.
+  constexpr int LPR = WN / 4, RPI = 64 / LPR, IT = 32 / RPI;
+  constexpr bool kEarly = TA * TB == 1;
+  const bool partial = g.splits > 1;
+  const bool has_bias = !partial && g.bias != nullptr;
+  const float* res = partial || !g.residual ? nullptr : g.residual + (int64_t)row0 * g.ldr + n0;
+  f32x4 bias = {0.0f, 0.0f, 0.0f, 0.0f}, add[IT];
+  auto load_bias = [&](int ln) {
+    const int cols = n_left - wn0 - 4 * (ln % LPR);
+    if (has_bias && cols > 0)
+      bias = load_upto(g.bias + group * g.ld_bias + n0 + wn0 + 4 * (ln % LPR), cols);
+  };
+  // Row q of block i of the wave tile, from the tile's first row.
+  constexpr bool kPairA = !AFAST && TA == 2, kPairB = !BFAST && TB == 2;
+  auto row_of = [&](int i, int q) { return wm0 + (kPairA ? 2 * q + i : 32 * i + q); };
+  auto load_residual = [&](int i, int ln) {
+    const int col = wn0 + 4 * (ln % LPR), cols = n_left - col;
+    if (!res) return;
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      const int row = row_of(i, it * RPI + ln / LPR);
+      if (row < m_left && cols > 0)
+        add[it] = load_upto(res + (uint32_t)row * (uint32_t)g.ldr + (uint32_t)col, cols);
+    }
+  };
+  if (kEarly && grp == 0) {
+    load_bias(lane);
+    load_residual(0, lane);
+  }
+
   // The tile's corner of each operand, and the bytes of it from there to the
   // last element this tile reads (one tile's rows when k is fast).
   const float* At = AFAST ? g.A + (int64_t)row0 * g.lda + kb : g.A + (int64_t)kb * g.lda + row0;
@@ -354,7 +387,6 @@ product_kernel(ProductArgs g) {
   };
 
   constexpr bool kSpread = KS == 1;
-  constexpr bool kPairA = !AFAST && TA == 2, kPairB = !BFAST && TB == 2;
   constexpr int NCH = 2 * SUB_G;
   struct Frag {
     f32x4 a[TA], b[TB];   // 4 k steps
@@ -536,9 +568,7 @@ product_kernel(ProductArgs g) {
     if (grp > 0) return;
   }
 
-  // The epilogue, 32 rows of the wave tile at a time.  LPR lanes take a row's
-  // 16-byte groups, so IT rounds cover the 32 rows.
-  constexpr int LPR = WN / 4, RPI = 64 / LPR, IT = 32 / RPI;
+  // The epilogue, 32 rows of the wave tile at a time.
   int ln = lane;
   asm volatile("" : "+v"(ln));
   const int col = 4 * (ln % LPR);              // from the wave's first column
@@ -546,7 +576,6 @@ product_kernel(ProductArgs g) {
   float* const rows = lds + sw * 32 * WN;
   float* out;
   int ld_out;
-  const bool partial = g.splits > 1;
   if (partial) {
     const int64_t plane = (int64_t)g.M * g.N;
     out = g.W + (g.mode == kSumGroups ? (int64_t)split * g.groups + group : split) * plane +
@@ -557,12 +586,8 @@ product_kernel(ProductArgs g) {
     ld_out = g.ldc;
   }
   out += n0;
-  const float* res = partial || !g.residual ? nullptr : g.residual + (int64_t)row0 * g.ldr + n0;
   float* pre = partial || !g.preact ? nullptr : g.preact + (int64_t)row0 * g.ldp + n0;
-  f32x4 bias = {0.0f, 0.0f, 0.0f, 0.0f};
-  const bool has_bias = !partial && g.bias != nullptr;
-  if (has_bias && cols > 0)
-    bias = load_upto(g.bias + group * g.ld_bias + n0 + wn0 + col, cols);
+  if (!kEarly) load_bias(ln);
   const int act = partial ? SGEMM_ACT_NONE : g.act;
 #pragma unroll
   for (int i = 0; i < TA; ++i) {
@@ -578,29 +603,22 @@ product_kernel(ProductArgs g) {
         for (int j = 0; j < TB; ++j) p[32 * j + li_c] = acc[i][j][r];
       }
     }
-    // Row q of the 32, from the tile's first row.
-    auto row_of = [&](int q) { return wm0 + (kPairA ? 2 * q + i : 32 * i + q); };
-    f32x4 add[IT];
-    if (res) {
-#pragma unroll
-      for (int it = 0; it < IT; ++it) {
-        const int row = row_of(it * RPI + ln / LPR);
-        if (row < m_left && cols > 0)
-          add[it] = load_upto(res + (uint32_t)row * (uint32_t)g.ldr + (uint32_t)(wn0 + col), cols);
-      }
-    }
+    if (!kEarly) load_residual(i, ln);
     // This wave's own part of LDS: its writes above, then its reads below.
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     f32x4* const mine = reinterpret_cast<f32x4*>(rows) + ln;
-    if (act != SGEMM_ACT_NONE || pre || has_bias) {
-#pragma unroll 1
+    // A bias alone is added with the residual.
+    const bool through = act != SGEMM_ACT_NONE || pre;
+    if (through) {
+      constexpr int kRounds = kEarly ? 2 : 1;
+#pragma unroll kRounds
       for (int it = 0; it < IT; ++it) {
         f32x4 z = mine[it * 64];
         z += bias;
         if (pre) {
-          const int row = row_of(it * RPI + ln / LPR);
+          const int row = row_of(i, it * RPI + ln / LPR);
           if (row < m_left && cols > 0)
             store_upto(pre + (uint32_t)row * (uint32_t)g.ldp + (uint32_t)(wn0 + col), cols, z);
         }
@@ -611,9 +629,10 @@ product_kernel(ProductArgs g) {
     }
 #pragma unroll
     for (int it = 0; it < IT; ++it) {
-      const int row = row_of(it * RPI + ln / LPR);
+      const int row = row_of(i, it * RPI + ln / LPR);
       if (row < m_left && cols > 0) {
         f32x4 v = mine[it * 64];
+        if (!through) v += bias;
         if (res) v += add[it];
         store_upto(out + (uint32_t)row * (uint32_t)ld_out + (uint32_t)(wn0 + col), cols, v);
       }

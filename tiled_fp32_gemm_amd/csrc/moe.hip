@@ -49,14 +49,9 @@ int check_move(int64_t T, int64_t top, int64_t H, int64_t ld_t, int64_t ld_rows,
 }
 
 int launch_move(const void* fn, MoveArgs& a, hipStream_t stream) {
-  const int64_t h4 = cdiv(a.H, 4);
-  a.tx = 4;
-  while (a.tx < 256 && a.tx < h4) a.tx *= 2;
-  a.chunks = (int)cdiv(h4, a.tx);
-  const int64_t blocks = cdiv(a.T, 256 / a.tx);
-  if (blocks > (int64_t(1) << 32) / a.chunks || !grid_fits(blocks * a.chunks, 256))
-    return SGEMM_ERR_UNSUPPORTED;
-  return launch(fn, blocks * a.chunks, 256, &a, stream);
+  const int64_t blocks = cdiv(a.T * cdiv(a.H, 4), 256);
+  if (!grid_fits(blocks, 256)) return SGEMM_ERR_UNSUPPORTED;
+  return launch(fn, blocks, 256, &a, stream);
 }
 
 }  // namespace

@@ -320,16 +320,126 @@ def test_linear_and_its_gradients_replay_from_a_graph(M, N, K):
             assert torch.equal(x, y), rep
 
 
-# Refusals (CPU).
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """Operands of more than 4 GiB, checked on rows from both ends."""
+    g = gen(17)
+    M, N, K = (1 << 20) + 3, 1100, 20
+    A = torch.randn(M, K, device="cuda", generator=g)
+    B = torch.randn(K, N, device="cuda", generator=g)
+    b = torch.randn(N, device="cuda", generator=g)
+    R, Z = torch.randn(M, N, device="cuda", generator=g), torch.empty(M, N, device="cuda")
+    rows = torch.tensor([0, 1, M // 2, M - 130, M - 2, M - 1], device="cuda")
+    C = sg.linear(A, B, b, "relu", R, preact=Z)
+    z = A[rows].double() @ B.double() + b.double()
+    tol = sum_tol(K) * (A[rows].double().abs() @ B.double().abs() + b.double().abs())
+    assert ((Z[rows].double() - z).abs() <= tol).all()
+    y = z.clamp(min=0) + R[rows].double()
+    assert ((C[rows].double() - y).abs() <= tol + 2 * U * y.abs()).all()
+    # the sums over all its rows, K slow in both operands
+    ws = torch.empty(1 << 24, device="cuda")
+    dz, db = sg.activation_backward(R, "relu", Z, out=C, workspace=ws)
+    assert torch.equal(dz[rows], torch.where(Z[rows] > 0, R[rows], 0.0))
+    dB = sg.linear(A, dz, transpose_a=True, workspace=ws)
+    # The same in 64 bits by parts, with the bounds of their sizes: 1e-5 as M is long.
+    want = torch.zeros(K, N, dtype=torch.float64, device="cuda")
+    size, sums, ssize = want.clone(), want[0].clone(), want[0].clone()
+    for i in range(0, M, 1 << 17):
+        a, d = A[i:i + (1 << 17)].double(), dz[i:i + (1 << 17)].double()
+        want += a.t() @ d
+        size += a.abs().t() @ d.abs()
+        sums += d.sum(0)
+        ssize += d.abs().sum(0)
+    assert ((dB.double() - want).abs() <= 1e-5 * size).all()
+    assert ((db.double() - sums).abs() <= 1e-5 * ssize).all()
+    # rows of a long k
+    T = dz.view(-1)[:(1 << 29) + 4].view(2, -1)[:, :(1 << 28) + 1]
+    W = torch.randn(3, T.shape[1], device="cuda", generator=g)
+    got = sg.linear(T, W, transpose_b=True, workspace=ws)
+    t, w = T.double(), W.double()
+    assert ((got.double() - t @ w.t()).abs() <= 1e-5 * (t.abs() @ w.abs().t())).all()
 
-BIG = 1 << 33
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("off", [0, 1, 2, 3])
+@pytest.mark.parametrize("M,N,K", [(3, 37, 70), (40, 37, 70), (70, 131, 64)])
+def test_every_alignment(off, M, N, K):
+    for pad in range(4):
+        run_case(M, N, K, act="silu", pad=pad, off=off)
+        run_case(M, N, K, tb=True, act="silu", pad=pad, off=off)
+
+
+@pytest.mark.gpu
+def test_non_finite_values_stay_in_their_rows_and_columns():
+    g = gen(19)
+    for M, N, K in ((5, 70, 100), (100, 130, 77), (300, 300, 64)):
+        A, B = torch.randn(M, K, device="cuda", generator=g), torch.randn(K, N, device="cuda",
+                                                                          generator=g)
+        clean = sg.linear(A, B)
+        A[M // 2, K - 1], B[0, N // 3] = float("nan"), float("inf")
+        for a, b, ta, tb in ((A, B, 0, 0), (A, B.t().contiguous(), 0, 1),
+                             (A.t().contiguous(), B, 1, 0)):
+            C = sg.linear(a, b, transpose_a=ta, transpose_b=tb)
+            assert C[M // 2].isnan().all() and not C[:, N // 3].isfinite().any()
+            keep = torch.ones(M, N, dtype=torch.bool, device="cuda")
+            keep[M // 2], keep[:, N // 3] = False, False
+            tol = 2 * sum_tol(K) * (A.nan_to_num(0).abs() @ B.nan_to_num(0, 0, 0).abs())
+            assert ((C - clean).abs()[keep] <= tol[keep]).all()
+
+
+# Plans (CPU).
 
 @pytest.fixture(scope="module")
 def lib():
     from tiled_fp32_gemm_amd import build
     build.ensure_built()
     return sg.load()
+
+
+@pytest.mark.parametrize("ta,tb,M,N,K,kernel", [
+    (0, 0, 4096, 4096, 4096, "product_fs_256x256x32"),
+    (0, 1, 4096, 4096, 4096, "product_ff_256x256x32"),
+    (1, 0, 4096, 4096, 4096, "product_ss_256x256x32"),
+    (1, 1, 8192, 8192, 8192, "product_sf_256x256x32"),
+    (0, 0, 1000, 1500, 777, "product_fs_32x64x32_ks2"),
+    (0, 0, 65536, 128, 256, "product_fs_128x128x32"),
+    (0, 1, 1, 4096, 4096, "rows_fast_1x16"), (0, 1, 1, 1024, 4096, "rows_fast_1x4"),
+    (0, 1, 12, 4096, 4096, "rows_fast_8x16"), (0, 0, 5, 4096, 4096, "rows_slow_8x16"),
+    (0, 0, 2, 32768, 1024, "rows_slow_2x64"), (0, 0, 9, 4096, 4096, "product_fs_32x64x32_ks2_s4"),
+    (1, 0, 1, 4096, 4096, "product_ss_32x64x32_ks2_s4")])
+def test_plans_without_workspace(lib, ta, tb, M, N, K, kernel):
+    st, plan = sg.sgemm_linear_plan_query(ta, tb, M, N, K)
+    assert st == sg.OK and plan.kernel.decode() == kernel
+    assert plan.splits == 1 and plan.workspace_bytes == 0 and plan.workgroups > 0
+
+
+def test_split_plans_fit_their_workspace(lib):
+    for ta, tb in itertools.product((0, 1), repeat=2):
+        for M, N, K in ((256, 256, 8192), (64, 64, 65536), (512, 512, 2048), (256, 128, 65536)):
+            need = sg.sgemm_linear_workspace_bytes(ta, tb, M, N, K)
+            st, plan = sg.sgemm_linear_plan_query(ta, tb, M, N, K, need)
+            assert st == sg.OK and plan.splits > 1
+            assert plan.workspace_bytes == need == plan.splits * M * N * 4
+            assert sg.sgemm_linear_plan_query(ta, tb, M, N, K, 1 << 40)[1].as_dict() \
+                == plan.as_dict()
+            less = sg.sgemm_linear_plan_query(ta, tb, M, N, K, need - 4)[1]
+            assert less.workspace_bytes <= need - 4
+            assert sg.sgemm_linear_plan_query(ta, tb, M, N, K)[1].splits == 1
+    for args in ((0, 0, 4096, 4096, 4096), (0, 1, 1, 4096, 4096), (0, 0, 256, 256, 0)):
+        assert sg.sgemm_linear_workspace_bytes(*args) == 0
+
+
+def test_plan_query_refuses(lib):
+    for args in ((2, 0, 4, 4, 4), (0, 0, -1, 4, 4), (0, 0, 4, 4, 4, -1)):
+        assert sg.sgemm_linear_plan_query(*args)[0] == sg.ERR_INVALID_ARG
+    assert sg.sgemm_linear_plan_query(0, 0, (1 << 31) - 1023, 4, 4)[0] == sg.ERR_UNSUPPORTED
+    assert lib.sgemm_linear_plan_query(0, 0, 4, 4, 4, 0, None) == sg.ERR_INVALID_ARG
+    assert sg.sgemm_linear_plan_query(0, 0, 0, 4, 4)[0] == sg.OK
+
+
+# Refusals (CPU).
+
+BIG = 1 << 33
 
 
 def test_the_headers_declare_the_binding_names(lib):
@@ -380,7 +490,10 @@ def test_linear_refuses(lib, args):
 
 @pytest.mark.parametrize("args", [
     dict(M=(1 << 31) - 1023, C=FAR * 2, B=FAR), dict(K=(1 << 31) - 1023, C=FAR, B=FAR * 2),
-    dict(lda=1 << 62)])
+    dict(lda=1 << 62), dict(K=1 << 29, ldb=8, B=FAR, C=FAR * 2),
+    dict(M=64, lda=1 << 25, B=FAR, C=FAR * 2), dict(M=64, N=64, K=64, ldb=1 << 26, B=FAR, C=FAR * 2),
+    dict(M=64, ldc=1 << 26, B=FAR, C=FAR * 2), dict(M=64, residual=FAR * 3, ldr=1 << 26),
+    dict(M=64, preact=FAR * 3, ldp=1 << 26), dict(ldb=1 << 29, B=FAR, C=FAR * 2)])
 def test_linear_unsupported(lib, args):
     assert call(**args) == sg.ERR_UNSUPPORTED
 

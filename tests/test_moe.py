@@ -256,6 +256,57 @@ def test_grouped_integers_are_exact_and_the_same_every_time(tb):
 
 
 @pytest.mark.gpu
+def test_moves_past_32_bits():
+    g = gen(12)
+    T, top, H = 310000, 4, 1000
+    ids = torch.randint(-1, 20, (T, top), device="cuda", generator=g)
+    offsets, order, place = sg.moe_sort(ids, 20)
+    kept = int(offsets[-1])
+    X = torch.randn(T, H, device="cuda", generator=g)
+    xp = sg.moe_permute(X, place, out=torch.zeros(T * top, H, device="cuda"))
+    for s in (slice(0, 5000), slice(kept - 5000, kept)):
+        assert torch.equal(xp[s], X[order[s].long() // top])
+    assert (xp[kept:] == 0).all()
+    w = torch.rand(T, top, device="cuda", generator=g)
+    y = sg.moe_unpermute(xp, place, w)
+    ws = (w * (place >= 0)).double().sum(1, keepdim=True)
+    for s in (slice(0, 5000), slice(T - 5000, T)):
+        want = ws[s] * X[s].double()
+        assert ((y[s].double() - want).abs() <= (top + 1) * U * want.abs()).all()
+    dyp, dw = sg.moe_unpermute_backward(X, xp, place, w, out=xp)
+    for s in (slice(0, 5000), slice(kept - 5000, kept)):
+        c = order[s].long()
+        assert torch.equal(dyp[s], w.reshape(-1)[c][:, None] * X[c // top])
+    for s in (slice(0, 5000), slice(T - 5000, T)):
+        size = X[s].double().square().sum(1, keepdim=True)
+        want = size * (place[s] >= 0)
+        assert ((dw[s].double() - want).abs() <= sum_tol(H) * size).all()
+
+
+@pytest.mark.gpu
+def test_a_stack_of_matrices_past_32_bits():
+    g = gen(14)
+    E, K, N = 300, 1900, 2000
+    B = torch.randn(E, K, N, device="cuda", generator=g)     # 4.5 GB
+    for per in (1, 40):
+        counts = [0] * E
+        for e in (0, 1, 150, 298, 299):
+            counts[e] = per
+        offsets, M = offsets_of(counts), 5 * per
+        A, dC = torch.randn(M, K, device="cuda", generator=g), torch.randn(M, N, device="cuda",
+                                                                           generator=g)
+        C = sg.grouped_linear(A, B, offsets)
+        dA, dB, _ = sg.grouped_linear_backward(dC, A, B, offsets)
+        for i, e in enumerate((0, 1, 150, 298, 299)):
+            s = slice(i * per, (i + 1) * per)
+            a, b, d = A[s].double(), B[e].double(), dC[s].double()
+            assert ((C[s].double() - a @ b).abs() <= 1e-5 * (a.abs() @ b.abs())).all()
+            assert ((dA[s].double() - d @ b.t()).abs() <= 1e-5 * (d.abs() @ b.t().abs())).all()
+            assert ((dB[e].double() - a.t() @ d).abs() <= 1e-5 * (a.t().abs() @ d.abs())).all()
+        assert (dB[2:150] == 0).all() and (dB[151:298] == 0).all()
+
+
+@pytest.mark.gpu
 def test_bad_offsets_stay_inside_the_operands():
     """Offsets past the rows, negative or falling: clamped, so the rows they
     still describe are right and nothing outside is touched."""

@@ -620,7 +620,7 @@ product_kernel(ProductArgs g) {
         if (pre) {
           const int row = row_of(i, it * RPI + ln / LPR);
           if (row < m_left && cols > 0)
-            store_upto(pre + (uint32_t)row * (uint32_t)g.ldp + (uint32_t)(wn0 + col), cols, z);
+            store_upto_once(pre + (uint32_t)row * (uint32_t)g.ldp + (uint32_t)(wn0 + col), cols, z);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) z[e] = activate(act, z[e]);
@@ -634,7 +634,9 @@ product_kernel(ProductArgs g) {
         f32x4 v = mine[it * 64];
         if (!through) v += bias;
         if (res) v += add[it];
-        store_upto(out + (uint32_t)row * (uint32_t)ld_out + (uint32_t)(wn0 + col), cols, v);
+        float* const p = out + (uint32_t)row * (uint32_t)ld_out + (uint32_t)(wn0 + col);
+        if (partial) store_upto(p, cols, v);
+        else store_upto_once(p, cols, v);
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");

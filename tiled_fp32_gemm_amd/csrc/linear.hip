@@ -267,7 +267,9 @@ struct RowsChoice {
 RowsChoice choose_rows(const Product& p) {
   const ProductArgs& g = p.g;
   RowsChoice none = {0, 0, 0};
-  if (p.trans_a || g.mode == sg::kSumGroups) return none;
+  // The kernels count k in ints, some way past K; a row that long is refused by
+  // product_kernel's spans as well.
+  if (p.trans_a || g.mode == sg::kSumGroups || g.K >= 1 << 29) return none;
   const bool grouped = g.mode == sg::kRowGroups;
   const int64_t live = grouped ? live_groups(g) : 1;
   const int64_t most = grouped ? 4 * live : p.trans_b ? 2 * sg::kRowsMost : sg::kRowsMost;
@@ -287,12 +289,19 @@ RowsChoice choose_rows(const Product& p) {
   return grid_fits(ch.workgroups, 256) ? ch : none;
 }
 
-// Few columns over a long K x N matrix leave the chip idle, where a split
-// product fills it: 1 x 1024 x 8192 takes 18.2 us by rows and 14.5 us split,
-// at K = 1024 it is 4.5 and 9.0.
+// Few columns over a long K leave the chip idle by rows, where a split product
+// fills it.  Measured (us, rows / split; N x K):
+//      B stored N x K   64 x 65536   64 x 16384   1024 x 8192
+//      1 row             17.5 / 27.4    5.1 / 12.6    7.3 / 12.9
+//      8 rows            40.4 / 27.4   10.8 / 13.3    9.7 / 12.9
+//      B stored K x N   64 x 16384   256 x 4096   1024 x 8192   1024 x 1024
+//      1 row             25.2 / 13.1    6.1 / 9.3    18.2 / 12.9    4.5 / 9.0
+//      8 rows            58.2 / 13.3   13.0 / 9.8    28.8 / 12.9    5.5 / 9.2
 bool rather_split(const Product& p, const RowsChoice& rows, const Choice& ch) {
-  return !p.trans_b && ch.v != nullptr && ch.splits > 1 && p.g.K > 4096 &&
-         rows.workgroups < kCUs / 2;
+  if (ch.v == nullptr || ch.splits == 1) return false;
+  const int64_t K = p.g.K;
+  return p.trans_b ? rows.workgroups < 64 && K * rows.rows > 196608
+                   : rows.workgroups <= kCUs / 2 && K * (rows.rows + 2) > 12288;
 }
 
 int run_product(Product& p, const int32_t* offsets, hipStream_t stream, void* ws,
@@ -300,8 +309,8 @@ int run_product(Product& p, const int32_t* offsets, hipStream_t stream, void* ws
   ProductArgs& g = p.g;
   const RowsChoice rows = choose_rows(p);
   Choice ch = {nullptr, 1, 0, 0};
-  // Only a long K asks what a split would be.
-  if (rows.rows == 0 || g.K > 4096) ch = choose(p, ws_bytes);
+  // Only a long K over few columns asks what a split would be.
+  if (rows.rows == 0 || (g.K > 1024 && rows.workgroups <= kCUs / 2)) ch = choose(p, ws_bytes);
   if (rows.rows > 0 && !rather_split(p, rows, ch)) {
     g.tiles_m = (int)cdiv(g.M, rows.rows);
     g.tiles_n = (int)cdiv(g.N, rows.cols);

@@ -202,6 +202,18 @@ int64_t likely_tiles(const ProductArgs& g, const sg::host::TileCost& c) {
   return (rows > live ? rows : live) * cdiv(g.N, c.tile_n);
 }
 
+// Estimated seconds of `tiles` workgroups over K.  The tiles of row groups differ
+// and are handed out as workgroups end, so a last round that is partly filled
+// counts in part (and a third of a tile more, for its uneven end).
+double likely_time(const ProductArgs& g, const sg::host::TileCost& c, int64_t tiles, int64_t K) {
+  const double t = estimate_grid(c, tiles, K);
+  const int64_t full = tiles / kCUs, rest = tiles % kCUs;
+  if (g.mode != sg::kRowGroups || full == 0 || rest == 0) return t;
+  const double part = (double)rest / kCUs + 0.3;
+  const double less = estimate_grid(c, full * kCUs, K);
+  return part >= 1.0 ? t : less + part * (t - less);
+}
+
 // The variant, and the split of K, with the least estimated time (the model
 // of host.hpp; the costs of a split are those sgemm_ws was fitted with).  A
 // null v: no variant can address this product.
@@ -219,7 +231,7 @@ Choice choose(const Product& p, int64_t ws_bytes) {
     const sg::host::TileCost& c = v.cost;
     const int64_t grid = grid_tiles(g, c), likely = likely_tiles(g, c);
     if (!variant_fits(p, v) || !grid_fits(grid, c.threads)) continue;
-    const double t = estimate_grid(c, likely, K);
+    const double t = likely_time(g, c, likely, K);
     if (one.v == nullptr || t < t_one * 0.995) {
       one = {&v, 1, 0, grid};
       t_one = t;
@@ -232,7 +244,7 @@ Choice choose(const Product& p, int64_t ws_bytes) {
           !grid_fits(out / g.N * cdiv(g.N, sg::kProductReduceCols),
                      64))
         continue;
-      const double ts = 0.95 * estimate_grid(c, likely * se, ks) + 3.0e-6 +
+      const double ts = 0.95 * likely_time(g, c, likely * se, ks) + 3.0e-6 +
                         (double)(se + 1) * out * 4.0 / 5.0e12;
       if (split.v == nullptr || ts < t_split) {
         split = {&v, (int)se, (int)ks, grid * se};

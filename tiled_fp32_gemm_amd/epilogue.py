@@ -265,20 +265,38 @@ def linear_backward(dC, A, B, activation="none", preact=None, *, transpose_a=Fal
     ``bias_grad``.  ``preact`` is what ``linear`` stored (not needed for
     activation "none").  The residual's gradient is ``dC``.
     """
+    act = _act(activation)
     dev = _device(dC, "dC")
-    M, N, _, _, _ = _inner(A, B, dev, transpose_a, transpose_b)
-    _sized(dC, "dC", dev, M, N)
+    M, N, K, lda, ldb = _inner(A, B, dev, transpose_a, transpose_b)
+    lddz = _sized(dC, "dC", dev, M, N)
+    if act:
+        if preact is None:
+            raise ValueError(f"activation {activation!r} needs preact")
+        _sized(preact, "preact", dev, M, N)
+    room, size = _workspace(workspace, dev)
+    ta, tb = bool(transpose_a), bool(transpose_b)
 
-    def call(_):   # dZ, when it is made here, belongs to the stream
-        dZ, dbias = activation_backward(dC, activation, preact, bias_grad=bias_grad,
-                                        workspace=workspace)
-        if transpose_a:
-            dA = linear(B, dZ, transpose_a=transpose_b, transpose_b=True, workspace=workspace)
+    def call(s):   # dZ, when it is made here, belongs to the stream
+        dz, dbias, ld = dC, None, lddz
+        if act or bias_grad:
+            dz, dbias = activation_backward(dC, activation, preact, bias_grad=bias_grad,
+                                            workspace=workspace)
+            ld = max(N, 1) if act else lddz
+        dA, dB = _empty(dev, *A.shape), _empty(dev, *B.shape)
+        a, b, d = (A.data_ptr(), lda), (B.data_ptr(), ldb), (dz.data_ptr(), ld)
+        sgemm_linear = sg.load().sgemm_linear
+
+        def product(out, left, trans_left, right, trans_right, m, n, k):
+            _check(sgemm_linear(trans_left, trans_right, m, n, k, *left, *right, out.data_ptr(),
+                                max(n, 1), None, s, room, size), "sgemm_linear")
+        # d op(A) = dZ op(B)^T and d op(B) = op(A)^T dZ, transposed where A and B are
+        if ta:
+            product(dA, b, tb, d, True, K, M, N)
         else:
-            dA = linear(dZ, B, transpose_b=not transpose_b, workspace=workspace)
-        if transpose_b:
-            dB = linear(dZ, A, transpose_a=True, transpose_b=transpose_a, workspace=workspace)
+            product(dA, d, False, b, not tb, M, K, N)
+        if tb:
+            product(dB, d, True, a, ta, N, K, M)
         else:
-            dB = linear(A, dZ, transpose_a=not transpose_a, workspace=workspace)
+            product(dB, a, not ta, d, False, K, N, M)
         return dA, dB, dbias
     return _on(dev, stream, call)

@@ -240,7 +240,7 @@ def grouped_linear_backward(dC, A, B, offsets, activation="none", preact=None, *
     group without rows.  The residual's gradient is ``dC``."""
     act = _act(activation)
     dev = _device(dC, "dC")
-    M, N, K, G, lda, _, _, off = _groups(A, B, offsets, dev, transpose_b)
+    M, N, K, G, lda, ldb, stride, off = _groups(A, B, offsets, dev, transpose_b)
     lddc = _sized(dC, "dC", dev, M, N)
     z, ldz = 0, 1
     if act:
@@ -258,8 +258,10 @@ def grouped_linear_backward(dC, A, B, offsets, activation="none", preact=None, *
             M, N, G, off, dC.data_ptr(), lddc, z, ldz, act, dZ.data_ptr() if act else None, lddz,
             dbias.data_ptr() if bias_grad else None, max(N, 1), s, ws, ws_bytes),
             "sgemm_grouped_act_backward")
-        dA = grouped_linear(dZ, B, offsets, transpose_b=not transpose_b, workspace=workspace)
-        dB = _empty(dev, *B.shape)
+        dA, dB = _empty(dev, M, K), _empty(dev, *B.shape)
+        _check(lib.sgemm_grouped(not transpose_b, M, K, N, G, off, dZ.data_ptr(), lddz,
+                                 B.data_ptr(), ldb, stride, dA.data_ptr(), max(K, 1), None, s, ws,
+                                 ws_bytes), "sgemm_grouped")
         r, c = B.shape[1:]
         _check(lib.sgemm_grouped_wgrad(
             bool(transpose_b), M, N, K, G, off, A.data_ptr(), lda, dZ.data_ptr(), lddz,

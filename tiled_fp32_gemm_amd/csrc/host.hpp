@@ -57,6 +57,8 @@ constexpr double kSaturate = 1.28;   // waves per SIMD that keep the pipes busy
 constexpr double kSlabFloor = 0.61e-6;  // s: a slab's wait for its loads
 constexpr double kRoundCost = 4.4e-6;   // s: fill and drain of one round
 constexpr double kWriteBW = 4.52e12;    // B/s: C stores of a final round
+constexpr double kReduceFixed = 3.0e-6;  // s: the second launch of a split product
+constexpr double kReduceBW = 5.0e12;     // B/s, a device copy's rate
 
 
 // What the time model needs to know of a tile variant.

@@ -228,24 +228,29 @@ Choice choose(const Product& p, int64_t ws_bytes) {
   static const int kSplits[] = {2, 3, 4, 6, 8, 12, 16, 24, 32};
   for (int i = 0; i < sg::kProductVariants; ++i) {
     const ProductVariant& v = table[i];
-    const sg::host::TileCost& c = v.cost;
-    const int64_t grid = grid_tiles(g, c), likely = likely_tiles(g, c);
-    if (!variant_fits(p, v) || !grid_fits(grid, c.threads)) continue;
-    const double t = likely_time(g, c, likely, K);
+    const int64_t grid = grid_tiles(g, v.cost);
+    if (!variant_fits(p, v) || !grid_fits(grid, v.cost.threads)) continue;
+    const double t = likely_time(g, v.cost, likely_tiles(g, v.cost), K);
     if (one.v == nullptr || t < t_one * 0.995) {
       one = {&v, 1, 0, grid};
       t_one = t;
     }
+  }
+  // A split takes the fixed costs of a round and of a second launch at least.
+  if (one.v == nullptr || t_one < kRoundCost + kReduceFixed || 2 * out > ws_bytes / 4) return one;
+  for (int i = 0; i < sg::kProductVariants; ++i) {
+    const ProductVariant& v = table[i];
+    const sg::host::TileCost& c = v.cost;
+    const int64_t grid = grid_tiles(g, c), likely = likely_tiles(g, c);
+    if (K < 2 * c.tile_k || !variant_fits(p, v)) continue;
     for (int S : kSplits) {
       const int64_t ks = cdiv(cdiv(K, S), c.tile_k) * c.tile_k;
       const int64_t se = g.mode == sg::kSumGroups ? S : cdiv(K, ks);
-      if (se < 2 || K < 2 * c.tile_k || se * out > ws_bytes / 4 ||
-          !grid_fits(grid * se, c.threads) ||
-          !grid_fits(out / g.N * cdiv(g.N, sg::kProductReduceCols),
-                     64))
+      if (se < 2 || se * out > ws_bytes / 4 || !grid_fits(grid * se, c.threads) ||
+          !grid_fits(out / g.N * cdiv(g.N, sg::kProductReduceCols), 64))
         continue;
-      const double ts = 0.95 * likely_time(g, c, likely * se, ks) + 3.0e-6 +
-                        (double)(se + 1) * out * 4.0 / 5.0e12;
+      const double ts = 0.95 * likely_time(g, c, likely * se, ks) + kReduceFixed +
+                        (double)(se + 1) * out * 4.0 / kReduceBW;
       if (split.v == nullptr || ts < t_split) {
         split = {&v, (int)se, (int)ks, grid * se};
         t_split = ts;

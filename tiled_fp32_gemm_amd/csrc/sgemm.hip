@@ -200,8 +200,6 @@ const Candidate* choose_mfma(int64_t M, int64_t N, int64_t K, int64_t lda,
 // second pass adds them in split order.  Its cost: the partial products
 // (the model above, on tiles x S workgroups of depth k_split), plus the
 // reduction's (S + 1) M N 4 bytes at HBM speed and its launch.
-constexpr double kReduceFixed = 3.0e-6;  // s
-constexpr double kReduceBW = 5.0e12;     // B/s, a device copy's rate
 constexpr double kSplitMargin = 0.97;    // split only when clearly faster
 // The model over-states the partial pass, whose workgroups see short K and
 // fill the CUs evenly; scaled by this (one value, chosen on timings of every

@@ -130,7 +130,8 @@ def _sized(t, name: str, dev: int, rows: int, cols: int) -> int:
 
 def _vector(t, name: str, dev: int, n: int) -> int:
     """The address of n floats with unit stride."""
-    if _float(t, name, dev).shape != (n,) or (n > 1 and t.stride(0) != 1):
+    _float(t, name, dev)
+    if t.dim() != 1 or t.numel() != n or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be 1-D of {n} with unit stride")
     return t.data_ptr()
 
@@ -148,15 +149,11 @@ def _workspace(workspace, dev: int) -> tuple[int, int]:
     return (workspace.data_ptr(), n) if n else (0, 0)
 
 
-def _empty(dev: int, *shape, dtype=None):
-    return torch.empty(shape, dtype=dtype or torch.float32, device=dev)
-
-
 def _on(dev: int, stream, body):
     """``body(handle)`` with GPU `dev` current and `stream` (default: its
     current one) the stream that tensors made inside belong to."""
     if stream is None:
-        if torch.cuda.current_device() == dev:
+        if torch._C._cuda_getDevice() == dev:
             return body(torch._C._cuda_getCurrentRawStream(dev))
         with torch.cuda.device(dev):
             return body(torch._C._cuda_getCurrentRawStream(dev))
@@ -217,7 +214,7 @@ def linear(A, B, bias=None, activation="none", residual=None, *, transpose_a=Fal
     ldc = max(N, 1) if out is None else _sized(out, "out", dev, M, N)
 
     def call(s):
-        c = _empty(dev, M, N) if out is None else out
+        c = A.new_empty(M, N) if out is None else out
         st = sg.load().sgemm_linear(bool(transpose_a), bool(transpose_b), M, N, K, A.data_ptr(),
                                     lda, B.data_ptr(), ldb, c.data_ptr(), ldc, epilogue, s, ws,
                                     ws_bytes)
@@ -247,8 +244,8 @@ def activation_backward(dC, activation="none", preact=None, *, bias_grad=True, o
     ws, ws_bytes = _workspace(workspace, dev)
 
     def call(s):
-        dz = _empty(dev, M, N) if out is None and act else out
-        dbias = _empty(dev, N) if bias_grad else None
+        dz = dC.new_empty(M, N) if out is None and act else out
+        dbias = dC.new_empty(N) if bias_grad else None
         st = sg.load().sgemm_act_backward(M, N, dC.data_ptr(), lddc, z, ldz, act,
                                           None if dz is None else dz.data_ptr(), lddz,
                                           dbias.data_ptr() if bias_grad else None, s, ws,
@@ -282,7 +279,7 @@ def linear_backward(dC, A, B, activation="none", preact=None, *, transpose_a=Fal
             dz, dbias = activation_backward(dC, activation, preact, bias_grad=bias_grad,
                                             workspace=workspace)
             ld = max(N, 1) if act else lddz
-        dA, dB = _empty(dev, *A.shape), _empty(dev, *B.shape)
+        dA, dB = A.new_empty(A.shape), B.new_empty(B.shape)
         a, b, d = (A.data_ptr(), lda), (B.data_ptr(), ldb), (dz.data_ptr(), ld)
         sgemm_linear = sg.load().sgemm_linear
 

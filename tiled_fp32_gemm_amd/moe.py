@@ -19,8 +19,8 @@ import torch
 
 import tiled_fp32_gemm_amd as sg
 
-from .epilogue import (Epilogue, _act, _check, _device, _empty, _epilogue, _float, _matrix, _on,
-                       _sized, _workspace)
+from .epilogue import (Epilogue, _act, _check, _device, _epilogue, _float, _matrix, _on, _sized,
+                       _workspace)
 
 MOE_SYMBOLS = ("sgemm_moe_sort", "sgemm_moe_sort_workspace_bytes", "sgemm_moe_permute",
                "sgemm_moe_unpermute", "sgemm_moe_unpermute_backward", "sgemm_grouped",
@@ -117,11 +117,11 @@ def moe_sort(experts, num_experts, *, stream=None, workspace=None):
     def call(s):
         room, size = ws, ws_bytes
         if need:
-            own = _empty(dev, need, dtype=torch.uint8)
+            own = experts.new_empty(need, dtype=torch.uint8)
             room, size = own.data_ptr(), need
-        offsets = _empty(dev, E + 1, dtype=torch.int32)
-        order = _empty(dev, n, dtype=torch.int32)
-        place = _empty(dev, *experts.shape, dtype=torch.int32)
+        offsets = experts.new_empty(E + 1, dtype=torch.int32)
+        order = experts.new_empty(n, dtype=torch.int32)
+        place = experts.new_empty(experts.shape, dtype=torch.int32)
         st = lib.sgemm_moe_sort(n, E, experts.data_ptr(), experts.element_size(),
                                 offsets.data_ptr(), order.data_ptr(), place.data_ptr(), s, room,
                                 size)
@@ -141,7 +141,7 @@ def moe_permute(X, place, *, out=None, stream=None):
     ld = max(H, 1) if out is None else _sized(out, "out", dev, T * top, H)
 
     def call(s):
-        xp = _empty(dev, T * top, H) if out is None else out
+        xp = X.new_empty(T * top, H) if out is None else out
         _check(sg.load().sgemm_moe_permute(T, top, H, X.data_ptr(), ldx, p, xp.data_ptr(), ld, s),
                "sgemm_moe_permute")
         return xp
@@ -160,7 +160,7 @@ def moe_unpermute(Yp, place, weights=None, *, out=None, stream=None):
     ld = max(H, 1) if out is None else _sized(out, "out", dev, T, H)
 
     def call(s):
-        y = _empty(dev, T, H) if out is None else out
+        y = Yp.new_empty(T, H) if out is None else out
         _check(sg.load().sgemm_moe_unpermute(T, top, H, Yp.data_ptr(), ldyp, p, w, y.data_ptr(),
                                              ld, s), "sgemm_moe_unpermute")
         return y
@@ -180,8 +180,8 @@ def moe_unpermute_backward(dY, Yp, place, weights=None, *, out=None, stream=None
     ld = max(H, 1) if out is None else _sized(out, "out", dev, T * top, H)
 
     def call(s):
-        dyp = _empty(dev, T * top, H) if out is None else out
-        dw = _empty(dev, T, top)
+        dyp = dY.new_empty(T * top, H) if out is None else out
+        dw = dY.new_empty(T, top)
         _check(sg.load().sgemm_moe_unpermute_backward(
             T, top, H, dY.data_ptr(), lddy, Yp.data_ptr(), ldyp, p, w, dyp.data_ptr(), ld,
             dw.data_ptr(), s), "sgemm_moe_unpermute_backward")
@@ -225,7 +225,7 @@ def grouped_linear(A, B, offsets, bias=None, activation="none", residual=None, *
     ldc = max(N, 1) if out is None else _sized(out, "out", dev, M, N)
 
     def call(s):
-        c = _empty(dev, M, N) if out is None else out
+        c = A.new_empty(M, N) if out is None else out
         _check(sg.load().sgemm_grouped(bool(transpose_b), M, N, K, G, off, A.data_ptr(), lda,
                                        B.data_ptr(), ldb, stride, c.data_ptr(), ldc, epilogue, s,
                                        ws, ws_bytes), "sgemm_grouped")
@@ -252,13 +252,13 @@ def grouped_linear_backward(dC, A, B, offsets, activation="none", preact=None, *
     lib = sg.load()
 
     def call(s):
-        dZ, lddz = (_empty(dev, M, N), max(N, 1)) if act else (dC, lddc)
-        dbias = _empty(dev, G, N) if bias_grad else None
+        dZ, lddz = (dC.new_empty(M, N), max(N, 1)) if act else (dC, lddc)
+        dbias = dC.new_empty(G, N) if bias_grad else None
         _check(lib.sgemm_grouped_act_backward(
             M, N, G, off, dC.data_ptr(), lddc, z, ldz, act, dZ.data_ptr() if act else None, lddz,
             dbias.data_ptr() if bias_grad else None, max(N, 1), s, ws, ws_bytes),
             "sgemm_grouped_act_backward")
-        dA, dB = _empty(dev, M, K), _empty(dev, *B.shape)
+        dA, dB = A.new_empty(M, K), B.new_empty(B.shape)
         _check(lib.sgemm_grouped(not transpose_b, M, K, N, G, off, dZ.data_ptr(), lddz,
                                  B.data_ptr(), ldb, stride, dA.data_ptr(), max(K, 1), None, s, ws,
                                  ws_bytes), "sgemm_grouped")

@@ -362,6 +362,21 @@ def test_offsets_past_32_bits():
 
 
 @pytest.mark.gpu
+def test_a_single_row_has_no_leading_dimension():
+    g = gen(23)
+    far, s = 1 << 40, torch.cuda.current_stream().cuda_stream
+    for M, N, K, lda, ldb, ldc in ((1, 70, 90, far, 70, far), (50, 70, 1, 1, far, 70),
+                                   (300, 200, 1, 1, far, 200)):
+        A, B = torch.randn(M, K, device="cuda", generator=g), torch.randn(K, N, device="cuda",
+                                                                          generator=g)
+        C = torch.empty(M, N, device="cuda")
+        assert sg.sgemm_linear(0, 0, M, N, K, A.data_ptr(), lda, B.data_ptr(), ldb, C.data_ptr(),
+                               ldc, None, s) == sg.OK
+        a, b = A.double(), B.double()
+        assert ((C.double() - a @ b).abs() <= sum_tol(K) * (a.abs() @ b.abs())).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("off", [0, 1, 2, 3])
 @pytest.mark.parametrize("M,N,K", [(3, 37, 70), (40, 37, 70), (70, 131, 64)])
 def test_every_alignment(off, M, N, K):
@@ -386,6 +401,41 @@ def test_non_finite_values_stay_in_their_rows_and_columns():
             keep[M // 2], keep[:, N // 3] = False, False
             tol = 2 * sum_tol(K) * (A.nan_to_num(0).abs() @ B.nan_to_num(0, 0, 0).abs())
             assert ((C - clean).abs()[keep] <= tol[keep]).all()
+
+
+@pytest.mark.gpu
+def test_two_graphs_share_a_workspace_and_two_streams_have_their_own():
+    g = gen(29)
+    shapes = [(256, 256, 4096), (64, 300, 8000)]
+    ins = [(torch.randn(M, K, device="cuda", generator=g),
+            torch.randn(K, N, device="cuda", generator=g)) for M, N, K in shapes]
+    shared = torch.empty(1 << 22, device="cuda")
+    for (A, B), (M, N, K) in zip(ins, shapes):
+        assert sg.sgemm_linear_plan_query(0, 0, M, N, K, 1 << 24)[1].splits > 1
+    want = [sg.linear(A, B, None, "gelu", workspace=shared) for A, B in ins]
+    graphs, outs = [], []
+    for A, B in ins:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(sg.linear(A, B, None, "gelu", workspace=shared))
+    for rep in range(4):
+        for o in outs:
+            o.fill_(float("nan"))
+        for i in ((0, 1), (1, 0))[rep % 2]:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w), rep
+    streams = [torch.cuda.Stream() for _ in ins]
+    rooms = [torch.empty(1 << 22, device="cuda") for _ in ins]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for (A, B), s, ws in zip(ins, streams, rooms):
+            got.append(sg.linear(A, B, None, "gelu", stream=s, workspace=ws))
+    torch.cuda.synchronize()
+    for i, o in enumerate(got):
+        assert torch.equal(o, want[i % 2])
 
 
 # Plans (CPU).
@@ -492,9 +542,10 @@ def test_linear_refuses(lib, args):
 @pytest.mark.parametrize("args", [
     dict(M=(1 << 31) - 1023, C=FAR * 2, B=FAR), dict(K=(1 << 31) - 1023, C=FAR, B=FAR * 2),
     dict(lda=1 << 62), dict(K=1 << 29, ldb=8, B=FAR, C=FAR * 2),
-    dict(M=64, lda=1 << 25, B=FAR, C=FAR * 2), dict(M=64, N=64, K=64, ldb=1 << 26, B=FAR, C=FAR * 2),
+    dict(M=64, lda=1 << 25, B=FAR, C=FAR * 2),
+    dict(M=64, N=64, K=64, ldb=1 << 26, B=FAR, C=FAR * 2),
     dict(M=64, ldc=1 << 26, B=FAR, C=FAR * 2), dict(M=64, residual=FAR * 3, ldr=1 << 26),
-    dict(M=64, preact=FAR * 3, ldp=1 << 26), dict(ldb=1 << 29, B=FAR, C=FAR * 2)])
+    dict(M=64, preact=FAR * 3, ldp=1 << 26), dict(ldb=1 << 31, B=FAR, C=FAR * 2)])
 def test_linear_unsupported(lib, args):
     assert call(**args) == sg.ERR_UNSUPPORTED
 
@@ -553,7 +604,8 @@ def test_the_binding_refuses_bad_tensors():
            lambda: sg.linear(A, B, preact=f(3, 8)), lambda: sg.linear(A, B, out=f(8, 4).t()),
            lambda: sg.linear(A, B, out=f(4, 7)), lambda: sg.linear(A, B, workspace=f(4, 8).t()),
            lambda: sg.linear(A, B, workspace=torch.zeros(4)),
-           lambda: sg.linear_backward(f(4, 7), A, B), lambda: sg.linear_backward(f(4, 8), A, B, "silu"),
+           lambda: sg.linear_backward(f(4, 7), A, B),
+           lambda: sg.linear_backward(f(4, 8), A, B, "silu"),
            lambda: sg.linear_backward(f(4, 8), A, B, "silu", f(4, 9))]
     for call_ in bad:
         with pytest.raises(ValueError):

@@ -16,6 +16,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "../../include/sgemm_linear.h"
 
 namespace sg {
@@ -72,7 +74,8 @@ __device__ __forceinline__ float finite(float z) {
 // The same for the lower tail only.
 __device__ __forceinline__ float above(float z) { return fmaxf(z, -1.0e18f); }
 
-__device__ __forceinline__ float activate(int act, float z) {
+template <int act>
+__device__ __forceinline__ float activate(float z) {
   if (act == SGEMM_ACT_RELU) return z <= 0.0f ? 0.0f : z;   // NaN stays NaN
   if (act == SGEMM_ACT_GELU) {
     float bell;
@@ -84,7 +87,8 @@ __device__ __forceinline__ float activate(int act, float z) {
   return z;
 }
 
-__device__ __forceinline__ float activation_slope(int act, float z) {
+template <int act>
+__device__ __forceinline__ float activation_slope(float z) {
   if (act == SGEMM_ACT_RELU) return z <= 0.0f ? 0.0f : (z > 0.0f ? 1.0f : z);
   if (act == SGEMM_ACT_GELU) {
     float bell;
@@ -105,6 +109,19 @@ __device__ __forceinline__ float activation_slope(int act, float z) {
     return s * fmaf(finite(z), rest, 1.0f);
   }
   return 1.0f;
+}
+
+// f(integral_constant<int, act>): a loop for each activation, rather than a
+// choice for each element.
+template <class F>
+__device__ __forceinline__ void with_activation(int act, F f) {
+  switch (act) {
+    case SGEMM_ACT_RELU: f(std::integral_constant<int, SGEMM_ACT_RELU>()); break;
+    case SGEMM_ACT_GELU: f(std::integral_constant<int, SGEMM_ACT_GELU>()); break;
+    case SGEMM_ACT_GELU_TANH: f(std::integral_constant<int, SGEMM_ACT_GELU_TANH>()); break;
+    case SGEMM_ACT_SILU: f(std::integral_constant<int, SGEMM_ACT_SILU>()); break;
+    default: f(std::integral_constant<int, SGEMM_ACT_NONE>());
+  }
 }
 
 }  // namespace sg

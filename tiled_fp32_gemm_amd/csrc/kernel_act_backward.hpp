@@ -6,7 +6,9 @@
 // side in a wave (lpr lanes a row).  The sums are added through LDS in a fixed
 // order and go to the strip's row of W, or straight to the result when a group
 // is one strip; column_sum_kernel adds the strips in a fixed order.  Bound by
-// HBM: dC and Z are read once and dZ is written once.
+// HBM: dC and Z are read once and dZ is written once.  Measured on MI355X with
+// SILU or GELU: 65536 x 128 in 19.4 us (5.2 TB/s), 4096 x 4096 in 45 us
+// (4.5 TB/s), and 4.7 us for the strips' sums.
 //
 // Loads and stores are 16 bytes at any 4-byte alignment (global, not buffer,
 // accesses); only a row's last one to three columns go one by one.
@@ -26,14 +28,14 @@ struct ActBackwardArgs {
   float* W;             // [strip][group][N], when strips > 1
   int64_t lddc, ldz, lddz, lddb;
   const int32_t* offsets;   // null: one group of all rows
-  int M, N, groups, strips, act;
+  int M, N, groups, strips;
   int lpr;              // lanes along a row: 1, 2, 4 .. 64
   int blocks_n;         // ceil(N / (4 lpr))
 };
 
 constexpr int kActWaves = 4;
 
-template <bool HAS_Z>
+template <int ACT>
 __global__ void __launch_bounds__(64 * kActWaves) act_backward_kernel(ActBackwardArgs a) {
   __shared__ f32x4 part[kActWaves * 64];
   const int lane = (int)threadIdx.x & 63;
@@ -58,16 +60,16 @@ __global__ void __launch_bounds__(64 * kActWaves) act_backward_kernel(ActBackwar
         const int64_t row = r + u * beside;
         if (row < r1) {
           d[u] = load_upto(a.dC + row * a.lddc + col, left);
-          if constexpr (HAS_Z) z[u] = load_upto(a.Z + row * a.ldz + col, left);
+          if constexpr (ACT != SGEMM_ACT_NONE) z[u] = load_upto(a.Z + row * a.ldz + col, left);
         }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t row = r + u * beside;
         if (row < r1) {
-          if constexpr (HAS_Z) {
+          if constexpr (ACT != SGEMM_ACT_NONE) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) d[u][e] *= activation_slope(a.act, z[u][e]);
+            for (int e = 0; e < 4; ++e) d[u][e] *= activation_slope<ACT>(z[u][e]);
           }
           if (a.dZ) store_upto(a.dZ + row * a.lddz + col, left, d[u]);
           sum += d[u];

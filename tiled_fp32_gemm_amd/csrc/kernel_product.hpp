@@ -2,9 +2,12 @@
 // transposed, an epilogue, and groups.
 //
 // The main loop is that of kernel_mfma_direct.hpp: slabs of BK values of k go
-// from global memory straight into LDS (two stages, one slab in flight), the
-// waves read their fragments one 8-deep chunk ahead of the 32x32x2 matrix
-// instructions, and the slab barrier sits before a slab's last chunk.  What is
+// from global memory straight into LDS (STAGES of them, all but one in flight),
+// the waves read their fragments one 8-deep chunk ahead of the 32x32x2 matrix
+// instructions, and the slab barrier sits before a slab's last chunk.  Bound by
+// the matrix pipe on full grids; measured on MI355X at 4096^3 (137.4 GFLOP,
+// 256 x 256 tiles): 914 us with A k fast and B k slow, 918 both fast, 916 both
+// slow, 916 the other way round, where sgemm takes 913 (150.5 TFLOP/s).  What is
 // new here:
 //
 // Operand layouts.  An operand is stored either with k running along its rows
@@ -33,8 +36,11 @@
 // wave in its own part, no barrier), so that bias, activation and residual are
 // applied four columns a lane in a short loop and every global access is 16
 // bytes a lane along a row.  The residual's loads are issued before the
-// activation runs, for small wave tiles before the main loop.  Split K (splits > 1) stores the partial sums instead;
-// kernel_product_reduce.hpp adds them and applies the epilogue.
+// activation runs, for small wave tiles before the main loop.  At 4096^3 a bias
+// costs 6 us, GELU 10, a residual 12, all of them and the stored
+// pre-activation 27 (192 MiB more to move).  Split K (splits > 1) stores the
+// partial sums instead; kernel_product_reduce.hpp adds them and applies the
+// epilogue.
 #pragma once
 
 #include <type_traits>
@@ -612,20 +618,23 @@ product_kernel(ProductArgs g) {
     // A bias alone is added with the residual.
     const bool through = act != SGEMM_ACT_NONE || pre;
     if (through) {
-      constexpr int kRounds = kEarly ? 2 : 1;
+      with_activation(act, [&](auto which) {
+        constexpr int kRounds = kEarly ? 2 : 1;
 #pragma unroll kRounds
-      for (int it = 0; it < IT; ++it) {
-        f32x4 z = mine[it * 64];
-        z += bias;
-        if (pre) {
-          const int row = row_of(i, it * RPI + ln / LPR);
-          if (row < m_left && cols > 0)
-            store_upto_once(pre + (uint32_t)row * (uint32_t)g.ldp + (uint32_t)(wn0 + col), cols, z);
-        }
+        for (int it = 0; it < IT; ++it) {
+          f32x4 z = mine[it * 64];
+          z += bias;
+          if (pre) {
+            const int row = row_of(i, it * RPI + ln / LPR);
+            if (row < m_left && cols > 0)
+              store_upto_once(pre + (uint32_t)row * (uint32_t)g.ldp + (uint32_t)(wn0 + col), cols,
+                              z);
+          }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[e] = activate(act, z[e]);
-        mine[it * 64] = z;
-      }
+          for (int e = 0; e < 4; ++e) z[e] = activate<decltype(which)::value>(z[e]);
+          mine[it * 64] = z;
+        }
+      });
     }
 #pragma unroll
     for (int it = 0; it < IT; ++it) {

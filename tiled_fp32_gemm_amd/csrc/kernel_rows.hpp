@@ -86,7 +86,7 @@ __device__ __forceinline__ void finish_one(const ProductArgs& g, const RowsPlace
   const int64_t row = p.row0 + r;
   if (g.bias) z += g.bias[p.group * g.ld_bias + col];
   if (g.preact) g.preact[row * g.ldp + col] = z;
-  z = activate(g.act, z);
+  with_activation(g.act, [&](auto which) { z = activate<decltype(which)::value>(z); });
   if (g.residual) z += g.residual[row * g.ldr + col];
   g.C[row * g.ldc + col] = z;
 }

@@ -43,6 +43,16 @@ bool overlaps(const Span& a, const Span& b) {
 
 int64_t at_least_one(int64_t n) { return n > 1 ? n : 1; }
 
+// Bytes of n floats; -1 where n is past any limit.
+int64_t floats(int64_t n) { return n > kMaxDim ? -1 : 4 * n; }
+
+// A leading dimension as the kernels take it: it only matters past the first
+// row.  -1: more than an int.
+int leading(int64_t rows, int64_t width, int64_t ld) {
+  const int64_t n = rows > 1 ? ld : at_least_one(width);
+  return n > INT32_MAX ? -1 : (int)n;
+}
+
 // Bytes of `groups` matrices of `one` bytes, `stride` floats apart.
 int64_t groups_bytes(int64_t groups, int64_t stride, int64_t one) {
   if (groups == 0 || one <= 0) return groups == 0 ? 0 : one;
@@ -90,8 +100,9 @@ int check_product(int mode, int ta, int tb, int64_t M, int64_t N, int64_t K, int
   p.c = {C, span_bytes(M, N, ldc)};
   p.res = {ep->residual, ep->residual ? span_bytes(M, N, ep->ldr) : 0};
   p.pre = {ep->preact, ep->preact ? span_bytes(M, N, ep->ldp) : 0};
-  p.bias = {ep->bias, !ep->bias ? 0 : mode == sg::kRowGroups
-                                          ? groups_bytes(groups, ep->ldbias, N * 4) : N * 4};
+  p.bias = {ep->bias, !ep->bias                ? 0
+                      : mode == sg::kRowGroups ? groups_bytes(groups, ep->ldbias, floats(N))
+                                               : floats(N)};
   if (mode == sg::kRowGroups) {
     if (p.b.bytes > 0 && groups > 1 && stride_b < p.b.bytes / 4) return SGEMM_ERR_INVALID_ARG;
     p.b.bytes = groups_bytes(groups, stride_b, p.b.bytes);
@@ -121,16 +132,16 @@ int check_product(int mode, int ta, int tb, int64_t M, int64_t N, int64_t K, int
   g.M = (int)M;
   g.N = (int)N;
   g.K = (int)K;
-  // A leading dimension only matters past the first row of an operand.
-  g.lda = (int)(ar > 1 ? lda : at_least_one(ac));
-  g.ldb = (int)(br > 1 ? ldb : at_least_one(bc));
-  g.ldc = (int)(M > 1 ? ldc : N);
+  g.lda = leading(K > 0 ? ar : 0, ac, lda);
+  g.ldb = leading(K > 0 ? br : 0, bc, ldb);
+  g.ldc = leading(M, N, ldc);
   g.bias = ep->bias;
   g.residual = ep->residual;
   g.preact = ep->preact;
   g.ld_bias = ep->ldbias;
-  g.ldr = (int)(M > 1 ? ep->ldr : N);
-  g.ldp = (int)(M > 1 ? ep->ldp : N);
+  g.ldr = ep->residual ? leading(M, N, ep->ldr) : 1;
+  g.ldp = ep->preact ? leading(M, N, ep->ldp) : 1;
+  if (g.lda < 0 || g.ldb < 0 || g.ldc < 0 || g.ldr < 0 || g.ldp < 0) return SGEMM_ERR_UNSUPPORTED;
   g.act = ep->act;
   g.mode = mode;
   g.groups = mode == sg::kDense ? 1 : (int)groups;
@@ -140,13 +151,6 @@ int check_product(int mode, int ta, int tb, int64_t M, int64_t N, int64_t K, int
   g.stride_c = stride_c;
   g.splits = 1;
   return SGEMM_OK;
-}
-
-// Leading dimensions are ints in the kernels.
-bool lds_fit(const Product& p, int64_t lda, int64_t ldb, int64_t ldc, const sgemm_epilogue* ep) {
-  const int64_t lim = int64_t(1) << 29;
-  return (p.a.bytes == 0 || p.g.lda == 1 || lda < lim) && ldb < lim && ldc < lim &&
-         (!ep || !ep->residual || ep->ldr < lim) && (!ep || !ep->preact || ep->ldp < lim);
 }
 
 const ProductVariant* variants(bool trans_a, bool trans_b) {
@@ -433,7 +437,7 @@ int act_backward(int64_t M, int64_t N, int64_t groups, const int32_t* offsets, b
   const Span c = {dC, span_bytes(M, N, lddc)};
   const Span z = {Z, act != SGEMM_ACT_NONE ? span_bytes(M, N, ldz) : 0};
   const Span d = {dZ, dZ ? span_bytes(M, N, lddz) : 0};
-  const Span b = {dbias, !dbias ? 0 : grouped ? groups_bytes(groups, lddb, N * 4) : N * 4};
+  const Span b = {dbias, !dbias ? 0 : grouped ? groups_bytes(groups, lddb, floats(N)) : floats(N)};
   const Span off = {offsets, grouped ? (groups + 1) * 4 : 0};
   const Span all[] = {c, z, d, b, off};
   const int st = check_spans(all, 5);
@@ -458,7 +462,6 @@ int act_backward(int64_t M, int64_t N, int64_t groups, const int32_t* offsets, b
   a.M = (int)M;
   a.N = (int)N;
   a.groups = (int)groups;
-  a.act = act;
   a.lpr = act_lanes(N);
   a.blocks_n = (int)cdiv(N, 4 * a.lpr);
   // Without sums the strips need no room.
@@ -472,9 +475,12 @@ int act_backward(int64_t M, int64_t N, int64_t groups, const int32_t* offsets, b
   const int64_t wgs = a.blocks_n * strips * groups, sums = cdiv(N, sg::kSumCols) * groups;
   if (!grid_fits(wgs, 64 * sg::kActWaves) || !grid_fits(sums, 1024)) return SGEMM_ERR_UNSUPPORTED;
   void* kargs[] = {&a};
-  const void* fn = Z ? reinterpret_cast<const void*>(sg::act_backward_kernel<true>)
-                     : reinterpret_cast<const void*>(sg::act_backward_kernel<false>);
-  hipError_t e = hipLaunchKernel(fn, dim3((unsigned)wgs), dim3(64 * sg::kActWaves), kargs, 0,
+  typedef void (*ActFn)(ActBackwardArgs);
+  static const ActFn table[] = {
+      sg::act_backward_kernel<SGEMM_ACT_NONE>, sg::act_backward_kernel<SGEMM_ACT_RELU>,
+      sg::act_backward_kernel<SGEMM_ACT_GELU>, sg::act_backward_kernel<SGEMM_ACT_GELU_TANH>,
+      sg::act_backward_kernel<SGEMM_ACT_SILU>};
+  hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(table[act]), dim3((unsigned)wgs), dim3(64 * sg::kActWaves), kargs, 0,
                                  stream);
   if (e == hipSuccess && dbias && strips > 1)
     e = hipLaunchKernel(reinterpret_cast<const void*>(sg::column_sum_kernel),
@@ -494,7 +500,6 @@ int sgemm_linear(int trans_a, int trans_b, int64_t M, int64_t N, int64_t K, cons
   const int st = check_product(sg::kDense, trans_a, trans_b, M, N, K, 0, nullptr, 0, A, lda, B,
                                ldb, 0, C, ldc, 0, epilogue, workspace, workspace_bytes, p);
   if (st != SGEMM_OK || !p.launch) return st;
-  if (!lds_fit(p, lda, ldb, ldc, epilogue)) return SGEMM_ERR_UNSUPPORTED;
   return run_product(p, p.g.offsets, stream, workspace, workspace_bytes);
 }
 
@@ -564,7 +569,6 @@ int sgemm_grouped(int trans_b, int64_t M, int64_t N, int64_t K, int64_t groups,
   const int st = check_product(sg::kRowGroups, 0, trans_b, M, N, K, groups, offsets, M, A, lda, B,
                                ldb, stride_b, C, ldc, 0, epilogue, workspace, workspace_bytes, p);
   if (st != SGEMM_OK || !p.launch) return st;
-  if (!lds_fit(p, lda, ldb, ldc, epilogue)) return SGEMM_ERR_UNSUPPORTED;
   return run_product(p, p.g.offsets, stream, workspace, workspace_bytes);
 }
 
@@ -587,7 +591,6 @@ int sgemm_grouped_wgrad(int trans_b, int64_t M, int64_t N, int64_t K, int64_t gr
                                trans_b ? A : dZ, trans_b ? lda : lddz, 0, dB, lddb, stride_db,
                                nullptr, workspace, workspace_bytes, p);
   if (st != SGEMM_OK || !p.launch) return st;
-  if (!lds_fit(p, lda, lddz, lddb, nullptr)) return SGEMM_ERR_UNSUPPORTED;
   return run_product(p, p.g.offsets, stream, workspace, workspace_bytes);
 }
 

@@ -59,8 +59,8 @@ __global__ void __launch_bounds__(64 * kActWaves) act_backward_kernel(ActBackwar
       for (int u = 0; u < U; ++u) {
         const int64_t row = r + u * beside;
         if (row < r1) {
-          d[u] = load_upto(a.dC + row * a.lddc + col, left);
-          if constexpr (ACT != SGEMM_ACT_NONE) z[u] = load_upto(a.Z + row * a.ldz + col, left);
+          d[u] = load_upto_once(a.dC + row * a.lddc + col, left);
+          if constexpr (ACT != SGEMM_ACT_NONE) z[u] = load_upto_once(a.Z + row * a.ldz + col, left);
         }
       }
 #pragma unroll

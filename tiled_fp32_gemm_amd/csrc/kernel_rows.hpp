@@ -18,10 +18,13 @@
 //                      four consecutive k rows, the others further k.
 //
 // Measured on MI355X (kernel trace; B of 64 MiB, 4096 x 4096, from HBM, one row
-// with bias and SILU): fast 13.4 us = 5.0 TB/s (KW = 4: 16.2), slow 15.4 us at
-// 16 columns a workgroup (32: 17.6, 64: 29: too few workgroups); product_kernel
-// with its second launch takes 20.4 and 21.9 us.  2, 4 and 8 rows cost 13 to
-// 16 us.
+// with bias and SILU): fast 13.4 us (KW = 4: 16.2), slow 15.4 us at 16 columns a
+// workgroup (32: 17.6, 64: 29: too few workgroups); product_kernel with its
+// second launch takes 20.4 and 21.9 us.  2, 4 and 8 rows cost 13 to 16 us.
+//
+// B is loaded nontemporal (one row by 4096 x 4096: 14.2 -> 12.7 us, 8192 x 8192:
+// 45 -> 43 us, 6.2 TB/s), but for the slow kernel's narrow blocks, whose
+// neighbours want the other half of a cache line (17.0 -> 18.3 us).
 //
 // Both take rows in chunks of R (more rows than R are further workgroups), of
 // one product or of groups, and A stored M x K.
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_fast_kernel(ProductArgs g) 
     for (int u = 0; u < U; ++u) {
 #pragma unroll
       for (int c = 0; c < NC; ++c)
-        bv[u][c] = *reinterpret_cast<const f32x4u*>(b[c] + k + u * STEP);
+        bv[u][c] = load_upto_once(b[c] + k + u * STEP, 4);
 #pragma unroll
       for (int r = 0; r < R; ++r)
         av[u][r] = *reinterpret_cast<const f32x4u*>(a[r] + k + u * STEP);
@@ -183,8 +186,9 @@ __global__ void __launch_bounds__(kRowsThreads) rows_slow_kernel(ProductArgs g) 
   auto sweep = [&](auto whole) {
     constexpr bool kWhole = decltype(whole)::value;
     auto load = [&](int k) {
-      return kWhole ? f32x4(*reinterpret_cast<const f32x4u*>(b + (int64_t)k * g.ldb))
-                    : load_upto(b + (int64_t)k * g.ldb, left);
+      const float* const p = b + (int64_t)k * g.ldb;
+      if (!kWhole) return load_upto(p, left);
+      return LC == 16 ? load_upto_once(p, 4) : load_upto(p, 4);
     };
     constexpr int kTwice = R == 8 ? 1 : 2;   // groups of rows in flight
     int k = 4 * (tid / LC);

@@ -265,27 +265,30 @@ def linear_backward(dC, A, B, activation="none", preact=None, *, transpose_a=Fal
     act = _act(activation)
     dev = _device(dC, "dC")
     M, N, K, lda, ldb = _inner(A, B, dev, transpose_a, transpose_b)
-    lddz = _sized(dC, "dC", dev, M, N)
+    lddc, ldz = _sized(dC, "dC", dev, M, N), 1
     if act:
         if preact is None:
             raise ValueError(f"activation {activation!r} needs preact")
-        _sized(preact, "preact", dev, M, N)
+        ldz = _sized(preact, "preact", dev, M, N)
     room, size = _workspace(workspace, dev)
     ta, tb = bool(transpose_a), bool(transpose_b)
+    lib = sg.load()
 
     def call(s):   # dZ, when it is made here, belongs to the stream
-        dz, dbias, ld = dC, None, lddz
+        dz, ld, dbias = dC, lddc, dC.new_empty(N) if bias_grad else None
+        if act:
+            dz, ld = dC.new_empty(M, N), max(N, 1)
         if act or bias_grad:
-            dz, dbias = activation_backward(dC, activation, preact, bias_grad=bias_grad,
-                                            workspace=workspace)
-            ld = max(N, 1) if act else lddz
+            _check(lib.sgemm_act_backward(
+                M, N, dC.data_ptr(), lddc, preact.data_ptr() if act else None, ldz, act,
+                dz.data_ptr() if act else None, ld, dbias.data_ptr() if bias_grad else None, s,
+                room, size), "sgemm_act_backward")
         dA, dB = A.new_empty(A.shape), B.new_empty(B.shape)
         a, b, d = (A.data_ptr(), lda), (B.data_ptr(), ldb), (dz.data_ptr(), ld)
-        sgemm_linear = sg.load().sgemm_linear
 
         def product(out, left, trans_left, right, trans_right, m, n, k):
-            _check(sgemm_linear(trans_left, trans_right, m, n, k, *left, *right, out.data_ptr(),
-                                max(n, 1), None, s, room, size), "sgemm_linear")
+            _check(lib.sgemm_linear(trans_left, trans_right, m, n, k, *left, *right, out.data_ptr(),
+                                    max(n, 1), None, s, room, size), "sgemm_linear")
         # d op(A) = dZ op(B)^T and d op(B) = op(A)^T dZ, transposed where A and B are
         if ta:
             product(dA, b, tb, d, True, K, M, N)

@@ -132,9 +132,12 @@ __device__ __forceinline__ void tile_order(int L, int tiles_m, int tiles_n, int 
 
 // False: no tile for this workgroup.  The groups' whole tiles come first, in
 // group order, then their partial last ones, which are shorter work: the
-// launch ends with them, and each XCD has its share of both.  Every wave does
-// this for itself, 64 groups at a time, and almost always has all of them at
-// once.
+// launch ends with them, and each XCD has its share of both.  Tiles of 128 rows
+// and more are sorted by length there: 16384 rows of sixteen uneven groups, N =
+// 4096, K = 1024, 256-row tiles 1179 -> 1024 us, 128-row tiles 1070 -> 1020 us
+// (64-row tiles lose by it, as neighbours part: 88 -> 95 us for 4096 rows of
+// eight groups, N = K = 1024).  Every wave does this for itself, 64 groups at a
+// time, and almost always has all of them at once.
 template <int BM>
 __device__ __forceinline__ bool row_group_tile(const ProductArgs& g, int lane, RowTile& t) {
   int b = 0, e = 0, whole = 0, upto = 0;
@@ -165,10 +168,30 @@ __device__ __forceinline__ bool row_group_tile(const ProductArgs& g, int lane, R
     total = count();
     if (w >= total * g.splits) return false;
   }
-  int L = xcd_order(w, total * g.splits);
+  // Large partial tiles go out longest first and to the XCDs in turn, so that
+  // the launch does not end on a long one.
+  const bool ranked = BM >= 128 && part && g.groups <= 64;
+  int L = ranked ? w : xcd_order(w, total * g.splits);
   t.split = L / total;
   L -= t.split * total;
   const int row_tile = L / g.tiles_n;   // of all groups' row tiles
+  if (ranked) {
+    const int rem = (e - b) % BM;
+    int rank = 0;   // groups with a longer partial tile
+    for (int j = 0; j < g.groups; ++j) {
+      const int other = __builtin_amdgcn_readlane(rem, j);
+      rank += other > rem || (other == rem && j < lane) ? 1 : 0;
+    }
+    const uint64_t hit = __ballot(rem > 0 && rank == row_tile);
+    if (hit == 0) return false;
+    const int at = __ffsll((unsigned long long)hit) - 1;
+    t.group = at;
+    t.first = __builtin_amdgcn_readlane(b, at);
+    t.end = __builtin_amdgcn_readlane(e, at);
+    t.tm = __builtin_amdgcn_readlane(whole, at);
+    t.tn = L - row_tile * g.tiles_n;
+    return t.tn >= 0 && t.tn < g.tiles_n && t.first + t.tm * BM < t.end;
+  }
   int before = 0;
   for (int e0 = 0;;) {
     const uint64_t past = __ballot(before + upto > row_tile);

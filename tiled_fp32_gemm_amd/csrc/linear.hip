@@ -208,12 +208,13 @@ int64_t likely_tiles(const ProductArgs& g, const sg::host::TileCost& c) {
 
 // Estimated seconds of `tiles` workgroups over K.  The tiles of row groups differ
 // and are handed out as workgroups end, so a last round that is partly filled
-// counts in part (and a third of a tile more, for its uneven end).
+// counts in part, and some more for its uneven end (less for the tiles that are
+// handed out longest first).
 double likely_time(const ProductArgs& g, const sg::host::TileCost& c, int64_t tiles, int64_t K) {
   const double t = estimate_grid(c, tiles, K);
   const int64_t full = tiles / kCUs, rest = tiles % kCUs;
   if (g.mode != sg::kRowGroups || full == 0 || rest == 0) return t;
-  const double part = (double)rest / kCUs + 0.3;
+  const double part = (double)rest / kCUs + (c.tile_m >= 128 ? 0.1 : 0.3);
   const double less = estimate_grid(c, full * kCUs, K);
   return part >= 1.0 ? t : less + part * (t - less);
 }

@@ -7,8 +7,10 @@
 // order and go to the strip's row of W, or straight to the result when a group
 // is one strip; column_sum_kernel adds the strips in a fixed order.  Bound by
 // HBM: dC and Z are read once and dZ is written once.  Measured on MI355X with
-// SILU or GELU: 65536 x 128 in 19.4 us (5.2 TB/s), 4096 x 4096 in 45 us
-// (4.5 TB/s), and 4.7 us for the strips' sums.
+// SILU or GELU: 65536 x 128 in 18.6 us (5.4 TB/s), 4096 x 4096 in 41 us
+// (4.9 TB/s), and 4.7 us for the strips' sums.  The loads are nontemporal, which
+// leaves dZ in the caches for the products after it (41 instead of 45 us here,
+// 109 -> 100 us with two products at K = 64).
 //
 // Loads and stores are 16 bytes at any 4-byte alignment (global, not buffer,
 // accesses); only a row's last one to three columns go one by one.

@@ -18,9 +18,10 @@
 //                      four consecutive k rows, the others further k.
 //
 // Measured on MI355X (kernel trace; B of 64 MiB, 4096 x 4096, from HBM, one row
-// with bias and SILU): fast 13.4 us (KW = 4: 16.2), slow 15.4 us at 16 columns a
-// workgroup (32: 17.6, 64: 29: too few workgroups); product_kernel with its
-// second launch takes 20.4 and 21.9 us.  2, 4 and 8 rows cost 13 to 16 us.
+// with bias and SILU) before the loads were nontemporal: fast 13.4 us (KW = 4:
+// 16.2), slow 15.4 us at 16 columns a workgroup (32: 17.6, 64: 29: too few
+// workgroups); product_kernel with its second launch takes 20.4 and 21.9 us.  2,
+// 4 and 8 rows cost 13 to 16 us.
 //
 // B is loaded nontemporal (one row by 4096 x 4096: 14.2 -> 12.7 us, 8192 x 8192:
 // 45 -> 43 us, 6.2 TB/s), but for the slow kernel's narrow blocks, whose
@@ -190,9 +191,9 @@ __global__ void __launch_bounds__(kRowsThreads) rows_slow_kernel(ProductArgs g) 
       if (!kWhole) return load_upto(p, left);
       return LC == 16 ? load_upto_once(p, 4) : load_upto(p, 4);
     };
-    constexpr int kTwice = R == 8 ? 1 : 2;   // groups of rows in flight
+    constexpr int kFlight = 2;   // groups of rows in flight
     int k = 4 * (tid / LC);
-#pragma unroll kTwice
+#pragma unroll kFlight
     for (; k + 4 <= g.K; k += 4 * KR) {
       f32x4 av[R], bv[4];
 #pragma unroll
@@ -221,16 +222,17 @@ __global__ void __launch_bounds__(kRowsThreads) rows_slow_kernel(ProductArgs g) 
   const int first = spread_sum<32, LC, V, V>(acc, lane);
   if (V >= SHARE || lane / LC % (SHARE / V > 0 ? SHARE / V : 1) == 0) {
 #pragma unroll
-    for (int i = 0; i < LEFT; ++i) part[wave][(first + i) * LC + cg] = acc[i];
+    for (int i = 0; i < LEFT; ++i) {   // [row][column], as they are read below
+      const int v = first + i;
+      part[wave][v / 4 * (4 * LC) + 4 * cg + v % 4] = acc[i];
+    }
   }
   __syncthreads();
   for (int i = tid; i < V * LC; i += kRowsThreads) {
     // Consecutive threads take consecutive columns of a row.
     const int r = i / (4 * LC), c = i % (4 * LC);
-    const int at = (r * 4 + c % 4) * LC + c / 4;
-    if (r < p.rows && n0 + c < g.N) {
-      finish_one(g, p, r, n0 + c, ((part[0][at] + part[1][at]) + part[2][at]) + part[3][at]);
-    }
+    if (r < p.rows && n0 + c < g.N)
+      finish_one(g, p, r, n0 + c, ((part[0][i] + part[1][i]) + part[2][i]) + part[3][i]);
   }
 }
 

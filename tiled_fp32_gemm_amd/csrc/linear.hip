@@ -277,15 +277,18 @@ struct RowsChoice {
   int64_t workgroups;
 };
 
-// Measured on MI355X against product_kernel with a workspace (us, B from HBM;
-// N = K = 4096, and eight groups of N = 4096, K = 1024):
-//      B stored         N x K             K x N
-//      8 rows           15.8 / 19.2       16.3 / 21.8
-//      16 rows          18.0 / 20.3       24.5 / 21.8
-//      groups, avg. 1   17.7 / 24.4       18.4 / 22.8
-//      groups, avg. 4   31.8 / 35.7       29.7 / 31.4
-//      groups, avg. 8   39.5 / 37.9       36.6 / 33.7
-// Columns a workgroup: the most that still give every CU a workgroup.
+// Measured on MI355X against product_kernel with a workspace (us, rows /
+// product; N = K = 4096, and groups of N = 4096, K = 1024):
+//      B stored           N x K             K x N
+//      4 rows           15.0 / 20.1       15.0 / 18.3
+//      8 rows           17.4 / 20.0       17.5 / 18.9
+//      16 rows          22.5 / 20.3
+//      groups, avg. 1   17.0 / 22.6       18.7 / 21.3
+//      groups, avg. 4   27.0 / 33.4       26.0 / 31.5
+//      groups, avg. 5   31.8 / 36.3       35.1 / 32.2
+//      groups, avg. 8   38.0 / 36.1       37.8 / 33.1
+// Without room to split, 16 rows of N x K are the faster way as well (product_
+// kernel 45).  Columns a workgroup: the most that still give every CU one.
 RowsChoice choose_rows(const Product& p) {
   const ProductArgs& g = p.g;
   RowsChoice none = {0, 0, 0};
@@ -294,7 +297,8 @@ RowsChoice choose_rows(const Product& p) {
   if (p.trans_a || g.mode == sg::kSumGroups || g.K >= 1 << 29) return none;
   const bool grouped = g.mode == sg::kRowGroups;
   const int64_t live = grouped ? live_groups(g) : 1;
-  const int64_t most = grouped ? 4 * live : p.trans_b ? 2 * sg::kRowsMost : sg::kRowsMost;
+  const int64_t most = grouped ? (p.trans_b ? 6 : 4) * live
+                               : p.trans_b ? 2 * sg::kRowsMost : sg::kRowsMost;
   if (g.M > most && g.M > sg::kRowsMost) return none;
   // A chunk has room for a group of twice the average.
   const int64_t want = grouped ? cdiv(2 * g.M, live) : g.M;
@@ -311,6 +315,12 @@ RowsChoice choose_rows(const Product& p) {
   return grid_fits(ch.workgroups, 256) ? ch : none;
 }
 
+// Two chunks of rows over a B that the caches do not hold twice: 16 x 4096 x 4096
+// takes 22.5 us by rows and 20.3 split, 16 x 1024 x 1024 5 and 9.
+bool many_rows(const ProductArgs& g) {
+  return g.mode == sg::kDense && g.M > sg::kRowsMost && (int64_t)g.N * g.K > 1 << 22;
+}
+
 // Few columns over a long K leave the chip idle by rows, where a split product
 // fills it.  Measured (us, rows / split; N x K):
 //      B stored N x K   64 x 65536   64 x 16384   1024 x 8192
@@ -322,6 +332,7 @@ RowsChoice choose_rows(const Product& p) {
 bool rather_split(const Product& p, const RowsChoice& rows, const Choice& ch) {
   if (ch.v == nullptr || ch.splits == 1) return false;
   const int64_t K = p.g.K;
+  if (many_rows(p.g)) return true;
   return p.trans_b ? rows.workgroups < 64 && K * rows.rows > 196608
                    : rows.workgroups <= kCUs / 2 && K * (rows.rows + 2) > 12288;
 }
@@ -331,8 +342,9 @@ int run_product(Product& p, const int32_t* offsets, hipStream_t stream, void* ws
   ProductArgs& g = p.g;
   const RowsChoice rows = choose_rows(p);
   Choice ch = {nullptr, 1, 0, 0};
-  // Only a long K over few columns asks what a split would be.
-  if (rows.rows == 0 || (g.K > 1024 && rows.workgroups <= kCUs / 2)) ch = choose(p, ws_bytes);
+  // Only many rows, or a long K over few columns, ask what a split would be.
+  if (rows.rows == 0 || many_rows(g) || (g.K > 1024 && rows.workgroups <= kCUs / 2))
+    ch = choose(p, ws_bytes);
   if (rows.rows > 0 && !rather_split(p, rows, ch)) {
     g.tiles_m = (int)cdiv(g.M, rows.rows);
     g.tiles_n = (int)cdiv(g.N, rows.cols);

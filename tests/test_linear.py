@@ -456,7 +456,8 @@ def lib():
     (0, 0, 65536, 128, 256, "product_fs_128x128x32"),
     (0, 1, 1, 4096, 4096, "rows_fast_1x16"), (0, 1, 1, 1024, 4096, "rows_fast_1x4"),
     (0, 1, 12, 4096, 4096, "rows_fast_8x16"), (0, 0, 5, 4096, 4096, "rows_slow_8x16"),
-    (0, 0, 2, 32768, 1024, "rows_slow_2x64"), (0, 0, 9, 4096, 4096, "product_fs_32x64x32_ks2_s4"),
+    (0, 0, 2, 32768, 1024, "rows_slow_2x64"), (0, 0, 9, 4096, 4096, "rows_slow_8x32"),
+    (0, 0, 17, 4096, 4096, "product_fs_32x64x32_ks2_s4"),
     (1, 0, 1, 4096, 4096, "product_ss_32x64x32_ks2_s4")])
 def test_plans_without_workspace(lib, ta, tb, M, N, K, kernel):
     st, plan = sg.sgemm_linear_plan_query(ta, tb, M, N, K)

@@ -282,13 +282,14 @@ struct RowsChoice {
 //      B stored           N x K             K x N
 //      4 rows           15.0 / 20.1       15.0 / 18.3
 //      8 rows           17.4 / 20.0       17.5 / 18.9
-//      16 rows          22.5 / 20.3
+//      16 rows          22.5 / 20.3       24.5 / 19.1
+//      16 rows, 1024 x 1024   4.6 / 9.4    5.6 / 9.2
 //      groups, avg. 1   17.0 / 22.6       18.7 / 21.3
 //      groups, avg. 4   27.0 / 33.4       26.0 / 31.5
 //      groups, avg. 5   31.8 / 36.3       35.1 / 32.2
 //      groups, avg. 8   38.0 / 36.1       37.8 / 33.1
-// Without room to split, 16 rows of N x K are the faster way as well (product_
-// kernel 45).  Columns a workgroup: the most that still give every CU one.
+// Without room to split, 16 rows are the faster way as well (product_kernel 42
+// and 45).  Columns a workgroup: the most that still give every CU one.
 RowsChoice choose_rows(const Product& p) {
   const ProductArgs& g = p.g;
   RowsChoice none = {0, 0, 0};
@@ -297,8 +298,7 @@ RowsChoice choose_rows(const Product& p) {
   if (p.trans_a || g.mode == sg::kSumGroups || g.K >= 1 << 29) return none;
   const bool grouped = g.mode == sg::kRowGroups;
   const int64_t live = grouped ? live_groups(g) : 1;
-  const int64_t most = grouped ? (p.trans_b ? 6 : 4) * live
-                               : p.trans_b ? 2 * sg::kRowsMost : sg::kRowsMost;
+  const int64_t most = grouped ? (p.trans_b ? 6 : 4) * live : 2 * sg::kRowsMost;
   if (g.M > most && g.M > sg::kRowsMost) return none;
   // A chunk has room for a group of twice the average.
   const int64_t want = grouped ? cdiv(2 * g.M, live) : g.M;
@@ -315,8 +315,7 @@ RowsChoice choose_rows(const Product& p) {
   return grid_fits(ch.workgroups, 256) ? ch : none;
 }
 
-// Two chunks of rows over a B that the caches do not hold twice: 16 x 4096 x 4096
-// takes 22.5 us by rows and 20.3 split, 16 x 1024 x 1024 5 and 9.
+// Two chunks of rows over a B that the caches do not hold: see choose_rows.
 bool many_rows(const ProductArgs& g) {
   return g.mode == sg::kDense && g.M > sg::kRowsMost && (int64_t)g.N * g.K > 1 << 22;
 }

@@ -507,6 +507,18 @@ def test_the_headers_declare_the_binding_names(lib):
             assert hasattr(lib, n) and hasattr(sg, n)
 
 
+def test_the_package_imports_torch_only_when_it_is_needed():
+    import os
+    import subprocess
+    import sys
+    code = ("import sys, tiled_fp32_gemm_amd as sg, tiled_fp32_gemm_amd.build; "
+            "assert 'torch' not in sys.modules; sg.linear; assert 'torch' in sys.modules; "
+            "assert all(hasattr(sg, n) for n in sg.__all__); "
+            "assert not hasattr(sg, 'no_such_name')")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root)
+
+
 def call(ta=0, tb=0, M=4, N=8, K=16, A=BIG, lda=None, B=BIG + (1 << 31), ldb=None,
          C=BIG + (1 << 32), ldc=None, ws=0, ws_bytes=0, **ep):
     lda = max(M if ta else K, 1) if lda is None else lda

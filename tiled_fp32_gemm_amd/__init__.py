@@ -23,6 +23,7 @@ the library.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 
 __all__ = ["sgemm", "sgemm_ex", "sgemm_plan_query", "sgemm_status_string",
@@ -123,8 +124,9 @@ def load():
     lib.sgemm_workspace_bytes.restype = i64
     lib.sgemm_plan_query_ws.argtypes = common + [i64, ctypes.POINTER(SgemmPlan)]
     lib.sgemm_plan_query_ws.restype = i32
-    _epilogue.prototypes(lib)
-    _moe.prototypes(lib)
+    from . import epilogue, moe
+    epilogue.prototypes(lib)
+    moe.prototypes(lib)
     _lib = lib
     return lib
 
@@ -309,19 +311,25 @@ def plan(A, B, out=None, algo: str | int = "auto") -> dict:
     return p.as_dict()
 
 
-from . import epilogue as _epilogue  # noqa: E402  (they use the names above)
-from . import moe as _moe  # noqa: E402
-from .epilogue import (ACTIVATIONS, LINEAR_SYMBOLS, Epilogue,  # noqa: E402
-                       activation_backward, linear, linear_backward,
-                       sgemm_act_backward, sgemm_act_backward_workspace_bytes,
-                       sgemm_linear, sgemm_linear_plan_query,
-                       sgemm_linear_workspace_bytes)
-from .moe import (MOE_MAX_EXPERTS, MOE_SYMBOLS, grouped_linear,  # noqa: E402
-                  grouped_linear_backward, moe_permute, moe_sort,
-                  moe_unpermute, moe_unpermute_backward, sgemm_grouped,
-                  sgemm_grouped_act_backward,
-                  sgemm_grouped_act_backward_workspace_bytes,
-                  sgemm_grouped_wgrad, sgemm_grouped_wgrad_workspace_bytes,
-                  sgemm_grouped_workspace_bytes, sgemm_moe_permute,
-                  sgemm_moe_sort, sgemm_moe_sort_workspace_bytes,
-                  sgemm_moe_unpermute, sgemm_moe_unpermute_backward)
+# Names of the modules that need torch, which this one imports only when the
+# library is loaded: they are imported when one of them is first asked for.
+_LATER = {
+    "epilogue": ("ACTIVATIONS", "LINEAR_SYMBOLS", "Epilogue", "activation_backward", "linear",
+                 "linear_backward", "sgemm_act_backward", "sgemm_act_backward_workspace_bytes",
+                 "sgemm_linear", "sgemm_linear_plan_query", "sgemm_linear_workspace_bytes"),
+    "moe": ("MOE_MAX_EXPERTS", "MOE_SYMBOLS", "grouped_linear", "grouped_linear_backward",
+            "moe_permute", "moe_sort", "moe_unpermute", "moe_unpermute_backward",
+            "sgemm_grouped", "sgemm_grouped_act_backward",
+            "sgemm_grouped_act_backward_workspace_bytes", "sgemm_grouped_wgrad",
+            "sgemm_grouped_wgrad_workspace_bytes", "sgemm_grouped_workspace_bytes",
+            "sgemm_moe_permute", "sgemm_moe_sort", "sgemm_moe_sort_workspace_bytes",
+            "sgemm_moe_unpermute", "sgemm_moe_unpermute_backward")}
+
+
+def __getattr__(name: str):
+    for module, names in _LATER.items():
+        if name in names:
+            found = importlib.import_module(f"{__name__}.{module}")
+            globals().update({n: getattr(found, n) for n in names})
+            return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -2,9 +2,10 @@
 (``include/sgemm_linear.h``), over torch tensors.
 
 ``linear`` and ``linear_backward`` follow ``matmul``: float32 GPU tensors,
-row-major with any row stride, the current stream unless one is given, a
-caller's workspace where sums may be split.  Nothing is differentiated
-automatically: ``linear_backward`` is a call of its own.
+row-major with any row stride, the current stream unless one is given (what a
+call makes then belongs to that stream), a caller's workspace where sums may be
+split.  Nothing is differentiated automatically: ``linear_backward`` is a call
+of its own.
 """
 from __future__ import annotations
 

@@ -256,6 +256,37 @@ def test_grouped_integers_are_exact_and_the_same_every_time(tb):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,G,N,K", [(9000, 9, 2100, 64), (17000, 7, 4000, 100),
+                                        (20000, 70, 2000, 64)])
+def test_large_tiles_over_uneven_groups_are_exact(rows, G, N, K):
+    """The 128- and 256-row tiles: whole ones first, partial ones by length (up
+    to 64 groups), waves without rows."""
+    g = gen(rows)
+    draw = lambda *s: torch.randint(-8, 9, s, device="cuda", generator=g).float()  # noqa: E731
+    p = torch.softmax(torch.randn(G, device="cuda", generator=g), 0)
+    p[1] = 0
+    counts = torch.bincount(torch.multinomial(p, rows, replacement=True, generator=g),
+                            minlength=G).tolist()
+    offsets = offsets_of(counts)
+    edges = offsets.tolist()
+    A, b, dC = draw(rows, K), draw(G, N), draw(rows, N)
+    R = draw(rows, N)
+    ws = torch.empty(1 << 24, device="cuda")
+    for tb in (False, True):
+        B = draw(G, *((N, K) if tb else (K, N)))
+        C = sg.grouped_linear(A, B, offsets, b, "relu", R, transpose_b=tb, workspace=ws)
+        dA, dB, db = sg.grouped_linear_backward(dC, A, B, offsets, transpose_b=tb, workspace=ws)
+        for e, (i, j) in enumerate(zip(edges, edges[1:])):
+            m = (B[e].t() if tb else B[e]).double()
+            a, d = A[i:j].double(), dC[i:j].double()
+            assert torch.equal(C[i:j].double(), (a @ m + b[e].double()).clamp(min=0) + R[i:j])
+            assert torch.equal(dA[i:j].double(), d @ m.t())
+            w = a.t() @ d
+            assert torch.equal(dB[e].double(), w.t() if tb else w)
+            assert torch.equal(db[e].double(), d.sum(0))
+
+
+@pytest.mark.gpu
 def test_moves_past_32_bits():
     g = gen(12)
     T, top, H = 310000, 4, 1000
@@ -394,6 +425,44 @@ def test_a_layer_of_experts_end_to_end():
         torch.cuda.synchronize()
         kept_out = [o.clone() for o in out]
         for a, b in zip(kept_out, ours()):
+            assert torch.equal(a, b), rep
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("own_room", [False, True])
+def test_routing_of_many_tokens_replays_from_a_graph(own_room):
+    g = gen(16)
+    T, top, E, H = 6000, 3, 40, 100       # more choices than one workgroup sorts
+    x, w = torch.randn(T, H, device="cuda", generator=g), torch.rand(T, top, device="cuda",
+                                                                     generator=g)
+    ids = torch.randint(-1, E + 1, (T, top), device="cuda", generator=g)
+    ws = torch.empty(1 << 20, device="cuda") if own_room else None
+    xp = torch.zeros(T * top, H, device="cuda")
+
+    def step():
+        offsets, order, place = sg.moe_sort(ids, E, workspace=ws)
+        sg.moe_permute(x, place, out=xp)
+        return offsets, order, place, sg.moe_unpermute(xp, place, w)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for rep in range(4):
+        ids.copy_(torch.randint(-1, E + 1, (T, top), device="cuda", generator=g))
+        x.normal_(generator=g)
+        for o in out:
+            o.fill_(-9)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in out]
+        for a, b in zip(got, plain_sort(ids.cpu(), E)):
+            assert torch.equal(a.cpu(), b), rep
+        for a, b in zip(got, step()):
             assert torch.equal(a, b), rep
 
 

@@ -212,6 +212,8 @@ int64_t likely_tiles(const ProductArgs& g, const sg::host::TileCost& c) {
 // handed out longest first).
 double likely_time(const ProductArgs& g, const sg::host::TileCost& c, int64_t tiles, int64_t K) {
   const double t = estimate_grid(c, tiles, K);
+  // Summed groups in one round take as long as the longest.
+  if (g.mode == sg::kSumGroups && g.groups > 1 && tiles <= kCUs * c.occ) return 1.25 * t;
   const int64_t full = tiles / kCUs, rest = tiles % kCUs;
   if (g.mode != sg::kRowGroups || full == 0 || rest == 0) return t;
   const double part = (double)rest / kCUs + (c.tile_m >= 128 ? 0.1 : 0.3);

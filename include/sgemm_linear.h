@@ -90,7 +90,10 @@ int64_t sgemm_linear_workspace_bytes(int trans_a, int trans_b, int64_t M,
  * and this much workspace.  A kernel "product_.." is a tile of matrix
  * instructions (then 's' or 'f' for A and B: k from row to row or along the
  * rows), "rows_.." the vector kernels for a few rows, for which tile_k,
- * lds_bytes and wg_per_cu are 0.  Host only. */
+ * lds_bytes and wg_per_cu are 0.  A product a little over whole rounds of its
+ * tiles is cut in two launches: "+4rows" or "+4cols" is what the second one
+ * computes, the plan is the first one's but for workspace_bytes, which is
+ * enough for both.  Host only. */
 int sgemm_linear_plan_query(int trans_a, int trans_b, int64_t M, int64_t N,
                             int64_t K, int64_t workspace_bytes,
                             sgemm_plan *plan);

@@ -154,6 +154,44 @@ def test_linear_integers_are_exact():
                            want)
 
 
+# Cut in two launches: by rows (one, a few by the vector kernels, many), by columns.
+CUTS = [(2049, 4096, 1000), (2053, 4096, 1024), (2100, 4096, 1001), (2048, 4104, 1024),
+        (4096, 4097, 1000), (4200, 4096, 1500)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ta,tb", [(False, False), (False, True), (True, False), (True, True)])
+@pytest.mark.parametrize("M,N,K", CUTS)
+def test_linear_in_two_launches(M, N, K, ta, tb):
+    assert "+" in sg.sgemm_linear_plan_query(ta, tb, M, N, K, 1 << 26)[1].kernel.decode()
+    run_case(M, N, K, ta, tb, "silu", ws_bytes=1 << 26, in_place=True)
+    run_case(M, N, K, ta, tb, "gelu", pad=3, off=1)
+
+
+@pytest.mark.gpu
+def test_linear_in_two_launches_is_exact_and_replays():
+    g = gen(8)
+    M, N, K = 4700, 4096, 4096   # the second launch splits K
+    A = torch.randint(-8, 9, (M, K), generator=g, device="cuda").float()
+    B = torch.randint(-8, 9, (K, N), generator=g, device="cuda").float()
+    b = torch.randint(-8, 9, (N,), generator=g, device="cuda").float()
+    need = sg.sgemm_linear_workspace_bytes(0, 0, M, N, K)
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    want = (A.double() @ B.double() + b).clamp(min=0).float()
+    assert torch.equal(sg.linear(A, B, b, "relu", workspace=ws), want)
+    assert torch.equal(sg.linear(A, B, b, "relu"), want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = sg.linear(A, B, b, "relu", workspace=ws)
+    for _ in range(3):
+        out.fill_(float("nan"))
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
 @pytest.mark.gpu
 def test_activations_at_the_extremes():
     inf, nan = float("inf"), float("nan")
@@ -479,6 +517,32 @@ def test_split_plans_fit_their_workspace(lib):
             assert sg.sgemm_linear_plan_query(ta, tb, M, N, K)[1].splits == 1
     for args in ((0, 0, 4096, 4096, 4096), (0, 1, 1, 4096, 4096), (0, 0, 256, 256, 0)):
         assert sg.sgemm_linear_workspace_bytes(*args) == 0
+
+
+@pytest.mark.parametrize("ta,tb,M,N,K,kernel", [
+    (0, 0, 4097, 4096, 4096, "product_fs_256x256x32+1rows"),
+    (0, 1, 8200, 4096, 4096, "product_ff_256x256x32+8rows"),
+    (1, 0, 2100, 4096, 4096, "product_ss_128x128x32+52rows"),
+    (0, 0, 4096, 4200, 4096, "product_fs_256x256x32+104cols"),
+    (0, 0, 4096, 4096, 4096, "product_fs_256x256x32"),
+    (0, 0, 5000, 4096, 4096, "product_fs_128x128x32"),
+    (0, 0, 1000, 1500, 777, "product_fs_32x64x32_ks2")])
+def test_plans_in_two_launches(lib, ta, tb, M, N, K, kernel):
+    assert sg.sgemm_linear_plan_query(ta, tb, M, N, K)[1].kernel.decode() == kernel
+
+
+def test_two_launches_fit_their_workspace(lib):
+    for ta, tb in itertools.product((0, 1), repeat=2):
+        for M, N, K in ((4700, 4096, 4096), (4096, 4700, 4096), (4097, 4096, 4096),
+                        (2100, 4096, 4096), (9000, 2048, 4096)):
+            need = sg.sgemm_linear_workspace_bytes(ta, tb, M, N, K)
+            st, plan = sg.sgemm_linear_plan_query(ta, tb, M, N, K, need)
+            assert st == sg.OK and plan.workspace_bytes == need
+            assert sg.sgemm_linear_plan_query(ta, tb, M, N, K, 1 << 40)[1].as_dict() \
+                == plan.as_dict()
+            if need:
+                less = sg.sgemm_linear_plan_query(ta, tb, M, N, K, need - 4)[1]
+                assert less.workspace_bytes <= need - 4
 
 
 def test_plan_query_refuses(lib):

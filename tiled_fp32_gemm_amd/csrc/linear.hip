@@ -180,6 +180,7 @@ struct Choice {
   const ProductVariant* v;
   int splits, k_split;
   int64_t workgroups;   // of the grid
+  double seconds;       // estimated
 };
 
 // Groups that can have rows.
@@ -230,7 +231,7 @@ Choice choose(const Product& p, int64_t ws_bytes) {
   // kSumGroups: the sum's length, groups taken as equal.
   const int64_t K = g.mode == sg::kSumGroups ? cdiv(g.rows, at_least_one(g.groups)) : g.K;
   const int64_t out = (int64_t)g.M * g.N * (g.mode == sg::kSumGroups ? g.groups : 1);
-  Choice one = {nullptr, 1, 0, 0}, split = one;
+  Choice one = {nullptr, 1, 0, 0, 0.0}, split = one;
   double t_one = 0, t_split = 0;
   static const int kSplits[] = {2, 3, 4, 6, 8, 12, 16, 24, 32};
   for (int i = 0; i < sg::kProductVariants; ++i) {
@@ -239,7 +240,7 @@ Choice choose(const Product& p, int64_t ws_bytes) {
     if (!variant_fits(p, v) || !grid_fits(grid, v.cost.threads)) continue;
     const double t = likely_time(g, v.cost, likely_tiles(g, v.cost), K);
     if (one.v == nullptr || t < t_one * 0.995) {
-      one = {&v, 1, 0, grid};
+      one = {&v, 1, 0, grid, t};
       t_one = t;
     }
   }
@@ -259,7 +260,7 @@ Choice choose(const Product& p, int64_t ws_bytes) {
       const double ts = 0.95 * likely_time(g, c, likely * se, ks) + kReduceFixed +
                         (double)(se + 1) * out * 4.0 / kReduceBW;
       if (split.v == nullptr || ts < t_split) {
-        split = {&v, (int)se, (int)ks, grid * se};
+        split = {&v, (int)se, (int)ks, grid * se, ts};
         t_split = ts;
       }
     }
@@ -338,49 +339,154 @@ bool rather_split(const Product& p, const RowsChoice& rows, const Choice& ch) {
                    : rows.workgroups <= kCUs / 2 && K * (rows.rows + 2) > 12288;
 }
 
-int run_product(Product& p, const int32_t* offsets, hipStream_t stream, void* ws,
-                int64_t ws_bytes) {
-  ProductArgs& g = p.g;
+// What one launch (or a split's two) of a product would be.
+struct Step {
+  RowsChoice rows;   // rows.rows > 0: by rows
+  Choice tile;
+};
+
+Step decide(const Product& p, int64_t ws_bytes) {
   const RowsChoice rows = choose_rows(p);
-  Choice ch = {nullptr, 1, 0, 0};
+  Step s = {{0, 0, 0}, {nullptr, 1, 0, 0, 0.0}};
   // Only many rows, or a long K over few columns, ask what a split would be.
-  if (rows.rows == 0 || many_rows(g) || (g.K > 1024 && rows.workgroups <= kCUs / 2))
-    ch = choose(p, ws_bytes);
-  if (rows.rows > 0 && !rather_split(p, rows, ch)) {
-    g.tiles_m = (int)cdiv(g.M, rows.rows);
-    g.tiles_n = (int)cdiv(g.N, rows.cols);
-    g.group_m = g.tiles_m < 8 ? g.tiles_m : 8;
-    void* args[] = {&g};
+  if (rows.rows == 0 || many_rows(p.g) || (p.g.K > 1024 && rows.workgroups <= kCUs / 2))
+    s.tile = choose(p, ws_bytes);
+  if (rows.rows > 0 && !rather_split(p, rows, s.tile)) s.rows = rows;
+  return s;
+}
+
+bool possible(const Step& s) { return s.rows.rows > 0 || s.tile.v != nullptr; }
+
+int64_t step_bytes(const Product& p, const Step& s) {
+  return s.rows.rows > 0 ? 0 : split_bytes(p.g, s.tile);
+}
+
+double step_seconds(const Product& p, const Step& s) {
+  // By rows: reading B, and a launch.
+  return s.rows.rows > 0 ? 4.0e-6 + 4.0 * p.g.N * p.g.K / 4.5e12 : s.tile.seconds;
+}
+
+// A dense product cut in two along M or N, each part a launch of its own: a
+// grid a little over what the chip holds at once otherwise pays a whole round
+// for its remainder, which alone takes a fitting kernel.
+struct Cut {
+  int64_t at;     // rows or columns of the first part; 0: not cut
+  bool columns;
+};
+
+// Rows (columns) `from` on, `count` of them.
+Product part_of(const Product& whole, bool columns, int64_t from, int64_t count) {
+  Product p = whole;
+  ProductArgs& g = p.g;
+  if (columns) {
+    g.B += p.trans_b ? from * g.ldb : from;
+    g.C += from;
+    if (g.bias) g.bias += from;
+    if (g.residual) g.residual += from;
+    if (g.preact) g.preact += from;
+    g.N = (int)count;
+  } else {
+    g.A += p.trans_a ? from : from * g.lda;
+    g.C += from * g.ldc;
+    if (g.residual) g.residual += from * g.ldr;
+    if (g.preact) g.preact += from * g.ldp;
+    g.M = (int)count;
+  }
+  return p;
+}
+
+// The cut with the least estimated time, if it is 6% under the uncut product's:
+// whole rounds of one of the three largest tiles, and the rest.  Not asked
+// where the whole is short or near what the chip can do anyway.  Measured on
+// MI355X (us, one launch / cut; K x N weight, N = K = 4096): M = 4097 1094 / 971, 4200
+// 1077 / 996, 8200 1977 / 1845; N x K, M = 2049 721 / 480.
+Cut find_cut(const Product& p, const Step& whole, int64_t ws_bytes) {
+  const ProductArgs& g = p.g;
+  Cut best = {0, false};
+  if (g.mode != sg::kDense || whole.rows.rows > 0 || whole.tile.v == nullptr) return best;
+  const double t_whole = whole.tile.seconds;
+  if (t_whole < 60e-6 || t_whole < 1.04 * 2.0 * g.M * g.N * g.K / 150e12) return best;
+  double t_best = 0.94 * t_whole;
+  const ProductVariant* table = variants(p.trans_a, p.trans_b);
+  for (int i = 0; i < 3; ++i) {
+    const sg::host::TileCost& c = table[i].cost;
+    if (!variant_fits(p, table[i])) continue;
+    const int64_t tm = cdiv(g.M, c.tile_m), tn = cdiv(g.N, c.tile_n);
+    const int64_t round = (int64_t)kCUs * c.occ, full = tm * tn / round * round;
+    for (int columns = 0; columns < 2; ++columns) {
+      const int64_t tiles = full / (columns ? tm : tn);
+      const int64_t at = tiles * (columns ? c.tile_n : c.tile_m), size = columns ? g.N : g.M;
+      if (at <= 0 || at >= size) continue;
+      const double t = estimate_grid(c, tiles * (columns ? tm : tn), g.K);
+      if (t >= t_best) continue;
+      const Product rest = part_of(p, columns, at, size - at);
+      const double both = t + step_seconds(rest, decide(rest, ws_bytes)) + 2.0e-6;
+      if (both < t_best) {
+        t_best = both;
+        best = {at, columns != 0};
+      }
+    }
+  }
+  return best;
+}
+
+int launch_step(Product& p, const Step& s, hipStream_t stream, void* ws) {
+  ProductArgs& g = p.g;
+  void* args[] = {&g};
+  const int tile_m = s.rows.rows > 0 ? s.rows.rows : s.tile.v->cost.tile_m;
+  const int tile_n = s.rows.rows > 0 ? s.rows.cols : s.tile.v->cost.tile_n;
+  g.tiles_m = (int)cdiv(g.M, tile_m);
+  g.tiles_n = (int)cdiv(g.N, tile_n);
+  g.group_m = g.tiles_m < 8 ? g.tiles_m : 8;
+  if (s.rows.rows > 0) {
     const hipError_t e = hipLaunchKernel(
-        reinterpret_cast<const void*>(sg::rows_kernel(p.trans_b, rows.rows, rows.cols)),
-        dim3((unsigned)rows.workgroups), dim3(256), args, 0, stream);
+        reinterpret_cast<const void*>(sg::rows_kernel(p.trans_b, s.rows.rows, s.rows.cols)),
+        dim3((unsigned)s.rows.workgroups), dim3(256), args, 0, stream);
     return e == hipSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH;
   }
-  if (ch.v == nullptr) return SGEMM_ERR_UNSUPPORTED;
-  const sg::host::TileCost& c = ch.v->cost;
-  g.tiles_m = (int)cdiv(g.M, c.tile_m);
-  g.tiles_n = (int)cdiv(g.N, c.tile_n);
-  g.group_m = g.tiles_m < 8 ? g.tiles_m : 8;
-  g.splits = ch.splits;
-  g.k_split = ch.k_split;
-  if (ch.splits > 1) {
-    g.W = static_cast<float*>(ws);
-    const Span w = {ws, split_bytes(g, ch)};
-    const Span off = {offsets, offsets ? (int64_t)(g.groups + 1) * 4 : 0};
+  g.splits = s.tile.splits;
+  g.k_split = s.tile.k_split;
+  g.W = static_cast<float*>(ws);
+  hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(s.tile.v->fn),
+                                 dim3((unsigned)s.tile.workgroups), dim3(s.tile.v->cost.threads),
+                                 args, 0, stream);
+  if (e == hipSuccess && s.tile.splits > 1) {
+    const int64_t rows = (int64_t)g.M * (g.mode == sg::kSumGroups ? g.groups : 1);
+    e = hipLaunchKernel(reinterpret_cast<const void*>(sg::product_reduce_kernel),
+                        dim3((unsigned)(rows * cdiv(g.N, sg::kProductReduceCols))), dim3(64), args,
+                        0, stream);
+  }
+  return e == hipSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH;
+}
+
+int run_product(Product& p, const int32_t* offsets, hipStream_t stream, void* ws,
+                int64_t ws_bytes) {
+  Product part[2] = {p, p};
+  Step step[2] = {decide(p, ws_bytes), {}};
+  if (!possible(step[0])) return SGEMM_ERR_UNSUPPORTED;
+  const Cut cut = find_cut(p, step[0], ws_bytes);
+  const int parts = cut.at > 0 ? 2 : 1;
+  if (parts == 2) {
+    part[0] = part_of(p, cut.columns, 0, cut.at);
+    part[1] = part_of(p, cut.columns, cut.at, (cut.columns ? p.g.N : p.g.M) - cut.at);
+    for (int i = 0; i < 2; ++i) {
+      step[i] = decide(part[i], ws_bytes);
+      if (!possible(step[i])) return SGEMM_ERR_UNSUPPORTED;
+    }
+  }
+  // Everything is checked before the first launch.
+  for (int i = 0; i < parts; ++i) {
+    const Span w = {ws, step_bytes(part[i], step[i])};
+    const Span off = {offsets, offsets ? (int64_t)(p.g.groups + 1) * 4 : 0};
     if (overlaps(w, p.a) || overlaps(w, p.b) || overlaps(w, p.c) || overlaps(w, p.bias) ||
         overlaps(w, p.res) || overlaps(w, p.pre) || overlaps(w, off))
       return SGEMM_ERR_INVALID_ARG;
   }
-  void* kargs[] = {&g};
-  hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(ch.v->fn),
-                                 dim3((unsigned)ch.workgroups), dim3(c.threads), kargs, 0, stream);
-  if (e == hipSuccess && ch.splits > 1) {
-    const int64_t rows = (int64_t)g.M * (g.mode == sg::kSumGroups ? g.groups : 1);
-    e = hipLaunchKernel(reinterpret_cast<const void*>(sg::product_reduce_kernel),
-                        dim3((unsigned)(rows * cdiv(g.N, sg::kProductReduceCols))),
-                        dim3(64), kargs, 0, stream);
+  for (int i = 0; i < parts; ++i) {
+    const int st = launch_step(part[i], step[i], stream, ws);
+    if (st != SGEMM_OK) return st;
   }
-  return e == hipSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH;
+  return SGEMM_OK;
 }
 
 // A product with no operands, for the questions about plans.
@@ -409,9 +515,13 @@ bool sizes_ok(int64_t a, int64_t b, int64_t c) {
 
 int64_t plan_workspace(const Product& p) {
   if (!p.launch) return 0;
-  const Choice ch = choose(p, INT64_MAX);
-  const RowsChoice rows = choose_rows(p);
-  return rows.rows > 0 && !rather_split(p, rows, ch) ? 0 : split_bytes(p.g, ch);
+  const Step s = decide(p, INT64_MAX);
+  const Cut cut = find_cut(p, s, INT64_MAX);
+  if (cut.at == 0) return step_bytes(p, s);
+  const Product a = part_of(p, cut.columns, 0, cut.at);
+  const Product b = part_of(p, cut.columns, cut.at, (cut.columns ? p.g.N : p.g.M) - cut.at);
+  const int64_t x = step_bytes(a, decide(a, INT64_MAX)), y = step_bytes(b, decide(b, INT64_MAX));
+  return x > y ? x : y;
 }
 
 int act_lanes(int64_t N) {
@@ -532,34 +642,43 @@ int sgemm_linear_plan_query(int trans_a, int trans_b, int64_t M, int64_t N, int6
   plan->splits = 1;
   const Product p = shape_only(sg::kDense, trans_a, trans_b, M, N, K, 1, 0);
   if (!p.launch) return SGEMM_OK;
-  const Choice ch = choose(p, workspace_bytes);
-  const RowsChoice rows = choose_rows(p);
-  if (rows.rows > 0 && !rather_split(p, rows, ch)) {
+  const Step whole = decide(p, workspace_bytes);
+  if (!possible(whole)) return SGEMM_ERR_UNSUPPORTED;
+  // Of a product cut in two, the first part, and the workspace of both.
+  const Cut cut = find_cut(p, whole, workspace_bytes);
+  const Product first = cut.at > 0 ? part_of(p, cut.columns, 0, cut.at) : p;
+  const Step s = cut.at > 0 ? decide(first, workspace_bytes) : whole;
+  plan->vec_a = plan->vec_b = 1;
+  plan->workspace_bytes = step_bytes(first, s);
+  char rest[24] = "";
+  if (cut.at > 0) {
+    const Product b = part_of(p, cut.columns, cut.at, (cut.columns ? N : M) - cut.at);
+    const int64_t more = step_bytes(b, decide(b, workspace_bytes));
+    if (more > plan->workspace_bytes) plan->workspace_bytes = more;
+    snprintf(rest, sizeof(rest), "+%d%s", cut.columns ? b.g.N : b.g.M, cut.columns ? "cols" : "rows");
+  }
+  if (s.rows.rows > 0) {
     plan->algo = SGEMM_ALGO_FMA;
-    plan->tile_m = rows.rows;
-    plan->tile_n = rows.cols;
+    plan->tile_m = s.rows.rows;
+    plan->tile_n = s.rows.cols;
     plan->threads = 256;
-    plan->vec_a = plan->vec_b = 1;
-    plan->workgroups = rows.workgroups;
-    snprintf(plan->kernel, sizeof(plan->kernel), "rows_%s_%dx%d", trans_b ? "fast" : "slow",
-             rows.rows, rows.cols);
+    plan->workgroups = s.rows.workgroups;
+    snprintf(plan->kernel, sizeof(plan->kernel), "rows_%s_%dx%d%s", trans_b ? "fast" : "slow",
+             s.rows.rows, s.rows.cols, rest);
     return SGEMM_OK;
   }
-  if (ch.v == nullptr) return SGEMM_ERR_UNSUPPORTED;
-  const sg::host::TileCost& c = ch.v->cost;
+  const sg::host::TileCost& c = s.tile.v->cost;
   plan->algo = SGEMM_ALGO_MFMA_DIRECT;
   plan->tile_m = c.tile_m;
   plan->tile_n = c.tile_n;
   plan->tile_k = c.tile_k;
   plan->threads = c.threads;
-  plan->vec_a = plan->vec_b = 1;
-  plan->workgroups = ch.workgroups;
-  plan->lds_bytes = ch.v->lds_bytes;
+  plan->workgroups = s.tile.workgroups;
+  plan->lds_bytes = s.tile.v->lds_bytes;
   plan->wg_per_cu = c.occ;
-  plan->splits = ch.splits;
-  plan->workspace_bytes = split_bytes(p.g, ch);
-  snprintf(plan->kernel, sizeof(plan->kernel), "product_%c%c_%s", trans_a ? 's' : 'f',
-           trans_b ? 'f' : 's', ch.v->name);
+  plan->splits = s.tile.splits;
+  snprintf(plan->kernel, sizeof(plan->kernel), "product_%c%c_%s%s", trans_a ? 's' : 'f',
+           trans_b ? 'f' : 's', s.tile.v->name, rest);
   return SGEMM_OK;
 }
 

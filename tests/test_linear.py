@@ -128,7 +128,7 @@ def test_linear_residual_in_place(M, N, K):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K", [(1, 64, 16384), (64, 64, 16384), (130, 70, 5001),
-                                   (256, 256, 8192), (20, 36, 4097)])
+                                   (256, 256, 8192), (20, 36, 4097), (33, 65, 65537)])
 @pytest.mark.parametrize("ta,tb", [(False, False), (False, True), (True, False)])
 def test_linear_long_k_with_and_without_workspace(M, N, K, ta, tb):
     need = sg.sgemm_linear_workspace_bytes(ta, tb, M, N, K)

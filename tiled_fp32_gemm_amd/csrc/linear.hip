@@ -233,7 +233,7 @@ Choice choose(const Product& p, int64_t ws_bytes) {
   const int64_t out = (int64_t)g.M * g.N * (g.mode == sg::kSumGroups ? g.groups : 1);
   Choice one = {nullptr, 1, 0, 0, 0.0}, split = one;
   double t_one = 0, t_split = 0;
-  static const int kSplits[] = {2, 3, 4, 6, 8, 12, 16, 24, 32};
+  static const int kSplits[] = {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
   for (int i = 0; i < sg::kProductVariants; ++i) {
     const ProductVariant& v = table[i];
     const int64_t grid = grid_tiles(g, v.cost);
@@ -252,13 +252,17 @@ Choice choose(const Product& p, int64_t ws_bytes) {
     const int64_t grid = grid_tiles(g, c), likely = likely_tiles(g, c);
     if (K < 2 * c.tile_k || !variant_fits(p, v)) continue;
     for (int S : kSplits) {
+      // Few tiles and a long K: 64 x 64 x 65536 in 32 splits 29.1 us, in 64 22.9; the
+      // second pass waits longer for more planes (64 x 64 x 16384: 14.0 with both).
+      if (S > 32 && 32 * grid >= kCUs) break;
       const int64_t ks = cdiv(cdiv(K, S), c.tile_k) * c.tile_k;
       const int64_t se = g.mode == sg::kSumGroups ? S : cdiv(K, ks);
       if (se < 2 || se * out > ws_bytes / 4 || !grid_fits(grid * se, c.threads) ||
           !grid_fits(out / g.N * cdiv(g.N, sg::kProductReduceCols), 64))
         continue;
       const double ts = 0.95 * likely_time(g, c, likely * se, ks) + kReduceFixed +
-                        (double)(se + 1) * out * 4.0 / kReduceBW;
+                        (double)(se + 1) * out * 4.0 / kReduceBW +
+                        (se > 32 ? 0.06e-6 * (se - 32) : 0.0);   // the planes' latency
       if (split.v == nullptr || ts < t_split) {
         split = {&v, (int)se, (int)ks, grid * se, ts};
         t_split = ts;

@@ -15,8 +15,16 @@
 // as K x N: "k slow"), and there are two LDS layouts to match, both permutations
 // of 16-byte units that keep every direct load lane-linear and every fragment
 // read conflict-free on 64 banks of 4 bytes (R: the tile's extent, CPR = BK/4):
-//   k fast   unit(r, c) = 16 CPR (r / 16) + 16 c + r % 16: a lane's four values
-//            of k come in one 128-bit read, 16 lanes read 256 contiguous bytes;
+//   k fast   unit(r, c) = CPR r + (c xor r / (16 / CPR) mod CPR): a lane's four
+//            values of k come in one 128-bit read, 16 rows read all 64 banks,
+//            and neighbouring lanes of a direct load fetch one row's cache line.
+//            The 256 x 256 tile, which has no register left for the xor's four
+//            addresses and loads little for what it computes, has
+//            unit(r, c) = 16 CPR (r / 16) + 16 c + r % 16, whose lanes fetch 16
+//            bytes of 16 rows.  With that in the smaller tiles the loads bound
+//            them, at 8.4 to 9 TB/s over the chip: 64 x 11008 x 4096 of an N x K
+//            weight 78.7 -> 61.5 us, 128 x 4096 x 4096 52.5 -> 46.6, 64 x 64 tiles
+//            at 4096^3 132 -> 143 TFLOP/s;
 //   k slow   unit(k, q) = (k R/4 + q) xor (k & 8): lanes 0-31 read row 16 s + p
 //            and lanes 32-63 row 16 s + 8 + p; the xor puts the two on
 //            different halves of the banks (within a row when R >= 64, on the
@@ -64,6 +72,7 @@ struct ProductCfg {
   static constexpr int STAGE_FLOATS = STAGES * (A_STAGE + B_STAGE);
   static constexpr int RED_FLOATS = (KS - 1) * BM * BN;
   static constexpr int OUT_FLOATS = SPATIAL * 32 * WN;
+  static constexpr bool LINES = BM * BN < 256 * 256;   // the k-fast layout
   static constexpr int max3(int a, int b, int c) {
     return a > b ? (a > c ? a : c) : (b > c ? b : c);
   }
@@ -81,11 +90,22 @@ template <int n>   // at most n vector-memory operations left
 constexpr int kWaitLoads = (n & 0xF) | (0x7 << 4) | (0xF << 8) | ((n >> 4) << 14);
 constexpr int kWaitLds = 0xF | (0x7 << 4) | (0x3 << 14);
 
+// What a k-fast row's k groups are xor-ed with: sixteen consecutive rows take the
+// sixteen 16-byte units of 64 banks for every k group.
+template <int CPR>
+__device__ __forceinline__ int fast_swizzle(int r) {
+  static_assert(CPR == 4 || CPR == 8 || CPR == 16, "16, 32 or 64 values of k a slab");
+  return (r / (16 / CPR)) & (CPR - 1);
+}
+
 // Where one operand's unit u of a slab stage comes from: for k fast the row
 // (of the tile) and k group, for k slow the k and the 4-float group.
-template <bool FAST, int R, int CPR>
+template <bool FAST, int R, int CPR, bool LINES>
 __device__ __forceinline__ void unit_source(int u, int& r, int& k) {
-  if constexpr (FAST) {
+  if constexpr (FAST && LINES) {
+    r = u / CPR;
+    k = 4 * ((u % CPR) ^ fast_swizzle<CPR>(r));
+  } else if constexpr (FAST) {
     r = (u / (16 * CPR)) * 16 + (u & 15);
     k = 4 * ((u >> 4) % CPR);
   } else {
@@ -368,13 +388,13 @@ product_kernel(ProductArgs g) {
 #pragma unroll
   for (int s = 0; s < Cfg::A_SLOTS; ++s) {
     int r, k;
-    unit_source<AFAST, BM, CPR>(s * NT + 64 * wave + lane, r, k);
+    unit_source<AFAST, BM, CPR, Cfg::LINES>(s * NT + 64 * wave + lane, r, k);
     a_off[s] = offset(AFastT(), r, k, m_left, g.lda);
   }
 #pragma unroll
   for (int s = 0; s < Cfg::B_SLOTS; ++s) {
     int r, k;
-    unit_source<BFAST, BN, CPR>(s * NT + 64 * wave + lane, r, k);
+    unit_source<BFAST, BN, CPR, Cfg::LINES>(s * NT + 64 * wave + lane, r, k);
     b_off[s] = offset(BFastT(), r, k, n_left, g.ldb);
   }
   // The resources of the slab from k0 (< K) on.
@@ -419,7 +439,7 @@ product_kernel(ProductArgs g) {
 #pragma unroll
       for (int s = 0; s < slots; ++s) {
         int r, k;
-        unit_source<true, decltype(extent)::value, CPR>(s * NT + 64 * wave + ln, r, k);
+        unit_source<true, decltype(extent)::value, CPR, Cfg::LINES>(s * NT + 64 * wave + ln, r, k);
         k += t * BK;
         if (k + 4 > K && r < left) {
           f32x4* unit = reinterpret_cast<f32x4*>(stage + 4 * (s * NT + 64 * wave + ln));
@@ -450,12 +470,13 @@ product_kernel(ProductArgs g) {
                       int sub, int h) {
     constexpr int R = decltype(extent)::value;
     if constexpr (decltype(fast)::value) {
+      // Either layout repeats every 32 rows.
+      const int c = 4 * sub + 2 * lh + h;
+      const int unit = Cfg::LINES ? (w0 + li) * CPR + (c ^ fast_swizzle<CPR>(li))
+                                  : w0 * CPR + (li >> 4) * (16 * CPR) + (li & 15) + 16 * c;
 #pragma unroll
-      for (int i = 0; i < T; ++i) {
-        const int r = w0 + 32 * i + li;
-        out[i] = *reinterpret_cast<const f32x4*>(
-            stage + 4 * ((r >> 4) * (16 * CPR) + (r & 15) + 16 * (4 * sub + 2 * lh + h)));
-      }
+      for (int i = 0; i < T; ++i)
+        out[i] = *reinterpret_cast<const f32x4*>(stage + 4 * (unit + 32 * i * CPR));
     } else {
       // One lane offset (two for R = 32, whose xor moves to the neighbouring
       // row), so that the k steps are immediates of the reads.

@@ -155,7 +155,7 @@ def test_linear_integers_are_exact():
 
 
 # Cut in two launches: by rows (one, a few by the vector kernels, many), by columns.
-CUTS = [(2049, 4096, 1000), (2053, 4096, 1024), (2100, 4096, 1001), (2048, 4104, 1024),
+CUTS = [(2049, 4096, 1000), (2053, 4096, 1024), (2100, 4096, 4001), (2048, 4104, 1024),
         (4096, 4097, 1000), (4200, 4096, 1500)]
 
 
@@ -495,8 +495,8 @@ def lib():
     (0, 1, 1, 4096, 4096, "rows_fast_1x16"), (0, 1, 1, 1024, 4096, "rows_fast_1x4"),
     (0, 1, 12, 4096, 4096, "rows_fast_8x16"), (0, 0, 5, 4096, 4096, "rows_slow_8x16"),
     (0, 0, 2, 32768, 1024, "rows_slow_2x64"), (0, 0, 9, 4096, 4096, "rows_slow_8x32"),
-    (0, 0, 17, 4096, 4096, "product_fs_32x64x32_ks2_s4"),
-    (1, 0, 1, 4096, 4096, "product_ss_32x64x32_ks2_s4")])
+    (0, 0, 17, 4096, 4096, "product_fs_32x64x64_ks4"),
+    (1, 0, 1, 4096, 4096, "product_ss_32x64x64_ks4")])
 def test_plans_without_workspace(lib, ta, tb, M, N, K, kernel):
     st, plan = sg.sgemm_linear_plan_query(ta, tb, M, N, K)
     assert st == sg.OK and plan.kernel.decode() == kernel

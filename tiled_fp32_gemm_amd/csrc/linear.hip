@@ -197,34 +197,50 @@ int64_t grid_tiles(const ProductArgs& g, const sg::host::TileCost& c) {
   return cdiv(g.M, c.tile_m) * tn * g.groups;
 }
 
-// Whole tiles' worth of work.  A row group's last tile has, on average, half a
-// wave's rows of padding: waves without rows leave the others their share.
-int64_t likely_tiles(const ProductArgs& g, const sg::host::TileCost& c) {
-  if (g.mode != sg::kRowGroups) return grid_tiles(g, c);
-  const int64_t live = live_groups(g);
-  const int64_t wave_rows = c.tile_m >= 256 ? 64 : 32;
-  const int64_t rows = (2 * g.M + live * wave_rows) / (2 * c.tile_m);
-  return (rows > live ? rows : live) * cdiv(g.N, c.tile_n);
+// The estimate for `level` tiles on the busiest CU, between whole numbers of them.
+double estimate_level(const sg::host::TileCost& c, double level, int64_t K) {
+  const int64_t n = level < 1 ? 1 : (int64_t)level;
+  const double less = estimate_grid(c, n * kCUs, K);
+  return level <= n ? less : less + (level - n) * (estimate_grid(c, (n + 1) * kCUs, K) - less);
 }
 
-// Estimated seconds of `tiles` workgroups over K.  The tiles of row groups differ
-// and are handed out as workgroups end, so a last round that is partly filled
-// counts in part, and some more for its uneven end (less for the tiles that are
-// handed out longest first).
-double likely_time(const ProductArgs& g, const sg::host::TileCost& c, int64_t tiles, int64_t K) {
-  const double t = estimate_grid(c, tiles, K);
-  // Summed groups in one round take as long as the longest.
-  if (g.mode == sg::kSumGroups && g.groups > 1 && tiles <= kCUs * c.occ) return 1.25 * t;
-  const int64_t full = tiles / kCUs, rest = tiles % kCUs;
-  if (g.mode != sg::kRowGroups || full == 0 || rest == 0) return t;
-  const double part = (double)rest / kCUs + (c.tile_m >= 128 ? 0.1 : 0.3);
-  const double less = estimate_grid(c, full * kCUs, K);
-  return part >= 1.0 ? t : less + part * (t - less);
+// Estimated seconds of a grid in `splits` parts of K each.  The lengths of
+// groups are not known here, and their tiles are handed out as workgroups end:
+// row groups are taken as 0.4, 0.7, 1, 1.3 and 1.6 times the average, which gives
+// the tiles and, in a wave's rows (waves without rows leave the others their
+// share), the work; the busiest CU has its share of the work and a part of a
+// tile more.  Summed groups: the same, or, in one round, the longest.  The
+// figures are fitted to 24 sets of uneven groups, 16 to 65536 rows in 4 to 128
+// of them: the choice is 1.6% behind the fastest on average, 20% at worst.
+double likely_time(const ProductArgs& g, const sg::host::TileCost& c, int64_t splits, int64_t K) {
+  const int64_t tiles = grid_tiles(g, c) * splits;
+  if (g.mode == sg::kDense || g.groups <= 1 || tiles == 0) return estimate_grid(c, tiles, K);
+  if (g.mode == sg::kSumGroups)
+    return tiles <= kCUs ? 1.2 * estimate_grid(c, tiles, K)
+                         : estimate_level(c, (double)tiles / kCUs + (g.groups <= 16 ? 0.6 : 1.0), K);
+  const int64_t live = live_groups(g), wave_rows = c.tile_m >= 256 ? 64 : 32;
+  int64_t likely = 0, waves = 0;   // of five groups
+  for (int i = 4; i <= 16; i += 3) {
+    const int64_t rows = cdiv((int64_t)g.M * i, 10 * live);
+    likely += cdiv(rows, c.tile_m);
+    waves += cdiv(rows, wave_rows);
+  }
+  const double all = (double)live / 5.0 * (double)(cdiv(g.N, c.tile_n) * splits);
+  const double more = c.tile_m >= 128 ? 1.2 : c.tile_m >= 64 ? 1.16 : 1.06;
+  const double count = 1.13 * all * likely, work = more * all * waves * wave_rows / c.tile_m;
+  if (count <= kCUs) return estimate_grid(c, (int64_t)count, K);
+  const double level = work / kCUs + (c.tile_m >= 128 ? 0.3 : 0.4);
+  const double most = (double)cdiv((int64_t)count, kCUs);
+  return estimate_level(c, level < most ? level : most, K);
 }
+
+// What a split costs beside its tiles and its planes' traffic, fitted with the
+// tiles' figures: the part of a grid's time that remains when it need not end
+// with C, a second launch, and that one's wait for each plane.
+constexpr double kSplitPart = 0.93, kSplitFixed = 3.5e-6, kSplitPlane = 0.08e-6;
 
 // The variant, and the split of K, with the least estimated time (the model
-// of host.hpp; the costs of a split are those sgemm_ws was fitted with).  A
-// null v: no variant can address this product.
+// of host.hpp).  A null v: no variant can address this product.
 Choice choose(const Product& p, int64_t ws_bytes) {
   const ProductArgs& g = p.g;
   const ProductVariant* table = variants(p.trans_a, p.trans_b);
@@ -238,18 +254,18 @@ Choice choose(const Product& p, int64_t ws_bytes) {
     const ProductVariant& v = table[i];
     const int64_t grid = grid_tiles(g, v.cost);
     if (!variant_fits(p, v) || !grid_fits(grid, v.cost.threads)) continue;
-    const double t = likely_time(g, v.cost, likely_tiles(g, v.cost), K);
+    const double t = likely_time(g, v.cost, 1, K);
     if (one.v == nullptr || t < t_one * 0.995) {
       one = {&v, 1, 0, grid, t};
       t_one = t;
     }
   }
   // A split takes the fixed costs of a round and of a second launch at least.
-  if (one.v == nullptr || t_one < kRoundCost + kReduceFixed || 2 * out > ws_bytes / 4) return one;
+  if (one.v == nullptr || t_one < kRoundCost + kSplitFixed || 2 * out > ws_bytes / 4) return one;
   for (int i = 0; i < sg::kProductVariants; ++i) {
     const ProductVariant& v = table[i];
     const sg::host::TileCost& c = v.cost;
-    const int64_t grid = grid_tiles(g, c), likely = likely_tiles(g, c);
+    const int64_t grid = grid_tiles(g, c);
     if (K < 2 * c.tile_k || !variant_fits(p, v)) continue;
     for (int S : kSplits) {
       // Few tiles and a long K: 64 x 64 x 65536 in 32 splits 29.1 us, in 64 22.9; the
@@ -260,9 +276,8 @@ Choice choose(const Product& p, int64_t ws_bytes) {
       if (se < 2 || se * out > ws_bytes / 4 || !grid_fits(grid * se, c.threads) ||
           !grid_fits(out / g.N * cdiv(g.N, sg::kProductReduceCols), 64))
         continue;
-      const double ts = 0.95 * likely_time(g, c, likely * se, ks) + kReduceFixed +
-                        (double)(se + 1) * out * 4.0 / kReduceBW +
-                        (se > 32 ? 0.06e-6 * (se - 32) : 0.0);   // the planes' latency
+      const double ts = kSplitPart * likely_time(g, c, se, ks) + kSplitFixed +
+                        kSplitPlane * se + (double)(se + 1) * out * 4.0 / kReduceBW;
       if (split.v == nullptr || ts < t_split) {
         split = {&v, (int)se, (int)ks, grid * se, ts};
         t_split = ts;
@@ -399,18 +414,18 @@ Product part_of(const Product& whole, bool columns, int64_t from, int64_t count)
   return p;
 }
 
-// The cut with the least estimated time, if it is 6% under the uncut product's:
+// The cut with the least estimated time, if it is 4% under the uncut product's:
 // whole rounds of one of the three largest tiles, and the rest.  Not asked
 // where the whole is short or near what the chip can do anyway.  Measured on
-// MI355X (us, one launch / cut; K x N weight, N = K = 4096): M = 4097 1094 / 971, 4200
-// 1077 / 996, 8200 1977 / 1845; N x K, M = 2049 721 / 480.
+// MI355X (us, one launch / cut): 4097 x 4096 x 4096 1020 / 923, 8200 x 4096 x
+// 4096 1992 / 1840, 16385 x 1024 x 1024 of an N x K weight 265 / 243.
 Cut find_cut(const Product& p, const Step& whole, int64_t ws_bytes) {
   const ProductArgs& g = p.g;
   Cut best = {0, false};
   if (g.mode != sg::kDense || whole.rows.rows > 0 || whole.tile.v == nullptr) return best;
   const double t_whole = whole.tile.seconds;
   if (t_whole < 60e-6 || t_whole < 1.04 * 2.0 * g.M * g.N * g.K / 150e12) return best;
-  double t_best = 0.94 * t_whole;
+  double t_best = 0.96 * t_whole;
   const ProductVariant* table = variants(p.trans_a, p.trans_b);
   for (int i = 0; i < 3; ++i) {
     const sg::host::TileCost& c = table[i].cost;

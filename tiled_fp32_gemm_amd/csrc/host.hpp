@@ -68,6 +68,7 @@ struct TileCost {
   int occ;      // workgroups a CU holds at once
   double slab_floor = kSlabFloor;   // s a slab takes however little it computes
   double saturate = kSaturate;      // waves per SIMD that keep the pipes busy
+  double round_more = 0.0;          // s a round takes beside kRoundCost
 };
 
 // Estimated seconds of a tile variant on an M x N x K product.  Workgroups are
@@ -88,7 +89,8 @@ inline double estimate_grid(const TileCost& v, int64_t tiles, int64_t K) {
     const double simd = r * waves / 4.0;
     const double busy = simd >= v.saturate ? 1.0 : simd / v.saturate;
     const double compute = r * slab_flops / (kPeakPerCU * v.eff * busy);
-    return (double)slabs * (compute > v.slab_floor ? compute : v.slab_floor) + kRoundCost;
+    return (double)slabs * (compute > v.slab_floor ? compute : v.slab_floor) + kRoundCost +
+           v.round_more;
   };
   const int64_t full = n / v.occ, rest = n % v.occ;
   double t = (double)full * round(v.occ) + (rest > 0 ? round(rest) : 0.0);

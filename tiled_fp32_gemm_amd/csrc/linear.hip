@@ -284,7 +284,7 @@ Choice choose(const Product& p, int64_t ws_bytes) {
       }
     }
   }
-  return split.v != nullptr && t_split < t_one * 0.97 ? split : one;
+  return split.v != nullptr && t_split < t_one * 0.95 ? split : one;
 }
 
 int64_t split_bytes(const ProductArgs& g, const Choice& ch) {

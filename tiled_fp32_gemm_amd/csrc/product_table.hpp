@@ -14,9 +14,9 @@ namespace sg {
 
 template <int BM, int BN, int WM, int WN, int BK, int KS, int ST, bool AF, bool BF>
 ProductVariant product_variant(const char* name, double eff, int occ, double slab_floor,
-                               double saturate = 1.0) {
+                               double saturate = 1.0, double round_more = 0.0) {
   using Cfg = ProductCfg<BM, BN, WM, WN, BK, KS, ST>;
-  return {name, {BM, BN, BK, Cfg::NT, eff, occ, slab_floor, saturate}, Cfg::LDS_FLOATS * 4,
+  return {name, {BM, BN, BK, Cfg::NT, eff, occ, slab_floor, saturate, round_more}, Cfg::LDS_FLOATS * 4,
           product_kernel<BM, BN, WM, WN, BK, KS, ST, AF, BF>};
 }
 
@@ -30,7 +30,8 @@ const ProductVariant* product_variants() {
       product_variant<64, 64, 32, 32, 32, 1, 2, AF, BF>("64x64x32", 0.915, 5, 0.50e-6),
       product_variant<64, 64, 32, 32, 32, 2, 2, AF, BF>("64x64x32_ks2", 0.895, 4, 0.56e-6),
       product_variant<32, 64, 32, 32, 32, 2, 2, AF, BF>("32x64x32_ks2", 0.840, 6, 0.34e-6, 1.28),
-      product_variant<32, 64, 32, 32, 64, 4, 2, AF, BF>("32x64x64_ks4", 0.855, 3, 0.56e-6),
+      product_variant<32, 64, 32, 32, 64, 4, 2, AF, BF>("32x64x64_ks4", 0.855, 3, 0.56e-6, 1.0,
+                                                        0.25e-6),
       product_variant<64, 64, 32, 32, 32, 1, 3, AF, BF>("64x64x32_s3", 0.890, 3, 0.58e-6),
       product_variant<32, 64, 32, 32, 32, 2, 4, AF, BF>("32x64x32_ks2_s4", 0.840, 3, 0.32e-6)};
   return table;

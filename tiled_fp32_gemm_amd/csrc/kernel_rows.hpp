@@ -20,7 +20,7 @@
 // Measured on MI355X (kernel trace; B of 64 MiB, 4096 x 4096, from HBM, one row
 // with bias and SILU) before the loads were nontemporal: fast 13.4 us (KW = 4:
 // 16.2), slow 15.4 us at 16 columns a workgroup (32: 17.6, 64: 29: too few
-// workgroups); product_kernel with its second launch takes 20.4 and 21.9 us.  2,
+// workgroups); product_kernel with its second launch takes 19.5 and 20.8 us.  2,
 // 4 and 8 rows cost 13 to 16 us.
 //
 // B is loaded nontemporal (one row by 4096 x 4096: 14.2 -> 12.7 us, 8192 x 8192:

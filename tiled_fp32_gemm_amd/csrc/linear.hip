@@ -300,18 +300,23 @@ struct RowsChoice {
 };
 
 // Measured on MI355X against product_kernel with a workspace (us, rows /
-// product; N = K = 4096, and groups of N = 4096, K = 1024):
-//      B stored           N x K             K x N
-//      4 rows           15.0 / 20.1       15.0 / 18.3
-//      8 rows           17.4 / 20.0       17.5 / 18.9
-//      16 rows          22.5 / 20.3       24.5 / 19.1
-//      16 rows, 1024 x 1024   4.6 / 9.4    5.6 / 9.2
-//      groups, avg. 1   17.0 / 22.6       18.7 / 21.3
-//      groups, avg. 4   27.0 / 33.4       26.0 / 31.5
-//      groups, avg. 5   31.8 / 36.3       35.1 / 32.2
-//      groups, avg. 8   38.0 / 36.1       37.8 / 33.1
-// Without room to split, 16 rows are the faster way as well (product_kernel 42
-// and 45).  Columns a workgroup: the most that still give every CU one.
+// product; B from HBM, the groups' rows drawn at random, E x K x N):
+//      B stored                 N x K                       K x N
+//      4 rows, 4096 x 4096   15.3 / 19.5                 20.5 / 20.8
+//      8 rows                17.8 / 19.5                 22.0 / 20.8
+//      16 rows               22.0 / 19.8                 30.2 / 21.1
+//      1 row, 11008 x 4096   30.4 / 43.5                 44.4 / 41.8
+//      8 rows                38.2 / 43.9                 48.2 / 42.2
+//      16 rows, 2048 x 2048  10.5 / 11.3                 10.5 / 11.2
+//      groups, on average    2       4       6            1       2       4
+//      8 x 1024 x 4096     23/32   28/34   33/36        20/26   23/28   27/29
+//      64 x 1024 x 1024    41/59   52/64   60/67        34/36   42/47   54/52
+//      16 x 2048 x 2048    41/51   51/57   64/61        34/40   40/45   50/48
+//      8 x 4096 x 1024     23/27   27/30   39/31        26/23   30/27   35/32
+// Without room to split, up to 16 rows are the faster way unless the product's
+// own tiles fill half the chip (16 rows, N = 4096: 22 / 50, N = 11008: 64 / 56; N
+// = 8192, K = 1024 13 / 16 and, K x N, 17 / 15).
+// Columns a workgroup: the most that still give every CU one.
 RowsChoice choose_rows(const Product& p) {
   const ProductArgs& g = p.g;
   RowsChoice none = {0, 0, 0};
@@ -320,7 +325,10 @@ RowsChoice choose_rows(const Product& p) {
   if (p.trans_a || g.mode == sg::kSumGroups || g.K >= 1 << 29) return none;
   const bool grouped = g.mode == sg::kRowGroups;
   const int64_t live = grouped ? live_groups(g) : 1;
-  const int64_t most = grouped ? (p.trans_b ? 6 : 4) * live : 2 * sg::kRowsMost;
+  const int64_t wide = g.N, deep = g.K;
+  const int64_t average = p.trans_b ? (wide >= deep ? 6 : 4)
+                                    : wide >= 2 * deep ? 4 : 2 * wide >= deep ? 2 : 0;
+  const int64_t most = grouped ? average * live : 2 * sg::kRowsMost;
   if (g.M > most && g.M > sg::kRowsMost) return none;
   // A chunk has room for a group of twice the average.
   const int64_t want = grouped ? cdiv(2 * g.M, live) : g.M;
@@ -337,9 +345,12 @@ RowsChoice choose_rows(const Product& p) {
   return grid_fits(ch.workgroups, 256) ? ch : none;
 }
 
-// Two chunks of rows over a B that the caches do not hold: see choose_rows.
-bool many_rows(const ProductArgs& g) {
-  return g.mode == sg::kDense && g.M > sg::kRowsMost && (int64_t)g.N * g.K > 1 << 22;
+// Where a split, if there is room for one, is faster than so many rows over a B
+// that the caches do not hold: see choose_rows.
+bool many_rows(const Product& p) {
+  const int64_t size = (int64_t)p.g.N * p.g.K;
+  return p.g.mode == sg::kDense &&
+         ((p.g.M > sg::kRowsMost && size > 1 << 22) || (!p.trans_b && size > 1 << 24));
 }
 
 // Few columns over a long K leave the chip idle by rows, where a split product
@@ -350,10 +361,13 @@ bool many_rows(const ProductArgs& g) {
 //      B stored K x N   64 x 16384   256 x 4096   1024 x 8192   1024 x 1024
 //      1 row             25.2 / 13.1    6.1 / 9.3    18.2 / 12.9    4.5 / 9.0
 //      8 rows            58.2 / 13.3   13.0 / 9.8    28.8 / 12.9    5.5 / 9.2
-bool rather_split(const Product& p, const RowsChoice& rows, const Choice& ch) {
-  if (ch.v == nullptr || ch.splits == 1) return false;
+bool rather_tiles(const Product& p, const RowsChoice& rows, const Choice& ch) {
+  if (ch.v == nullptr) return false;
+  if (many_rows(p))
+    return ch.splits > 1 || (p.g.M > sg::kRowsMost && cdiv(p.g.N, 64) >= kCUs / 2 &&
+                             (!p.trans_b || (int64_t)p.g.N * p.g.K > 1 << 24));
+  if (ch.splits == 1) return false;
   const int64_t K = p.g.K;
-  if (many_rows(p.g)) return true;
   return p.trans_b ? rows.workgroups < 64 && K * rows.rows > 196608
                    : rows.workgroups <= kCUs / 2 && K * (rows.rows + 2) > 12288;
 }
@@ -368,9 +382,9 @@ Step decide(const Product& p, int64_t ws_bytes) {
   const RowsChoice rows = choose_rows(p);
   Step s = {{0, 0, 0}, {nullptr, 1, 0, 0, 0.0}};
   // Only many rows, or a long K over few columns, ask what a split would be.
-  if (rows.rows == 0 || many_rows(p.g) || (p.g.K > 1024 && rows.workgroups <= kCUs / 2))
+  if (rows.rows == 0 || many_rows(p) || (p.g.K > 1024 && rows.workgroups <= kCUs / 2))
     s.tile = choose(p, ws_bytes);
-  if (rows.rows > 0 && !rather_split(p, rows, s.tile)) s.rows = rows;
+  if (rows.rows > 0 && !rather_tiles(p, rows, s.tile)) s.rows = rows;
   return s;
 }
 

@@ -4,10 +4,10 @@
 //
 // Such a product is bound by reading B (2 R flop a float for R rows, where the
 // chip has 32 flop for each float of HBM bandwidth), so what counts is bytes in
-// flight: a workgroup of four waves takes a few columns and splits K over its
-// threads, each with several 16-byte groups in flight, and the partial sums
-// meet once at the end, first within the waves, then through LDS in wave order.
-// No second launch and no workspace.  A (R rows) comes from the caches.
+// flight: a workgroup of four or eight waves takes a few columns and splits K
+// over its threads, each with several 16-byte groups in flight, and the partial
+// sums meet once at the end, first within the waves, then through LDS in wave
+// order.  No second launch and no workspace.  A (R rows) comes from the caches.
 //
 //   rows_fast_kernel   B is N x K: a wave takes four columns (four rows of B),
 //                      its lanes 256 consecutive k at a time.  KW = 1: each of
@@ -17,11 +17,11 @@
 //   rows_slow_kernel   B is K x N: LC lanes take 4 LC consecutive columns of
 //                      four consecutive k rows, the others further k.
 //
-// Measured on MI355X (kernel trace; B of 64 MiB, 4096 x 4096, from HBM, one row
-// with bias and SILU) before the loads were nontemporal: fast 13.4 us (KW = 4:
-// 16.2), slow 15.4 us at 16 columns a workgroup (32: 17.6, 64: 29: too few
-// workgroups); product_kernel with its second launch takes 19.5 and 20.8 us.  2,
-// 4 and 8 rows cost 13 to 16 us.
+// Measured on MI355X (B of 64 MiB, 4096 x 4096, from HBM, one row): fast 12.5 us
+// (KW = 4 16.2), slow 18.2 us at 16 columns a workgroup and eight waves (four:
+// 18.8; 32 columns 19.1, 64: 24.6, too few workgroups); product_kernel with its
+// second launch takes 19.5 and 20.8 us.  11008 x 4096: fast 30.4 us (5.9 TB/s), slow
+// 32.2 at 64 columns (four waves: 42.9; 32 columns 43.2).
 //
 // B is loaded nontemporal (one row by 4096 x 4096: 14.2 -> 12.7 us, 8192 x 8192:
 // 45 -> 43 us, 6.2 TB/s), but for the slow kernel's narrow blocks, whose
@@ -163,13 +163,13 @@ __global__ void __launch_bounds__(kRowsThreads) rows_fast_kernel(ProductArgs g) 
                KW == 4 ? ((part[0][i] + part[1][i]) + part[2][i]) + part[3][i] : part[wave][i]);
 }
 
-template <int R, int LC>
-__global__ void __launch_bounds__(kRowsThreads) rows_slow_kernel(ProductArgs g) {
+template <int R, int LC, int T>
+__global__ void __launch_bounds__(T) rows_slow_kernel(ProductArgs g) {
   constexpr int V = 4 * R;
-  constexpr int KR = kRowsThreads / LC;   // groups of four k rows at a time
+  constexpr int KR = T / LC;   // groups of four k rows at a time
   constexpr int SHARE = 64 / LC;          // of them in a wave
   constexpr int LEFT = V > SHARE ? V / SHARE : 1;   // values a lane ends with
-  __shared__ float part[4][V * LC];
+  __shared__ float part[T / 64][V * LC];
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
   RowsPlace p;
   if (!rows_place<R>(g, p)) return;
@@ -228,11 +228,15 @@ __global__ void __launch_bounds__(kRowsThreads) rows_slow_kernel(ProductArgs g) 
     }
   }
   __syncthreads();
-  for (int i = tid; i < V * LC; i += kRowsThreads) {
+  for (int i = tid; i < V * LC; i += T) {
     // Consecutive threads take consecutive columns of a row.
     const int r = i / (4 * LC), c = i % (4 * LC);
-    if (r < p.rows && n0 + c < g.N)
-      finish_one(g, p, r, n0 + c, ((part[0][i] + part[1][i]) + part[2][i]) + part[3][i]);
+    if (r < p.rows && n0 + c < g.N) {
+      float z = part[0][i];
+#pragma unroll
+      for (int w = 1; w < T / 64; ++w) z += part[w][i];
+      finish_one(g, p, r, n0 + c, z);
+    }
   }
 }
 

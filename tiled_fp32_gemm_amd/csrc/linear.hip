@@ -295,54 +295,57 @@ int64_t split_bytes(const ProductArgs& g, const Choice& ch) {
 // The kernels for a few rows (kernel_rows.hpp): rows a chunk, columns a
 // workgroup; rows 0: not for this product.
 struct RowsChoice {
-  int rows, cols;
+  int rows, cols, threads;
   int64_t workgroups;
 };
 
 // Measured on MI355X against product_kernel with a workspace (us, rows /
 // product; B from HBM, the groups' rows drawn at random, E x K x N):
 //      B stored                 N x K                       K x N
-//      4 rows, 4096 x 4096   15.3 / 19.5                 20.5 / 20.8
-//      8 rows                17.8 / 19.5                 22.0 / 20.8
-//      16 rows               22.0 / 19.8                 30.2 / 21.1
-//      1 row, 11008 x 4096   30.4 / 43.5                 44.4 / 41.8
-//      8 rows                38.2 / 43.9                 48.2 / 42.2
-//      16 rows, 2048 x 2048  10.5 / 11.3                 10.5 / 11.2
-//      groups, on average    2       4       6            1       2       4
-//      8 x 1024 x 4096     23/32   28/34   33/36        20/26   23/28   27/29
-//      64 x 1024 x 1024    41/59   52/64   60/67        34/36   42/47   54/52
-//      16 x 2048 x 2048    41/51   51/57   64/61        34/40   40/45   50/48
-//      8 x 4096 x 1024     23/27   27/30   39/31        26/23   30/27   35/32
+//      1 row, 4096 x 4096    12.8 / 19.5                 18.2 / 21.8
+//      4 rows                15.3 / 19.5                 19.2 / 20.9
+//      8 rows                17.8 / 19.5                 21.0 / 20.8
+//      16 rows               22.0 / 19.8                 22.3 / 21.1
+//      8 rows, 11008 x 4096  38.2 / 43.9                 40.1 / 42.0
+//      1 row, 4096 x 11008   30.4 / 47.9                 44.1 / 40.0
+//      16 rows, 8192 x 1024  13.4 / 14.1                 12.2 / 13.8
+//      16 rows, 2048 x 2048  10.5 / 11.3                 10.1 / 11.2
+//      groups, on average    2       4       6            2       3       4
+//      8 x 1024 x 4096     23/32   28/34   33/36        23/28   26/28   27/29
+//      8 x 4096 x 1024     23/27   27/30   39/31        27/27   28/30   29/32
+//      16 x 2048 x 2048    41/51   51/57   64/61        40/45   45/46   50/48
+//      64 x 1024 x 1024    41/59   52/64   60/67        42/46   53/50   54/52
 // Without room to split, up to 16 rows are the faster way unless the product's
-// own tiles fill half the chip (16 rows, N = 4096: 22 / 50, N = 11008: 64 / 56; N
-// = 8192, K = 1024 13 / 16 and, K x N, 17 / 15).
-// Columns a workgroup: the most that still give every CU one.
+// own tiles fill half the chip (16 rows, N = 4096: 22 / 50, N = 11008: 64 / 56).
+// Columns a workgroup, K x N: the most that still give 5/8 of the CUs one, and
+// eight waves for fewer than two a CU (4 rows, us, at 16, 32 and 64 columns with
+// four / eight waves: N = K = 4096 20.1 / 19.1, 25.4 / 20.8, 43 / 27; 11008 x 4096
+// 55 / 43, 45 / 49, 48 / 34; 32768 x 1024 32 / 33, 28 / 27, 21.6 / 22.5).
 RowsChoice choose_rows(const Product& p) {
   const ProductArgs& g = p.g;
-  RowsChoice none = {0, 0, 0};
+  RowsChoice none = {0, 0, 0, 0};
   // The kernels count k in ints, some way past K; a row that long is refused by
   // product_kernel's spans as well.
   if (p.trans_a || g.mode == sg::kSumGroups || g.K >= 1 << 29) return none;
   const bool grouped = g.mode == sg::kRowGroups;
   const int64_t live = grouped ? live_groups(g) : 1;
-  const int64_t wide = g.N, deep = g.K;
-  const int64_t average = p.trans_b ? (wide >= deep ? 6 : 4)
-                                    : wide >= 2 * deep ? 4 : 2 * wide >= deep ? 2 : 0;
+  const int64_t average = p.trans_b ? (g.N >= g.K ? 6 : 4) : live <= 8 ? 4 : 3;
   const int64_t most = grouped ? average * live : 2 * sg::kRowsMost;
   if (g.M > most && g.M > sg::kRowsMost) return none;
   // A chunk has room for a group of twice the average.
   const int64_t want = grouped ? cdiv(2 * g.M, live) : g.M;
-  RowsChoice ch = {1, p.trans_b ? 16 : 64, 0};
+  RowsChoice ch = {1, p.trans_b ? 16 : 64, 256, 0};
   while (ch.rows < sg::kRowsMost && ch.rows < want && ch.rows < g.M) ch.rows *= 2;
   const int64_t chunks = grouped ? live : cdiv(g.M, ch.rows);
   if (p.trans_b) {
     if (cdiv(g.N, 16) * chunks < kCUs) ch.cols = 4;
   } else {
-    while (ch.cols > 16 && cdiv(g.N, ch.cols) * chunks < kCUs) ch.cols /= 2;
+    while (ch.cols > 16 && cdiv(g.N, ch.cols) * chunks < kCUs * 5 / 8) ch.cols /= 2;
+    if (cdiv(g.N, ch.cols) * chunks < 2 * kCUs) ch.threads = 512;
   }
   const sg::host::TileCost c = {ch.rows, ch.cols, 0, 0, 0, 0, 0, 0};
   ch.workgroups = grid_tiles(g, c);
-  return grid_fits(ch.workgroups, 256) ? ch : none;
+  return grid_fits(ch.workgroups, ch.threads) ? ch : none;
 }
 
 // Where a split, if there is room for one, is faster than so many rows over a B
@@ -350,7 +353,8 @@ RowsChoice choose_rows(const Product& p) {
 bool many_rows(const Product& p) {
   const int64_t size = (int64_t)p.g.N * p.g.K;
   return p.g.mode == sg::kDense &&
-         ((p.g.M > sg::kRowsMost && size > 1 << 22) || (!p.trans_b && size > 1 << 24));
+         ((p.g.M > sg::kRowsMost && size > 1 << 23) ||
+          (!p.trans_b && size > 1 << 24 && cdiv(p.g.N, 64) < kCUs * 5 / 8));
 }
 
 // Few columns over a long K leave the chip idle by rows, where a split product
@@ -365,7 +369,7 @@ bool rather_tiles(const Product& p, const RowsChoice& rows, const Choice& ch) {
   if (ch.v == nullptr) return false;
   if (many_rows(p))
     return ch.splits > 1 || (p.g.M > sg::kRowsMost && cdiv(p.g.N, 64) >= kCUs / 2 &&
-                             (!p.trans_b || (int64_t)p.g.N * p.g.K > 1 << 24));
+                             (int64_t)p.g.N * p.g.K > 1 << 24);
   if (ch.splits == 1) return false;
   const int64_t K = p.g.K;
   return p.trans_b ? rows.workgroups < 64 && K * rows.rows > 196608
@@ -380,7 +384,7 @@ struct Step {
 
 Step decide(const Product& p, int64_t ws_bytes) {
   const RowsChoice rows = choose_rows(p);
-  Step s = {{0, 0, 0}, {nullptr, 1, 0, 0, 0.0}};
+  Step s = {{0, 0, 0, 0}, {nullptr, 1, 0, 0, 0.0}};
   // Only many rows, or a long K over few columns, ask what a split would be.
   if (rows.rows == 0 || many_rows(p) || (p.g.K > 1024 && rows.workgroups <= kCUs / 2))
     s.tile = choose(p, ws_bytes);
@@ -473,8 +477,9 @@ int launch_step(Product& p, const Step& s, hipStream_t stream, void* ws) {
   g.group_m = g.tiles_m < 8 ? g.tiles_m : 8;
   if (s.rows.rows > 0) {
     const hipError_t e = hipLaunchKernel(
-        reinterpret_cast<const void*>(sg::rows_kernel(p.trans_b, s.rows.rows, s.rows.cols)),
-        dim3((unsigned)s.rows.workgroups), dim3(256), args, 0, stream);
+        reinterpret_cast<const void*>(sg::rows_kernel(p.trans_b, s.rows.rows, s.rows.cols,
+                                                          s.rows.threads)),
+        dim3((unsigned)s.rows.workgroups), dim3(s.rows.threads), args, 0, stream);
     return e == hipSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH;
   }
   g.splits = s.tile.splits;
@@ -694,7 +699,7 @@ int sgemm_linear_plan_query(int trans_a, int trans_b, int64_t M, int64_t N, int6
     plan->algo = SGEMM_ALGO_FMA;
     plan->tile_m = s.rows.rows;
     plan->tile_n = s.rows.cols;
-    plan->threads = 256;
+    plan->threads = s.rows.threads;
     plan->workgroups = s.rows.workgroups;
     snprintf(plan->kernel, sizeof(plan->kernel), "rows_%s_%dx%d%s", trans_b ? "fast" : "slow",
              s.rows.rows, s.rows.cols, rest);

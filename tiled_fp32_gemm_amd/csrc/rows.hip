@@ -7,20 +7,21 @@ namespace sg {
 namespace {
 
 template <int R>
-ProductFn rows_variant(bool b_fast, int cols) {
+ProductFn rows_variant(bool b_fast, int cols, int threads) {
   if (b_fast) return cols == 16 ? rows_fast_kernel<R, 4, 1> : rows_fast_kernel<R, 4, 4>;
-  return cols == 16   ? rows_slow_kernel<R, 4>
-         : cols == 32 ? rows_slow_kernel<R, 8>
-                      : rows_slow_kernel<R, 16>;
+  return cols == 16       ? rows_slow_kernel<R, 4, 512>
+         : cols == 32     ? rows_slow_kernel<R, 8, 512>
+         : threads == 512 ? rows_slow_kernel<R, 16, 512>
+                          : rows_slow_kernel<R, 16, 256>;
 }
 
 }  // namespace
 
-ProductFn rows_kernel(bool b_fast, int rows, int cols) {
-  return rows == 1   ? rows_variant<1>(b_fast, cols)
-         : rows == 2 ? rows_variant<2>(b_fast, cols)
-         : rows == 4 ? rows_variant<4>(b_fast, cols)
-                     : rows_variant<8>(b_fast, cols);
+ProductFn rows_kernel(bool b_fast, int rows, int cols, int threads) {
+  return rows == 1   ? rows_variant<1>(b_fast, cols, threads)
+         : rows == 2 ? rows_variant<2>(b_fast, cols, threads)
+         : rows == 4 ? rows_variant<4>(b_fast, cols, threads)
+                     : rows_variant<8>(b_fast, cols, threads);
 }
 
 }  // namespace sg

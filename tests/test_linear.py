@@ -154,6 +154,28 @@ def test_linear_integers_are_exact():
                            want)
 
 
+# A shape of odd sizes for every tile, whatever the layouts.
+TILES = [("256x256x32", 7461, 3931, 45), ("128x128x32", 7208, 389, 47),
+         ("64x128x32", 513, 6694, 49), ("64x128x32_ks2", 8553, 69, 47),
+         ("64x64x32", 8663, 16, 45), ("32x64x32_ks2", 9098, 69, 47),
+         ("32x64x64_ks4", 33, 16, 163), ("32x64x32_ks2_s4", 35, 17, 45)]
+
+
+@pytest.mark.parametrize("ta,tb", [(0, 0), (0, 1), (1, 0), (1, 1)])
+@pytest.mark.parametrize("tile,M,N,K", TILES)
+def test_shapes_of_every_tile(lib, tile, M, N, K, ta, tb):
+    kernel = sg.sgemm_linear_plan_query(ta, tb, M, N, K)[1].kernel.decode()
+    assert kernel == f"product_{'sf'[not ta]}{'sf'[tb]}_{tile}"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ta,tb", [(False, False), (False, True), (True, False), (True, True)])
+@pytest.mark.parametrize("tile,M,N,K", TILES)
+def test_linear_every_tile(tile, M, N, K, ta, tb):
+    run_case(M, N, K, ta, tb, "gelu", pad=3, off=1)
+    run_case(M, N, K, ta, tb, "none", bias=False, residual=False, preact=False)
+
+
 # Cut in two launches: by rows (one, a few by the vector kernels, many), by columns.
 CUTS = [(2049, 4096, 1000), (2053, 4096, 1024), (2100, 4096, 4001), (2048, 4104, 1024),
         (4096, 4097, 1000), (4200, 4096, 1500)]

@@ -3,8 +3,8 @@
 // shapes (17 to 65536 rows, 100^3 to 4096^3) in all four layouts, each with
 // every tile and up to sixteen splits of K: the choice is 1% behind the fastest
 // on average, 6% at worst; the four layouts need no figures of their
-// own.  Two tiles keep three and two slabs in flight ("s4", "s3"), for grids
-// that leave CUs with a workgroup or two, where a slab costs its loads' latency.
+// own.  "s4" keeps three slabs in flight, for grids that leave CUs with a
+// workgroup or two, where a slab costs its loads' latency.
 #pragma once
 
 #include "kernel_product.hpp"
@@ -28,11 +28,9 @@ const ProductVariant* product_variants() {
       product_variant<64, 128, 32, 64, 32, 1, 2, AF, BF>("64x128x32", 0.940, 3, 0.50e-6, 1.28),
       product_variant<64, 128, 32, 64, 32, 2, 2, AF, BF>("64x128x32_ks2", 0.885, 3, 0.44e-6),
       product_variant<64, 64, 32, 32, 32, 1, 2, AF, BF>("64x64x32", 0.915, 5, 0.50e-6),
-      product_variant<64, 64, 32, 32, 32, 2, 2, AF, BF>("64x64x32_ks2", 0.895, 4, 0.56e-6),
       product_variant<32, 64, 32, 32, 32, 2, 2, AF, BF>("32x64x32_ks2", 0.840, 6, 0.34e-6, 1.28),
       product_variant<32, 64, 32, 32, 64, 4, 2, AF, BF>("32x64x64_ks4", 0.855, 3, 0.56e-6, 1.0,
                                                         0.25e-6),
-      product_variant<64, 64, 32, 32, 32, 1, 3, AF, BF>("64x64x32_s3", 0.890, 3, 0.58e-6),
       product_variant<32, 64, 32, 32, 32, 2, 4, AF, BF>("32x64x32_ks2_s4", 0.840, 3, 0.32e-6)};
   return table;
 }

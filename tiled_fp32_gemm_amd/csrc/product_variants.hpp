@@ -16,7 +16,7 @@ struct ProductVariant {
   ProductFn fn;
 };
 
-constexpr int kProductVariants = 10;
+constexpr int kProductVariants = 8;
 
 // [A stored M x K][B stored N x K]
 const ProductVariant* product_variants_ss();   // A is K x M, B is K x N

@@ -176,6 +176,29 @@ def test_linear_every_tile(tile, M, N, K, ta, tb):
     run_case(M, N, K, ta, tb, "none", bias=False, residual=False, preact=False)
 
 
+# Both kernels for a few rows, every width of theirs, short and long K.
+ROWS = [(True, 37, 300, "fast_%dx4"), (True, 37, 2051, "fast_%dx4"), (True, 61, 5000, "fast_%dx4"),
+        (True, 4100, 301, "fast_%dx16"), (True, 4100, 2051, "fast_%dx16"),
+        (False, 243, 301, "slow_%dx16"), (False, 5203, 130, "slow_%dx32"),
+        (False, 10501, 99, "slow_%dx64"), (False, 33001, 77, "slow_%dx64")]
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 5, 8])
+@pytest.mark.parametrize("tb,N,K,kernel", ROWS)
+def test_shapes_of_the_rows_kernels(lib, tb, N, K, kernel, M):
+    plan = sg.sgemm_linear_plan_query(0, tb, M, N, K)[1]
+    assert plan.kernel.decode() == "rows_" + kernel % {3: 4, 5: 8}.get(M, M)
+    assert plan.threads == (512 if not tb and N < 32768 else 256)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 2, 3, 5, 8])
+@pytest.mark.parametrize("tb,N,K,kernel", ROWS)
+def test_linear_by_rows(tb, N, K, kernel, M):
+    run_case(M, N, K, tb=tb, act="silu", pad=3, off=1)
+    run_case(M, N, K, tb=tb, act="none", bias=False, residual=False, preact=False)
+
+
 # Cut in two launches: by rows (one, a few by the vector kernels, many), by columns.
 CUTS = [(2049, 4096, 1000), (2053, 4096, 1024), (2100, 4096, 4001), (2048, 4104, 1024),
         (4096, 4097, 1000), (4200, 4096, 1500)]

@@ -14,6 +14,7 @@
 //                      the four waves has columns of its own and all of K.
 //                      KW = 4: they share the columns and take K by turns, for
 //                      N too small to fill the chip otherwise.
+//                      DEEP: more loads in flight, in more registers.
 //   rows_slow_kernel   B is K x N: LC lanes take 4 LC consecutive columns of
 //                      four consecutive k rows, the others further k.
 //
@@ -22,6 +23,12 @@
 // 18.8; 32 columns 19.1, 64: 24.6, too few workgroups); product_kernel with its
 // second launch takes 19.5 and 20.8 us.  11008 x 4096: fast 30.4 us (5.9 TB/s), slow
 // 32.2 at 64 columns (four waves: 42.9; 32 columns 43.2).
+//
+// Fast, four rows: two steps in flight (DEEP) 13.1 us, one 15.2; eight rows: a
+// step's loads before the other's products (DEEP) 16.5 us, one step at a time
+// 17.9 (one to four rows that way: level or slower).  Over a short K the waves
+// that the registers keep out cost more: 16 rows of eight groups, K = 1024, 24.2 us
+// DEEP and 22.9; so DEEP is for K of 2048 and more.
 //
 // B is loaded nontemporal (one row by 4096 x 4096: 14.2 -> 12.7 us, 8192 x 8192:
 // 45 -> 43 us, 6.2 TB/s), but for the slow kernel's narrow blocks, whose
@@ -95,11 +102,10 @@ __device__ __forceinline__ void finish_one(const ProductArgs& g, const RowsPlace
   g.C[row * g.ldc + col] = z;
 }
 
-template <int R, int NC, int KW>
+template <int R, int NC, int KW, bool DEEP>
 __global__ void __launch_bounds__(kRowsThreads) rows_fast_kernel(ProductArgs g) {
   constexpr int V = R * NC;
   constexpr int STEP = 256 * KW;            // k taken at a time
-  constexpr int U = V >= 16 ? 1 : 2;        // of these in flight
   __shared__ float part[4][V];
   const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
   RowsPlace p;
@@ -129,19 +135,43 @@ __global__ void __launch_bounds__(kRowsThreads) rows_fast_kernel(ProductArgs g) 
           acc[r * NC + c] = fmaf(av[r][e], bv[c][e], acc[r * NC + c]);
   };
   int k = 4 * (KW == 4 ? (int)threadIdx.x : lane);
-  for (; k + (U - 1) * STEP + 4 <= g.K; k += U * STEP) {
-    f32x4 av[U][R], bv[U][NC];
+  if constexpr (DEEP && V > 16) {
+    // Two steps' registers by turns: a step's loads go out before the other's
+    // products.
+    f32x4 av[2][R], bv[2][NC];
+    auto load = [&](int s, int at) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+      for (int c = 0; c < NC; ++c) bv[s][c] = load_upto_once(b[c] + at, 4);
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
-        bv[u][c] = load_upto_once(b[c] + k + u * STEP, 4);
+      for (int r = 0; r < R; ++r) av[s][r] = *reinterpret_cast<const f32x4u*>(a[r] + at);
+    };
+    if (k + 4 <= g.K) load(0, k);
+    while (k + 4 <= g.K) {
 #pragma unroll
-      for (int r = 0; r < R; ++r)
-        av[u][r] = *reinterpret_cast<const f32x4u*>(a[r] + k + u * STEP);
+      for (int s = 0; s < 2; ++s) {
+        if (s == 1 && k + 4 > g.K) break;
+        if (k + STEP + 4 <= g.K) load(1 - s, k + STEP);
+        __builtin_amdgcn_sched_barrier(0);
+        take(av[s], bv[s]);
+        k += STEP;
+      }
     }
+  } else {
+    constexpr int U = V < 16 || (DEEP && V == 16) ? 2 : 1;   // steps in flight
+    for (; k + (U - 1) * STEP + 4 <= g.K; k += U * STEP) {
+      f32x4 av[U][R], bv[U][NC];
 #pragma unroll
-    for (int u = 0; u < U; ++u) take(av[u], bv[u]);
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          bv[u][c] = load_upto_once(b[c] + k + u * STEP, 4);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          av[u][r] = *reinterpret_cast<const f32x4u*>(a[r] + k + u * STEP);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) take(av[u], bv[u]);
+    }
   }
   for (; k < g.K; k += STEP) {
     f32x4 av[R], bv[NC];

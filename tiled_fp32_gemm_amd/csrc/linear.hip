@@ -303,10 +303,10 @@ struct RowsChoice {
 // product; B from HBM, the groups' rows drawn at random, E x K x N):
 //      B stored                 N x K                       K x N
 //      1 row, 4096 x 4096    12.8 / 19.5                 18.2 / 21.8
-//      4 rows                15.3 / 19.5                 19.2 / 20.9
-//      8 rows                17.8 / 19.5                 21.0 / 20.8
+//      4 rows                13.1 / 19.5                 19.2 / 20.9
+//      8 rows                16.5 / 19.5                 21.0 / 20.8
 //      16 rows               22.0 / 19.8                 22.3 / 21.1
-//      8 rows, 11008 x 4096  38.2 / 43.9                 40.1 / 42.0
+//      8 rows, 11008 x 4096  36.9 / 43.9                 40.1 / 42.0
 //      1 row, 4096 x 11008   30.4 / 47.9                 44.1 / 40.0
 //      16 rows, 8192 x 1024  13.4 / 14.1                 12.2 / 13.8
 //      16 rows, 2048 x 2048  10.5 / 11.3                 10.1 / 11.2
@@ -478,7 +478,7 @@ int launch_step(Product& p, const Step& s, hipStream_t stream, void* ws) {
   if (s.rows.rows > 0) {
     const hipError_t e = hipLaunchKernel(
         reinterpret_cast<const void*>(sg::rows_kernel(p.trans_b, s.rows.rows, s.rows.cols,
-                                                          s.rows.threads)),
+                                                          s.rows.threads, g.K >= 2048)),
         dim3((unsigned)s.rows.workgroups), dim3(s.rows.threads), args, 0, stream);
     return e == hipSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH;
   }

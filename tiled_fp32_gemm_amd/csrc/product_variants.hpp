@@ -27,6 +27,6 @@ const ProductVariant* product_variants_ff();   // A is M x K, B is N x K
 // kernel_rows.hpp: chunks of `rows` (1, 2, 4 or 8) rows; `cols` a workgroup are
 // 16 or 4 with B stored N x K (KW 1 and 4), and 64, 32 or 16 with K x N.
 constexpr int kRowsMost = 8;
-ProductFn rows_kernel(bool b_fast, int rows, int cols, int threads);
+ProductFn rows_kernel(bool b_fast, int rows, int cols, int threads, bool deep);
 
 }  // namespace sg

@@ -286,6 +286,69 @@ def test_large_tiles_over_uneven_groups_are_exact(rows, G, N, K):
             assert torch.equal(db[e].double(), d.sum(0))
 
 
+# Weight gradients whose sum over a group's rows is split: one group with nearly
+# all rows, empty ones, some shorter than a slab (so that splits are empty), more
+# than sixteen (which go out in order) and more than a wave's.
+SPLIT_SUMS = [([16000, 0, 5, 379], 64, 64), ([16000, 0, 5, 379], 128, 128),
+              ([5990, 3, 7], 70, 36), ([1, 8900, 0, 2, 0, 97], 33, 65),
+              ([0, 31, 32, 33, 1, 0, 38000, 64, 65, 5, 0, 700, 2, 3, 0, 900, 164, 0, 0, 0], 100, 60),
+              ([2, 0] * 34 + [59000, 932], 20, 20)]
+
+
+def test_sums_over_groups_are_split(lib):
+    for counts, N, K in SPLIT_SUMS:
+        for tb in (0, 1):
+            size = 4 * N * K * len(counts)
+            need = sg.sgemm_grouped_wgrad_workspace_bytes(tb, sum(counts), N, K, len(counts))
+            assert need >= 2 * size and need % size == 0, (counts, N, K, tb)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("counts,N,K", SPLIT_SUMS)
+@pytest.mark.parametrize("tb", [False, True])
+def test_split_sums_over_uneven_groups_are_exact_and_replay(counts, N, K, tb):
+    g = gen(N)
+    M, G = sum(counts), len(counts)
+    draw = lambda *s: torch.randint(-8, 9, s, device="cuda", generator=g).float()  # noqa: E731
+    # 60000 products of at most 64 stay below 2^24
+    A, dC, B = draw(M + 3, K), draw(M + 3, N), draw(G, *((N, K) if tb else (K, N)))
+    A[M:], dC[M:] = float("nan"), float("nan")
+    need = sg.sgemm_grouped_wgrad_workspace_bytes(tb, M + 3, N, K, G)
+    assert need > 0
+
+    def want(offsets):
+        edges = offsets.tolist()
+        w = torch.stack([A[i:j].double().t().contiguous() @ dC[i:j].double()
+                         for i, j in zip(edges, edges[1:])])
+        return w.transpose(1, 2) if tb else w
+
+    offsets = offsets_of(counts)
+    exact = want(offsets)
+    for room in (need, need // 2, 0):
+        ws = torch.full((room // 4,), float("nan"), device="cuda") if room else None
+        for _ in range(2):
+            dB = sg.grouped_linear_backward(dC, A, B, offsets, transpose_b=tb, workspace=ws)[1]
+            assert torch.equal(dB.double(), exact), room
+    ws = torch.full((need // 4,), float("nan"), device="cuda")
+    run = lambda: sg.grouped_linear_backward(dC, A, B, offsets, transpose_b=tb,  # noqa: E731
+                                             workspace=ws)[1]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for other in (counts[::-1], counts, [M] + [0] * (G - 1), [0] * G):
+        offsets.copy_(offsets_of(other))
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.double(), want(offsets)), other
+        assert torch.equal(run(), out)
+
+
 @pytest.mark.gpu
 def test_moves_past_32_bits():
     g = gen(12)

@@ -286,6 +286,40 @@ def test_large_tiles_over_uneven_groups_are_exact(rows, G, N, K):
             assert torch.equal(db[e].double(), d.sum(0))
 
 
+# Few rows a group through an N x K stack over a long K: chunks of four and eight
+# rows, more rows than a chunk, columns by fours (N = 300) and by sixteens.
+@pytest.mark.gpu
+@pytest.mark.parametrize("counts", [[1, 3, 0, 2, 0, 0, 4, 1], [3, 8, 0, 1, 5, 2], [11, 1, 4, 0]])
+@pytest.mark.parametrize("N", [300, 2100])
+@pytest.mark.parametrize("K", [2048, 2051, 4099])
+def test_few_rows_a_group_over_a_long_k(counts, N, K):
+    g = gen(N + K)
+    G, kept = len(counts), sum(counts)
+    offsets = offsets_of(counts)
+    of = torch.repeat_interleave(torch.arange(G, device="cuda"),
+                                 torch.tensor(counts, device="cuda"))
+    for pad, off, act in ((0, 0, "none"), (1, 1, "silu")):
+        A = wide(kept + 2, K, pad, off, g)
+        A[kept:] = float("nan")
+        B = wide(G * (N + 1), K, pad, off, g, K ** -0.5).unflatten(0, (G, N + 1))[:, :N]
+        bias, R = wide(G, N, pad, off, g), wide(kept + 2, N, pad, off, g)
+        out, Z = (wide(kept + 2, N, pad, off, g, fill=7.0) for _ in range(2))
+        before = out.clone(), Z.clone()
+        sg.grouped_linear(A, B, offsets, bias, act, R, transpose_b=True, out=out, preact=Z)
+        z = torch.empty(kept, N, dtype=torch.float64, device="cuda")
+        T = torch.empty_like(z)
+        for e in range(G):
+            s, b = slice(*offsets[e:e + 2].tolist()), B[e].double().t().contiguous()
+            z[s], T[s] = A[s].double() @ b, A[s].double().abs() @ b.abs()
+        z, T = z + bias.double()[of], T + bias.double().abs()[of]
+        ztol = sum_tol(K) * T
+        assert ((Z[:kept].double() - z).abs() <= ztol).all()
+        y = act64(act, z) + R[:kept].double()
+        tol = 1.13 * ztol + 32 * U * z.abs() + U * y.abs()
+        assert ((out[:kept].double() - y).abs() <= 1.001 * tol).all()
+        assert torch.equal(out[kept:], before[0][kept:]) and torch.equal(Z[kept:], before[1][kept:])
+
+
 # Weight gradients whose sum over a group's rows is split: one group with nearly
 # all rows, empty ones, some shorter than a slab (so that splits are empty), more
 # than sixteen (which go out in order) and more than a wave's.

@@ -383,6 +383,91 @@ def test_split_sums_over_uneven_groups_are_exact_and_replay(counts, N, K, tb):
         assert torch.equal(run(), out)
 
 
+def grouped_act(dC, Z, act, dZ, db, offsets, room, N):
+    """sgemm_grouped_act_backward over every row of dC, in `room` floats."""
+    ws = torch.full((room,), float("nan"), device="cuda") if room else None
+    lead = lambda t: t.stride(0) if t is not None else 1  # noqa: E731
+    ptr = lambda t: t.data_ptr() if t is not None else 0  # noqa: E731
+    st = sg.sgemm_grouped_act_backward(
+        dC.shape[0], N, offsets.numel() - 1, offsets.data_ptr(), ptr(dC), lead(dC), ptr(Z),
+        lead(Z), sg.ACTIVATIONS[act], ptr(dZ), lead(dZ), ptr(db), lead(db),
+        torch.cuda.current_stream().cuda_stream, ptr(ws), 4 * room)
+    assert st == sg.OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("counts,N", [
+    ([0, 0, 0], 40), ([5], 3), ([0, 2000, 0, 1, 37], 130), ([4000, 0, 16, 17], 33),
+    ([3, 0, 9000, 200, 0, 0, 800], 300), ([64, 65, 0, 63, 128, 1], 1500),
+    ([1, 0, 40] * 30 + [30000], 5), ([0] * 100 + [700, 0, 70000] + [0, 1] * 50, 64)])
+def test_the_activation_pass_over_uneven_groups(counts, N):
+    """Integers, so exactly: spans of the rows that end inside groups and with
+    them, groups of no row and of nearly all, with every amount of room."""
+    g = gen(N)
+    G, kept = len(counts), sum(counts)
+    offsets = offsets_of(counts)
+    edges = offsets.tolist()
+    need = sg.sgemm_grouped_act_backward_workspace_bytes(kept + 7, N, G) // 4
+    for pad, off in ((0, 0), (3, 1)):
+        dC, Z = wide(kept + 7, N, pad, off, g, 4.0), wide(kept + 7, N, pad, off, g)
+        dC.round_()
+        dC[kept:] = Z[kept:] = float("nan")
+        want = dC[:kept].double() * (Z[:kept] > 0)
+        sums = torch.stack([want[i:j].sum(0) for i, j in zip(edges, edges[1:])])
+        plain = torch.stack([dC[i:j].double().sum(0) for i, j in zip(edges, edges[1:])])
+        for room in {need, need // 2, (G + 2) * N, 0}:
+            dZ, db = wide(kept + 7, N, pad, off, g, fill=7.0), wide(G, N, pad, off, g, fill=7.0)
+            before = dZ.clone()
+            grouped_act(dC, Z, "relu", dZ, db, offsets, room, N)
+            assert torch.equal(dZ[:kept].double(), want) and torch.equal(db.double(), sums), room
+            assert torch.equal(dZ[kept:], before[kept:])
+            db.fill_(7.0)
+            grouped_act(dC, Z, "relu", None, db, offsets, room, N)       # the sums alone
+            assert torch.equal(db.double(), sums), room
+            grouped_act(dC, None, "none", None, db, offsets, room, N)
+            assert torch.equal(db.double(), plain), room
+            over = dC.clone()                                            # in place, without them
+            grouped_act(over, Z, "relu", over, None, offsets, room, N)
+            assert torch.equal(over[:kept], dZ[:kept])
+
+
+@pytest.mark.gpu
+def test_sums_of_a_group_with_nearly_all_rows_keep_their_accuracy():
+    """A column's 262144 equal values in one of 64 groups: a lane adds at most 64
+    of them one after another, a span's lanes and the spans fewer than 32 more, so
+    fewer than 128 roundings of at most U of the sum meet."""
+    M, N, G = 1 << 18, 256, 64
+    counts = [3] * G
+    counts[5] = M - 3 * (G - 1)
+    dC = torch.full((M, N), 0.1, device="cuda")
+    db = torch.empty(G, N, device="cuda")
+    room = sg.sgemm_grouped_act_backward_workspace_bytes(M, N, G) // 4
+    grouped_act(dC, None, "none", None, db, offsets_of(counts), room, N)
+    want = dC[0, 0].double() * torch.tensor(counts, device="cuda", dtype=torch.float64)[:, None]
+    assert ((db.double() - want).abs() <= 128 * U * want).all()
+
+
+@pytest.mark.gpu
+def test_the_activation_pass_with_bad_offsets_stays_inside_its_operands():
+    g = gen(3)
+    M, N = 5000, 24
+    dC = torch.randn(M, N, device="cuda", generator=g)
+    guard = torch.full((M + 40, N), 7.0, device="cuda")
+    sums = torch.full((3 + 40, N), 7.0, device="cuda")
+    for off in ([-5, 4, 10, 1 << 30], [0, 4900, 3, 4999], [6000, 7000, 8000, 9000],
+                [(1 << 31) - 1, -(1 << 31), (1 << 31) - 1, 0]):
+        offsets = torch.tensor(off, dtype=torch.int32, device="cuda")
+        need = sg.sgemm_grouped_act_backward_workspace_bytes(M, N, 3) // 4
+        for room in (need, 0):
+            guard.fill_(7.0)
+            sums.fill_(7.0)
+            grouped_act(dC, None, "none", guard[20:M + 20], sums[20:23], offsets, room, N)
+            for t in (guard, sums):
+                assert (t[:20] == 7).all() and (t[-20:] == 7).all()
+            if off[0] == -5:
+                assert torch.equal(guard[20:M + 20], dC)
+
+
 @pytest.mark.gpu
 def test_moves_past_32_bits():
     g = gen(12)

@@ -568,17 +568,43 @@ int act_lanes(int64_t N) {
   return lpr;
 }
 
-// Strips of rows per group: enough workgroups for the chip (four a CU), at
-// least four rounds of rows each, within the workspace.
-int64_t act_strips(int64_t M, int64_t N, int64_t groups, int64_t ws_bytes) {
-  const int lpr = act_lanes(N);
-  const int64_t blocks = cdiv(N, 4 * lpr) * groups;
-  int64_t s = cdiv(4 * kCUs, blocks);
-  const int64_t most = cdiv(cdiv(M, groups), 4 * (64 / lpr) * sg::kActWaves);
+// Up to so many workgroups of 16 columns add the spans' sums, more of 128 (1024
+// threads that mostly find one span: 4096 x 4096 of 128 groups 127 us, now 45).
+constexpr int64_t kSumNarrow = 1024;
+
+// How the activation pass cuts the rows: into spans of so many, each group's
+// counted from its first row, and how many of them there can be.
+struct ActSpans {
+  int64_t rows, most;
+};
+
+// Spans enough for four workgroups a CU, of at least four rounds of rows.  The
+// lengths of the groups are not known here: `groups` ends add as many spans.
+// Sums of several spans go through W: then no more of them than it has rows, and
+// over groups with no more than 32 rounds in all a span each, without the second
+// launch (us, both ways: 128 rows of 8 groups, N = 2048, 5.3 / 9.9; 256 rows, past
+// it, 8.1, and 7.5 with all of them in one group, where a span each took 24).
+ActSpans act_spans(int64_t M, int64_t N, int64_t groups, bool grouped, bool sums,
+                   int64_t ws_bytes) {
+  const int lpr = act_lanes(N), beside = 64 / lpr * sg::kActWaves;
+  int64_t s = cdiv(4 * kCUs, cdiv(N, 4 * lpr));
+  const int64_t most = cdiv(M, 4 * beside);
   if (s > most) s = most;
-  const int64_t room = ws_bytes / 4 / (groups * N);
-  if (s > room) s = room;
-  return s < 1 ? 1 : s;
+  if (sums) {
+    const int64_t room = ws_bytes / 4 / N - (grouped ? groups : 0);
+    if (s > room) s = room;
+    if (grouped && M <= 32 * beside) s = 1;
+  }
+  if (s < 1) s = 1;
+  const int64_t rows = at_least_one(cdiv(M, s));
+  return {rows, grouped ? M / rows + groups : at_least_one(cdiv(M, rows))};
+}
+
+int64_t act_workspace(int64_t M, int64_t N, int64_t groups, bool grouped) {
+  if (M <= 0 || N <= 0 || groups <= 0 || M > kMaxDim || N > kMaxDim || groups > sg::kMaxGroups)
+    return 0;
+  const ActSpans s = act_spans(M, N, groups, grouped, true, INT64_MAX);
+  return M > s.rows ? s.most * N * 4 : 0;
 }
 
 int act_backward(int64_t M, int64_t N, int64_t groups, const int32_t* offsets, bool grouped,
@@ -626,27 +652,35 @@ int act_backward(int64_t M, int64_t N, int64_t groups, const int32_t* offsets, b
   a.groups = (int)groups;
   a.lpr = act_lanes(N);
   a.blocks_n = (int)cdiv(N, 4 * a.lpr);
-  // Without sums the strips need no room.
-  const int64_t strips = act_strips(M, N, groups, dbias ? ws_bytes : INT64_MAX);
-  a.strips = (int)strips;
-  if (dbias && strips > 1) {
-    const Span w = {ws, strips * groups * N * 4};
+  const ActSpans spans = act_spans(M, N, groups, grouped, dbias != nullptr, ws_bytes);
+  const bool through_w = dbias && M > spans.rows;   // a group can have several
+  a.span = (int)spans.rows;
+  a.spans = (int)spans.most;
+  if (through_w) {
+    const Span w = {ws, spans.most * N * 4};
     if (overlaps(w, c) || overlaps(w, z) || overlaps(w, d) || overlaps(w, b) || overlaps(w, off))
       return SGEMM_ERR_INVALID_ARG;
   }
-  const int64_t wgs = a.blocks_n * strips * groups, sums = cdiv(N, sg::kSumCols) * groups;
-  if (!grid_fits(wgs, 64 * sg::kActWaves) || !grid_fits(sums, 1024)) return SGEMM_ERR_UNSUPPORTED;
+  const int64_t wgs = a.blocks_n * spans.most;
+  if (!grid_fits(wgs, 64 * sg::kActWaves)) return SGEMM_ERR_UNSUPPORTED;
   void* kargs[] = {&a};
   typedef void (*ActFn)(ActBackwardArgs);
   static const ActFn table[] = {
       sg::act_backward_kernel<SGEMM_ACT_NONE>, sg::act_backward_kernel<SGEMM_ACT_RELU>,
       sg::act_backward_kernel<SGEMM_ACT_GELU>, sg::act_backward_kernel<SGEMM_ACT_GELU_TANH>,
       sg::act_backward_kernel<SGEMM_ACT_SILU>};
-  hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(table[act]), dim3((unsigned)wgs), dim3(64 * sg::kActWaves), kargs, 0,
-                                 stream);
-  if (e == hipSuccess && dbias && strips > 1)
-    e = hipLaunchKernel(reinterpret_cast<const void*>(sg::column_sum_kernel),
-                        dim3((unsigned)sums), dim3(1024), kargs, 0, stream);
+  hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(table[act]), dim3((unsigned)wgs),
+                                 dim3(64 * sg::kActWaves), kargs, 0, stream);
+  if (e == hipSuccess && through_w) {
+    // Groups that can have several spans.
+    const int64_t several = groups < (M - 1) / spans.rows ? groups : (M - 1) / spans.rows;
+    const bool wide = cdiv(N, 16) * several > kSumNarrow;
+    const int cols = wide ? 128 : 16;
+    e = hipLaunchKernel(wide ? reinterpret_cast<const void*>(sg::column_sum_kernel<128>)
+                             : reinterpret_cast<const void*>(sg::column_sum_kernel<16>),
+                        dim3((unsigned)(cdiv(N, cols) * several)),
+                        dim3(wide ? sg::kSumThreads<128> : sg::kSumThreads<16>), kargs, 0, stream);
+  }
   return e == hipSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH;
 }
 
@@ -728,7 +762,7 @@ int sgemm_act_backward(int64_t M, int64_t N, const float* dC, int64_t lddc, cons
 }
 
 int64_t sgemm_act_backward_workspace_bytes(int64_t M, int64_t N) {
-  return sgemm_grouped_act_backward_workspace_bytes(M, N, 1);
+  return act_workspace(M, N, 1, false);
 }
 
 int sgemm_grouped(int trans_b, int64_t M, int64_t N, int64_t K, int64_t groups,
@@ -781,10 +815,7 @@ int sgemm_grouped_act_backward(int64_t M, int64_t N, int64_t groups, const int32
 }
 
 int64_t sgemm_grouped_act_backward_workspace_bytes(int64_t M, int64_t N, int64_t groups) {
-  if (M <= 0 || N <= 0 || groups <= 0 || M > kMaxDim || N > kMaxDim || groups > sg::kMaxGroups)
-    return 0;
-  const int64_t s = act_strips(M, N, groups, INT64_MAX);
-  return s > 1 ? s * groups * N * 4 : 0;
+  return act_workspace(M, N, groups, true);
 }
 
 }  // extern "C"

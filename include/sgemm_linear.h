@@ -105,10 +105,9 @@ int sgemm_linear_plan_query(int trans_a, int trans_b, int64_t M, int64_t N,
  *             (same pointer, lddz == lddc) or preact itself; otherwise it
  *             overlaps neither.
  *   dbias     N floats, or NULL.  With M == 0 it is set to 0.
- *   workspace as above: room for the partial sums of dbias, up to
- *             sgemm_act_backward_workspace_bytes; less makes fewer, longer
- *             sums (0: one workgroup a column block).  The grouping of the
- *             sum, and so its rounding, goes by the room given. */
+ *   workspace as above: room for the partial sums of dbias,
+ *             sgemm_act_backward_workspace_bytes; with less the sums are a
+ *             pass of their own over dZ, slower, with the same result. */
 int sgemm_act_backward(int64_t M, int64_t N, const float *dC, int64_t lddc,
                        const float *preact, int64_t ldp, int act, float *dZ,
                        int64_t lddz, float *dbias, hipStream_t stream,

@@ -297,6 +297,87 @@ def test_activation_backward(act, M, N):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,N", [(1 << 18, 256), (1 << 19, 3), (300000, 130), (40000, 1030)])
+def test_sums_of_tall_matrices_keep_their_accuracy_without_room(M, N):
+    """Equal values of one sign: a lane adds at most 256 of them one after another
+    (and at most 16 such runs), a span's lanes at most 256, the spans at most 1024
+    / 64 and 6 halvings, so fewer than 600 roundings of at most U of the sum meet."""
+    dC = torch.full((M, N), 0.1, device="cuda")
+    want = float(dC[0, 0]) * M
+    stream = torch.cuda.current_stream().cuda_stream
+    need = sg.sgemm_act_backward_workspace_bytes(M, N)
+    assert need > 0
+    sums = []
+    for room in (0, 16, need - 4, need):
+        ws = torch.full((need // 4,), float("nan"), device="cuda")
+        db = torch.empty(N, device="cuda")
+        assert sg.sgemm_act_backward(M, N, dC.data_ptr(), N, 0, 1, 0, 0, 1, db.data_ptr(), stream,
+                                     ws.data_ptr() if room else 0, room) == sg.OK
+        assert ((db.double() - want).abs() <= 600 * U * want).all(), room
+        sums.append(db)
+    sums.append(sg.activation_backward(dC)[1])
+    for db in sums[1:]:      # the same whatever the room
+        assert torch.equal(db, sums[0])
+
+
+@pytest.mark.gpu
+def test_gradients_without_a_workspace_replay_from_a_graph():
+    g = gen(21)
+    M, N, K = 9000, 130, 40
+    A, B, Z = (torch.randn(*s, device="cuda", generator=g) for s in ((M, K), (K, N), (M, N)))
+    dC = torch.randn(M, N, device="cuda", generator=g)
+    sums = torch.empty(N, device="cuda")
+
+    def step():
+        assert sg.sgemm_act_backward(M, N, dC.data_ptr(), N, Z.data_ptr(), N, 4, 0, 1,
+                                     sums.data_ptr(), torch.cuda.current_stream().cuda_stream,
+                                     0, 0) == sg.OK
+        return (*sg.linear_backward(dC, A, B, "silu", Z), sums)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for rep in range(4):
+        for t in (A, B, Z, dC):
+            t.normal_(generator=g)
+        for o in out:
+            o.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in out]
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b), rep
+        assert torch.equal(got[2], got[3])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M,N", [(70, 5), (1000, 17), (5000, 300), (20001, 1), (9000, 1500)])
+def test_the_activation_pass_is_the_same_whatever_the_room(act, M, N):
+    g = gen(M)
+    for pad in (0, 3):
+        dC, Z = wide(M, N, pad, pad, g), wide(M, N, pad, pad, g, 2.0)
+        z = None if act == "none" else Z
+        need = sg.sgemm_act_backward_workspace_bytes(M, N)
+        room = lambda n: torch.empty(n, dtype=torch.uint8, device="cuda")  # noqa: E731
+        dz, db = sg.activation_backward(dC, act, z, out=wide(M, N, pad, pad, g))
+        for ws in (room(4), room(max(need - 4, 4)), room(max(need, 4)), room(need + 400)):
+            for out in (wide(M, N, pad, pad, g), dC.clone(), Z.clone()):
+                src = out if torch.equal(out, dC) else dC
+                pre = z if z is None or not torch.equal(out, Z) else out
+                got = sg.activation_backward(src, act, pre, out=out, workspace=ws)
+                assert torch.equal(got[0], dz) and torch.equal(got[1], db)
+            A, B = torch.empty(M, 0, device="cuda"), torch.empty(0, N, device="cuda")
+            assert torch.equal(sg.linear_backward(dC, A, B, act, z, workspace=ws)[2], db)
+        assert torch.equal(sg.linear_backward(dC, A, B, act, z)[2], db)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K", [(1, 30, 50), (5, 64, 40), (130, 70, 200), (257, 100, 64),
                                    (2000, 24, 36), (0, 20, 30)])
 @pytest.mark.parametrize("ta,tb", [(False, False), (False, True), (True, False), (True, True)])

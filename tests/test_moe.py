@@ -432,6 +432,25 @@ def test_the_activation_pass_over_uneven_groups(counts, N):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("counts,N", [([0, 2000, 0, 1, 37], 130), ([3, 0, 9000, 200, 0, 0, 800], 300),
+                                      ([1, 0, 40] * 30 + [30000], 5), ([9000] * 3 + [1], 1)])
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_grouped_sums_are_the_same_whatever_the_room(counts, N, act):
+    g = gen(N)
+    G, M = len(counts), sum(counts)
+    offsets = offsets_of(counts)
+    need = sg.sgemm_grouped_act_backward_workspace_bytes(M, N, G) // 4
+    dC, Z = wide(M, N, 0, 0, g), wide(M, N, 0, 0, g)
+    B, A = torch.empty(G, 0, N, device="cuda"), torch.empty(M, 0, device="cuda")
+    db = sg.grouped_linear_backward(dC, A, B, offsets, act, Z)[2]
+    for room in (need, need - 1, G * N, 1, 0):
+        for dZ in (torch.empty(M, N, device="cuda") if act != "none" else None, None):
+            got = torch.full((G, N), 7.0, device="cuda")
+            grouped_act(dC, Z, act, dZ, got, offsets, room, N)
+            assert torch.equal(got, db), room
+
+
+@pytest.mark.gpu
 def test_sums_of_a_group_with_nearly_all_rows_keep_their_accuracy():
     """A column's 262144 equal values in one of 64 groups: a lane adds at most 64
     of them one after another, a span's lanes and the spans fewer than 32 more, so

@@ -6,7 +6,10 @@
 // 256 columns, four columns a lane.  Narrow matrices put several rows side by
 // side in a wave (lpr lanes a row).  A span's sums are added through LDS in a
 // fixed order and go to its row of W, or straight to the result when it is the
-// group's only one; column_sum_kernel adds the rows of W in a fixed order.
+// group's only one; column_sum_kernel adds the rows of W in a fixed order.  Without
+// room for W the same pass makes dZ, and act_sum_kernel adds the spans up by
+// itself, sixteen columns a workgroup, in the same order: the sums go by the sizes
+// alone, whatever room there is.
 //
 // Bound by HBM: dC and Z are read once and dZ is written once.  Measured on
 // MI355X with SILU or GELU: 65536 x 128 in 18.6 us (5.4 TB/s), 4096 x 4096 in 41
@@ -32,7 +35,7 @@ struct ActBackwardArgs {
   const float* Z;       // null: act is NONE
   float* dZ;            // null: only the sums
   float* dbias;         // null: no sums
-  float* W;             // [span][N], when a group can have several
+  float* W;             // [span][N], of the groups with several; null: no room
   int64_t lddc, ldz, lddz, lddb;
   const int32_t* offsets;   // null: one group of all rows
   int M, N, groups;
@@ -42,6 +45,9 @@ struct ActBackwardArgs {
 };
 
 constexpr int kActWaves = 4;
+// A lane's sum starts anew after so many rows: its rounding errors grow with
+// n / 256 + 256 rather than n.
+constexpr int kActRun = 256;
 
 // A group's rows and spans.
 struct ActGroup {
@@ -102,6 +108,48 @@ __device__ __forceinline__ bool act_group(const ActBackwardArgs& a, int at, int&
               : out.first >= 0 && out.first < a.spans;
 }
 
+// dZ (if it is wanted) and this lane's sum over rows r, r + beside .. below end.
+template <int ACT>
+__device__ __forceinline__ f32x4 act_rows(const ActBackwardArgs& a, int64_t r, int64_t end,
+                                          int beside, int col, int left, float* dZ) {
+  f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f}, total = sum;
+  constexpr int U = 4;   // rounds of rows in flight
+  int run = 0;
+  for (; r < end; r += U * beside) {
+    f32x4 d[U], z[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = r + u * beside;
+      if (row < end) {
+        d[u] = load_upto_once(a.dC + row * a.lddc + col, left);
+        if constexpr (ACT != SGEMM_ACT_NONE) z[u] = load_upto_once(a.Z + row * a.ldz + col, left);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = r + u * beside;
+      if (row < end) {
+        if constexpr (ACT != SGEMM_ACT_NONE) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float v = d[u][e] * activation_slope<ACT>(z[u][e]);
+            asm("" : "+v"(v));   // summed as it is stored, not in one FMA
+            d[u][e] = v;
+          }
+        }
+        if (dZ) store_upto(dZ + row * a.lddz + col, left, d[u]);
+        sum += d[u];
+      }
+    }
+    if (++run == kActRun / U) {
+      total += sum;
+      sum = {0.0f, 0.0f, 0.0f, 0.0f};
+      run = 0;
+    }
+  }
+  return total + sum;
+}
+
 template <int ACT>
 __global__ void __launch_bounds__(64 * kActWaves) act_backward_kernel(ActBackwardArgs a) {
   __shared__ f32x4 part[kActWaves * 64];
@@ -110,38 +158,15 @@ __global__ void __launch_bounds__(64 * kActWaves) act_backward_kernel(ActBackwar
   int group;
   ActGroup g;
   if (!act_group<true>(a, span, group, g)) return;
+  const bool later = g.count > 1 && !a.W;   // act_sum_kernel's sums
+  if (later && !a.dZ) return;
   const int64_t r0 = g.begin + (int64_t)(span - g.first) * a.span;
   const int64_t r1 = min(r0 + a.span, (int64_t)g.end);
   const int beside = 64 / a.lpr * kActWaves;   // rows at a time
   const int col = 4 * (bn * a.lpr + lane % a.lpr), left = a.N - col;
   f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (left > 0) {
-    constexpr int U = 4;   // rounds of rows in flight
-    for (int64_t r = r0 + (int)threadIdx.x / a.lpr; r < r1; r += U * beside) {
-      f32x4 d[U], z[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t row = r + u * beside;
-        if (row < r1) {
-          d[u] = load_upto_once(a.dC + row * a.lddc + col, left);
-          if constexpr (ACT != SGEMM_ACT_NONE) z[u] = load_upto_once(a.Z + row * a.ldz + col, left);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t row = r + u * beside;
-        if (row < r1) {
-          if constexpr (ACT != SGEMM_ACT_NONE) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) d[u][e] *= activation_slope<ACT>(z[u][e]);
-          }
-          if (a.dZ) store_upto(a.dZ + row * a.lddz + col, left, d[u]);
-          sum += d[u];
-        }
-      }
-    }
-  }
-  if (!a.dbias) return;
+  if (left > 0) sum = act_rows<ACT>(a, r0 + (int)threadIdx.x / a.lpr, r1, beside, col, left, a.dZ);
+  if (!a.dbias || later) return;
   part[threadIdx.x] = sum;
   __syncthreads();
   if ((int)threadIdx.x >= a.lpr || left <= 0) return;
@@ -199,6 +224,52 @@ __global__ void __launch_bounds__(kSumThreads<COLS>) column_sum_kernel(ActBackwa
     if (tid < half) part[tid] += part[tid + half];
   }
   if (tid < COLS && col < a.N) a.dbias[group * a.lddb + col] = part[tid];
+}
+
+// The same without W: a group and up to 16 columns a workgroup, which takes as many
+// spans at a time as its threads have room for and adds them up as the two kernels
+// above do.  With dZ made before it, it reads that (as dC).  Bound by the loads in
+// flight of few workgroups: 65536 x 128 (eight) 208 us, 4096 x 4096 25, 1000 x 777 7,
+// against the 5 of the pass through W.
+template <int ACT>
+__global__ void __launch_bounds__(1024) act_sum_kernel(ActBackwardArgs a) {
+  constexpr int NT = 1024;
+  __shared__ f32x4 part[NT];
+  __shared__ f32x4 acc[kSumParts * 4];         // [part][column]
+  const int tid = (int)threadIdx.x;
+  const int L = min(a.lpr, 4);                 // lanes along a row
+  const int beside = 64 / a.lpr * kActWaves;   // rows of a span at a time
+  const int P = NT / L / beside;               // spans at a time: 4 .. 64
+  const int blocks = (a.N + 4 * L - 1) / (4 * L);
+  int group = (int)blockIdx.x / blocks;
+  const int bn = (int)blockIdx.x - group * blocks;
+  ActGroup g;
+  if (!act_group<false>(a, group, group, g)) return;
+  const int q0 = tid / L % beside, j = tid / L / beside;
+  const int col = 4 * (bn * L + tid % L), left = a.N - col;
+  if (tid < kSumParts * L) acc[tid] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s0 = 0; s0 < g.count; s0 += P) {
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int64_t r0 = g.begin + (int64_t)(s0 + j) * a.span;
+    if (left > 0)
+      sum = act_rows<ACT>(a, r0 + q0, min(r0 + a.span, (int64_t)g.end), beside, col, left, nullptr);
+    part[tid] = sum;
+    __syncthreads();
+    // P divides kSumParts, so a thread meets its own words of acc only.
+    const int s = s0 + tid / L;
+    if (tid < P * L && s < g.count) {
+      const f32x4* p = part + tid / L * beside * L + tid % L;
+      f32x4 v = p[0];
+      for (int q = 1; q < beside; ++q) v += p[q * L];
+      acc[s % kSumParts * L + tid % L] += v;
+    }
+    __syncthreads();
+  }
+  for (int half = kSumParts / 2 * L; half >= L; half /= 2) {
+    if (tid < half) acc[tid] += acc[tid + half];
+    __syncthreads();
+  }
+  if (tid < L && left > 0) store_upto(a.dbias + group * a.lddb + col, left, acc[tid]);
 }
 
 }  // namespace sg

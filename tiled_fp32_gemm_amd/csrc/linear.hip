@@ -580,22 +580,16 @@ struct ActSpans {
 
 // Spans enough for four workgroups a CU, of at least four rounds of rows.  The
 // lengths of the groups are not known here: `groups` ends add as many spans.
-// Sums of several spans go through W: then no more of them than it has rows, and
-// over groups with no more than 32 rounds in all a span each, without the second
-// launch (us, both ways: 128 rows of 8 groups, N = 2048, 5.3 / 9.9; 256 rows, past
-// it, 8.1, and 7.5 with all of them in one group, where a span each took 24).
-ActSpans act_spans(int64_t M, int64_t N, int64_t groups, bool grouped, bool sums,
-                   int64_t ws_bytes) {
+// Sums of several spans take a second launch: over groups with no more than 32
+// rounds in all a span each, without it (us, both ways: 128 rows of 8 groups, N =
+// 2048, 5.3 / 9.9; 256 rows, past it, 8.1, and 7.5 with all of them in one group,
+// where a span each took 24).
+ActSpans act_spans(int64_t M, int64_t N, int64_t groups, bool grouped, bool sums) {
   const int lpr = act_lanes(N), beside = 64 / lpr * sg::kActWaves;
   int64_t s = cdiv(4 * kCUs, cdiv(N, 4 * lpr));
   const int64_t most = cdiv(M, 4 * beside);
   if (s > most) s = most;
-  if (sums) {
-    const int64_t room = ws_bytes / 4 / N - (grouped ? groups : 0);
-    if (s > room) s = room;
-    if (grouped && M <= 32 * beside) s = 1;
-  }
-  if (s < 1) s = 1;
+  if (s < 1 || (grouped && sums && M <= 32 * beside)) s = 1;
   const int64_t rows = at_least_one(cdiv(M, s));
   return {rows, grouped ? M / rows + groups : at_least_one(cdiv(M, rows))};
 }
@@ -603,7 +597,7 @@ ActSpans act_spans(int64_t M, int64_t N, int64_t groups, bool grouped, bool sums
 int64_t act_workspace(int64_t M, int64_t N, int64_t groups, bool grouped) {
   if (M <= 0 || N <= 0 || groups <= 0 || M > kMaxDim || N > kMaxDim || groups > sg::kMaxGroups)
     return 0;
-  const ActSpans s = act_spans(M, N, groups, grouped, true, INT64_MAX);
+  const ActSpans s = act_spans(M, N, groups, grouped, true);
   return M > s.rows ? s.most * N * 4 : 0;
 }
 
@@ -641,7 +635,6 @@ int act_backward(int64_t M, int64_t N, int64_t groups, const int32_t* offsets, b
   a.Z = Z;
   a.dZ = dZ;
   a.dbias = dbias;
-  a.W = static_cast<float*>(ws);
   a.lddc = lddc;
   a.ldz = ldz;
   a.lddz = lddz;
@@ -652,15 +645,16 @@ int act_backward(int64_t M, int64_t N, int64_t groups, const int32_t* offsets, b
   a.groups = (int)groups;
   a.lpr = act_lanes(N);
   a.blocks_n = (int)cdiv(N, 4 * a.lpr);
-  const ActSpans spans = act_spans(M, N, groups, grouped, dbias != nullptr, ws_bytes);
-  const bool through_w = dbias && M > spans.rows;   // a group can have several
+  const ActSpans spans = act_spans(M, N, groups, grouped, dbias != nullptr);
   a.span = (int)spans.rows;
   a.spans = (int)spans.most;
-  if (through_w) {
-    const Span w = {ws, spans.most * N * 4};
-    if (overlaps(w, c) || overlaps(w, z) || overlaps(w, d) || overlaps(w, b) || overlaps(w, off))
-      return SGEMM_ERR_INVALID_ARG;
-  }
+  // Room for the sums, where a group can have several spans.
+  const int64_t need = dbias && M > spans.rows ? spans.most * N * 4 : 0;
+  const Span w = {ws, ws_bytes < need ? ws_bytes : need};
+  if (overlaps(w, c) || overlaps(w, z) || overlaps(w, d) || overlaps(w, b) || overlaps(w, off))
+    return SGEMM_ERR_INVALID_ARG;
+  const bool room = need > 0 && ws_bytes >= need;
+  a.W = room ? static_cast<float*>(ws) : nullptr;
   const int64_t wgs = a.blocks_n * spans.most;
   if (!grid_fits(wgs, 64 * sg::kActWaves)) return SGEMM_ERR_UNSUPPORTED;
   void* kargs[] = {&a};
@@ -669,18 +663,34 @@ int act_backward(int64_t M, int64_t N, int64_t groups, const int32_t* offsets, b
       sg::act_backward_kernel<SGEMM_ACT_NONE>, sg::act_backward_kernel<SGEMM_ACT_RELU>,
       sg::act_backward_kernel<SGEMM_ACT_GELU>, sg::act_backward_kernel<SGEMM_ACT_GELU_TANH>,
       sg::act_backward_kernel<SGEMM_ACT_SILU>};
-  hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(table[act]), dim3((unsigned)wgs),
-                                 dim3(64 * sg::kActWaves), kargs, 0, stream);
-  if (e == hipSuccess && through_w) {
-    // Groups that can have several spans.
-    const int64_t several = groups < (M - 1) / spans.rows ? groups : (M - 1) / spans.rows;
-    const bool wide = cdiv(N, 16) * several > kSumNarrow;
-    const int cols = wide ? 128 : 16;
-    e = hipLaunchKernel(wide ? reinterpret_cast<const void*>(sg::column_sum_kernel<128>)
-                             : reinterpret_cast<const void*>(sg::column_sum_kernel<16>),
-                        dim3((unsigned)(cdiv(N, cols) * several)),
-                        dim3(wide ? sg::kSumThreads<128> : sg::kSumThreads<16>), kargs, 0, stream);
+  hipError_t e = hipSuccess;
+  // Nothing to do where act_sum_kernel does everything.
+  if (dZ || room || need == 0 || grouped)
+    e = hipLaunchKernel(reinterpret_cast<const void*>(table[act]), dim3((unsigned)wgs),
+                        dim3(64 * sg::kActWaves), kargs, 0, stream);
+  if (e != hipSuccess || need == 0) return e == hipSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH;
+  // Groups that can have several spans.
+  const int64_t several = groups < (M - 1) / spans.rows ? groups : (M - 1) / spans.rows;
+  int cols = 16, threads = 1024;
+  const void* fn = reinterpret_cast<const void*>(sg::column_sum_kernel<16>);
+  if (room && cdiv(N, 16) * several > kSumNarrow) {
+    cols = 128;
+    threads = sg::kSumThreads<128>;
+    fn = reinterpret_cast<const void*>(sg::column_sum_kernel<128>);
+  } else if (!room) {
+    cols = a.lpr < 4 ? 4 * a.lpr : 16;
+    if (dZ) {
+      a.dC = dZ;
+      a.lddc = lddz;
+    }
+    static const ActFn sums[] = {
+        sg::act_sum_kernel<SGEMM_ACT_NONE>, sg::act_sum_kernel<SGEMM_ACT_RELU>,
+        sg::act_sum_kernel<SGEMM_ACT_GELU>, sg::act_sum_kernel<SGEMM_ACT_GELU_TANH>,
+        sg::act_sum_kernel<SGEMM_ACT_SILU>};
+    fn = reinterpret_cast<const void*>(sums[dZ ? SGEMM_ACT_NONE : act]);
   }
+  e = hipLaunchKernel(fn, dim3((unsigned)(cdiv(N, cols) * several)), dim3(threads), kargs, 0,
+                      stream);
   return e == hipSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH;
 }
 

@@ -150,6 +150,15 @@ def _workspace(workspace, dev: int) -> tuple[int, int]:
     return (workspace.data_ptr(), n) if n else (0, 0)
 
 
+def _own(like, need: int, ws: int, ws_bytes: int):
+    """A workspace of `need` bytes made for a call (0: the caller's), its address
+    and size.  It has to be held until the last launch that uses it."""
+    if not need:
+        return None, ws, ws_bytes
+    own = like.new_empty(need, dtype=torch.uint8)
+    return own, own.data_ptr(), need
+
+
 def _on(dev: int, stream, body):
     """``body(handle)`` with GPU `dev` current and `stream` (default: its
     current one) the stream that tensors made inside belong to."""
@@ -231,6 +240,7 @@ def activation_backward(dC, activation="none", preact=None, *, bias_grad=True, o
 
     ``out`` receives dZ and may be ``dC`` or ``preact``.  For activation
     "none" dZ is dC: unless ``out`` asks for a copy, dC itself is returned.
+    Without a ``workspace`` one is made for the sums.
     """
     act = _act(activation)
     dev = _device(dC, "dC")
@@ -243,14 +253,18 @@ def activation_backward(dC, activation="none", preact=None, *, bias_grad=True, o
         z = preact.data_ptr()
     lddz = max(N, 1) if out is None else _sized(out, "out", dev, M, N)
     ws, ws_bytes = _workspace(workspace, dev)
+    lib = sg.load()
+    need = 0
+    if workspace is None and bias_grad:
+        need = lib.sgemm_act_backward_workspace_bytes(M, N)
 
     def call(s):
         dz = dC.new_empty(M, N) if out is None and act else out
         dbias = dC.new_empty(N) if bias_grad else None
-        st = sg.load().sgemm_act_backward(M, N, dC.data_ptr(), lddc, z, ldz, act,
-                                          None if dz is None else dz.data_ptr(), lddz,
-                                          dbias.data_ptr() if bias_grad else None, s, ws,
-                                          ws_bytes)
+        own, room, size = _own(dC, need, ws, ws_bytes)  # noqa: F841
+        st = lib.sgemm_act_backward(M, N, dC.data_ptr(), lddc, z, ldz, act,
+                                    None if dz is None else dz.data_ptr(), lddz,
+                                    dbias.data_ptr() if bias_grad else None, s, room, size)
         _check(st, "sgemm_act_backward")
         return (dC if dz is None else dz), dbias
     return _on(dev, stream, call)
@@ -261,7 +275,8 @@ def linear_backward(dC, A, B, activation="none", preact=None, *, transpose_a=Fal
     """``(dA, dB, dbias)`` of ``linear`` for the gradient ``dC`` of its output:
     dA and dB in the shapes A and B are stored in, dbias None without
     ``bias_grad``.  ``preact`` is what ``linear`` stored (not needed for
-    activation "none").  The residual's gradient is ``dC``.
+    activation "none").  The residual's gradient is ``dC``.  Without a
+    ``workspace`` one is made for dbias, and the products' sums are not split.
     """
     act = _act(activation)
     dev = _device(dC, "dC")
@@ -274,16 +289,20 @@ def linear_backward(dC, A, B, activation="none", preact=None, *, transpose_a=Fal
     room, size = _workspace(workspace, dev)
     ta, tb = bool(transpose_a), bool(transpose_b)
     lib = sg.load()
+    need = 0
+    if workspace is None and bias_grad:
+        need = lib.sgemm_act_backward_workspace_bytes(M, N)
 
     def call(s):   # dZ, when it is made here, belongs to the stream
         dz, ld, dbias = dC, lddc, dC.new_empty(N) if bias_grad else None
         if act:
             dz, ld = dC.new_empty(M, N), max(N, 1)
         if act or bias_grad:
+            own, *sums = _own(dC, need, room, size)  # noqa: F841
             _check(lib.sgemm_act_backward(
                 M, N, dC.data_ptr(), lddc, preact.data_ptr() if act else None, ldz, act,
                 dz.data_ptr() if act else None, ld, dbias.data_ptr() if bias_grad else None, s,
-                room, size), "sgemm_act_backward")
+                *sums), "sgemm_act_backward")
         dA, dB = A.new_empty(A.shape), B.new_empty(B.shape)
         a, b, d = (A.data_ptr(), lda), (B.data_ptr(), ldb), (dz.data_ptr(), ld)
 

@@ -19,8 +19,8 @@ import torch
 
 import tiled_fp32_gemm_amd as sg
 
-from .epilogue import (Epilogue, _act, _check, _device, _epilogue, _float, _matrix, _on, _sized,
-                       _workspace)
+from .epilogue import (Epilogue, _act, _check, _device, _epilogue, _float, _matrix, _on, _own,
+                       _sized, _workspace)
 
 MOE_SYMBOLS = ("sgemm_moe_sort", "sgemm_moe_sort_workspace_bytes", "sgemm_moe_permute",
                "sgemm_moe_unpermute", "sgemm_moe_unpermute_backward", "sgemm_grouped",
@@ -115,10 +115,7 @@ def moe_sort(experts, num_experts, *, stream=None, workspace=None):
     ws, ws_bytes = _workspace(workspace, dev)
 
     def call(s):
-        room, size = ws, ws_bytes
-        if need:
-            own = experts.new_empty(need, dtype=torch.uint8)
-            room, size = own.data_ptr(), need
+        own, room, size = _own(experts, need, ws, ws_bytes)  # noqa: F841
         offsets = experts.new_empty(E + 1, dtype=torch.int32)
         order = experts.new_empty(n, dtype=torch.int32)
         place = experts.new_empty(experts.shape, dtype=torch.int32)
@@ -237,7 +234,8 @@ def grouped_linear_backward(dC, A, B, offsets, activation="none", preact=None, *
                             transpose_b=False, bias_grad=True, stream=None, workspace=None):
     """``(dA, dB, dbias)`` of ``grouped_linear``: dA for the groups' rows, dB
     stored like B and dbias (groups x N; None without ``bias_grad``) 0 for a
-    group without rows.  The residual's gradient is ``dC``."""
+    group without rows.  The residual's gradient is ``dC``.  Without a
+    ``workspace`` one is made for dbias, and the products' sums are not split."""
     act = _act(activation)
     dev = _device(dC, "dC")
     M, N, K, G, lda, ldb, stride, off = _groups(A, B, offsets, dev, transpose_b)
@@ -250,13 +248,17 @@ def grouped_linear_backward(dC, A, B, offsets, activation="none", preact=None, *
         z = preact.data_ptr()
     ws, ws_bytes = _workspace(workspace, dev)
     lib = sg.load()
+    need = 0
+    if workspace is None and bias_grad:
+        need = lib.sgemm_grouped_act_backward_workspace_bytes(M, N, G)
 
     def call(s):
         dZ, lddz = (dC.new_empty(M, N), max(N, 1)) if act else (dC, lddc)
         dbias = dC.new_empty(G, N) if bias_grad else None
+        own, *sums = _own(dC, need, ws, ws_bytes)  # noqa: F841
         _check(lib.sgemm_grouped_act_backward(
             M, N, G, off, dC.data_ptr(), lddc, z, ldz, act, dZ.data_ptr() if act else None, lddz,
-            dbias.data_ptr() if bias_grad else None, max(N, 1), s, ws, ws_bytes),
+            dbias.data_ptr() if bias_grad else None, max(N, 1), s, *sums),
             "sgemm_grouped_act_backward")
         dA, dB = A.new_empty(M, K), B.new_empty(B.shape)
         _check(lib.sgemm_grouped(not transpose_b, M, K, N, G, off, dZ.data_ptr(), lddz,

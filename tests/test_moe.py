@@ -132,6 +132,32 @@ def test_moves_and_their_gradients(T, top, H, drop):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,E,H", [(1, 3, 5), (40, 4, 33), (9000, 16, 20)])
+def test_one_choice_a_token_in_one_dimension(T, E, H):
+    g = gen(T)
+    ids = torch.randint(-1, E, (T,), device="cuda", generator=g)
+    offsets, order, place = sg.moe_sort(ids, E)
+    x, dy = (torch.randn(T, H, device="cuda", generator=g) for _ in range(2))
+    w = torch.rand(T, device="cuda", generator=g)
+    flat, column = [], []
+    for out, p, weights in ((flat, place, w), (column, place[:, None], w[:, None])):
+        xp = sg.moe_permute(x, p, out=torch.zeros(T, H, device="cuda"))
+        dyp, dw = sg.moe_unpermute_backward(dy, xp, p, weights, out=torch.zeros_like(xp))
+        out += [xp, sg.moe_unpermute(xp, p, weights), sg.moe_unpermute(xp, p), dyp, dw]
+    assert flat[-1].shape == (T,)
+    column[-1] = column[-1][:, 0]
+    for a, b in zip(flat, column):
+        assert torch.equal(a, b)
+    kept = (ids >= 0).float()[:, None]
+    assert torch.equal(flat[2], x * kept) and torch.equal(flat[1], w[:, None] * x * kept)
+    for bad in (w[:, None], w[: T - 1]):
+        with pytest.raises(ValueError):
+            sg.moe_unpermute(flat[0], place, bad)
+    with pytest.raises(ValueError):
+        sg.moe_permute(x, place.reshape(1, T, 1))
+
+
+@pytest.mark.gpu
 def test_places_outside_the_rows_count_as_dropped():
     g = gen(2)
     place = torch.tensor([[0, 1], [6, -5], [2, 1 << 30], [-(1 << 31), 3]], dtype=torch.int32,

@@ -84,22 +84,22 @@ def _index(t, name: str, dev: int, shape=None) -> int:
 def _place(place, dev: int) -> tuple[int, int, int]:
     """T, top and the address of a place tensor."""
     p = _index(place, "place", dev)
-    if place.dim() != 2:
-        raise ValueError("place must be 2-D (tokens x choices)")
-    return *place.shape, p
+    if place.dim() not in (1, 2):
+        raise ValueError("place must be 2-D (tokens x choices) or 1-D (one choice a token)")
+    return place.shape[0], place.shape[1] if place.dim() == 2 else 1, p
 
 
-def _weights(weights, dev: int, T: int, top: int):
+def _weights(weights, dev: int, place):
     if weights is None:
         return None
-    if _float(weights, "weights", dev).shape != (T, top) or not weights.is_contiguous():
-        raise ValueError(f"weights must be contiguous and {T} x {top}")
+    if _float(weights, "weights", dev).shape != place.shape or not weights.is_contiguous():
+        raise ValueError(f"weights must be contiguous and shaped like place: {tuple(place.shape)}")
     return weights.data_ptr()
 
 
 def moe_sort(experts, num_experts, *, stream=None, workspace=None):
-    """``(offsets, order, place)`` of a T x top (or 1-D) tensor of expert ids,
-    int32 or int64: expert e's rows are ``offsets[e]`` to ``offsets[e+1]-1``,
+    """``(offsets, order, place)`` of a T x top tensor of expert ids (1-D: one a
+    token), int32 or int64: expert e's rows are ``offsets[e]`` to ``offsets[e+1]-1``,
     row r holds choice ``order[r]`` (-1 behind the last row), choice c is in
     row ``place`` [c] (-1: dropped; shaped like ``experts``).  Equal experts
     keep their order.  Without a ``workspace`` one is made for the call.
@@ -147,13 +147,13 @@ def moe_permute(X, place, *, out=None, stream=None):
 
 def moe_unpermute(Yp, place, weights=None, *, out=None, stream=None):
     """T x H: each token's rows of Yp (T·top x H) times their ``weights``
-    (T x top; None: 1), summed; 0 for a token without rows."""
+    (shaped like ``place``; None: 1), summed; 0 for a token without rows."""
     dev = _device(Yp, "Yp")
     T, top, p = _place(place, dev)
     rows, H, ldyp = _matrix(Yp, "Yp", dev)
     if rows != T * top:
         raise ValueError(f"Yp has {rows} rows, place {T} x {top}")
-    w = _weights(weights, dev, T, top)
+    w = _weights(weights, dev, place)
     ld = max(H, 1) if out is None else _sized(out, "out", dev, T, H)
 
     def call(s):
@@ -166,19 +166,20 @@ def moe_unpermute(Yp, place, weights=None, *, out=None, stream=None):
 
 def moe_unpermute_backward(dY, Yp, place, weights=None, *, out=None, stream=None):
     """``(dYp, dweights)`` of ``moe_unpermute`` for the gradient dY (T x H) of
-    its result.  ``out`` receives dYp and may be ``Yp``."""
+    its result; dweights is shaped like ``place``.  ``out`` receives dYp and may
+    be ``Yp``."""
     dev = _device(dY, "dY")
     T, top, p = _place(place, dev)
     rows, H, lddy = _matrix(dY, "dY", dev)
     if rows != T:
         raise ValueError(f"dY has {rows} rows, place {T}")
     ldyp = _sized(Yp, "Yp", dev, T * top, H)
-    w = _weights(weights, dev, T, top)
+    w = _weights(weights, dev, place)
     ld = max(H, 1) if out is None else _sized(out, "out", dev, T * top, H)
 
     def call(s):
         dyp = dY.new_empty(T * top, H) if out is None else out
-        dw = dY.new_empty(T, top)
+        dw = dY.new_empty(place.shape)
         _check(sg.load().sgemm_moe_unpermute_backward(
             T, top, H, dY.data_ptr(), lddy, Yp.data_ptr(), ldyp, p, w, dyp.data_ptr(), ld,
             dw.data_ptr(), s), "sgemm_moe_unpermute_backward")

@@ -12,8 +12,8 @@
 // alone, whatever room there is.
 //
 // Bound by HBM: dC and Z are read once and dZ is written once.  Measured on
-// MI355X with SILU or GELU: 65536 x 128 in 18.6 us (5.4 TB/s), 4096 x 4096 in 41
-// us (4.9 TB/s), and 4.7 us for the spans' sums; both passes over 16384 x 2048 of 64
+// MI355X with SILU or GELU: 65536 x 128 in 18.8 us (5.3 TB/s), 4096 x 4096 in 38 to
+// 41 us (5 TB/s), and 4.7 us for the spans' sums; both passes over 16384 x 2048 of 64
 // groups 79 us, of one group with all the rows and 63 without 81 (as many spans
 // for every group: 101 and 878), of 16384 x 1024 of 1000 groups, where every wave
 // has many to count, 59 (38 and 1690).  The loads are nontemporal, which

@@ -18,7 +18,7 @@
 //   rows_slow_kernel   B is K x N: LC lanes take 4 LC consecutive columns of
 //                      four consecutive k rows, the others further k.
 //
-// Measured on MI355X (B of 64 MiB, 4096 x 4096, from HBM, one row): fast 12.5 us
+// Measured on MI355X (B of 64 MiB, 4096 x 4096, from HBM, one row): fast 12.8 us
 // (KW = 4 16.2), slow 18.2 us at 16 columns a workgroup and eight waves (four:
 // 18.8; 32 columns 19.1, 64: 24.6, too few workgroups); product_kernel with its
 // second launch takes 19.5 and 20.8 us.  11008 x 4096: fast 30.4 us (5.9 TB/s), slow

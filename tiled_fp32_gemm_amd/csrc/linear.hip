@@ -568,8 +568,10 @@ int act_lanes(int64_t N) {
   return lpr;
 }
 
-// Up to so many workgroups of 16 columns add the spans' sums, more of 128 (1024
-// threads that mostly find one span: 4096 x 4096 of 128 groups 127 us, now 45).
+// Up to so many workgroups of 16 columns add the spans' sums; where there would be
+// more, of 1024 threads with little to do, they take 128 (us, both passes, by 16 and
+// by 128: 4096 x 4096 of 128 groups 82 / 45, 8190 x 1500 of 16 39 / 35, 256 x 1024 of
+// 8 8.3 / 8.0, 65536 x 128 of one 23 / 33).
 constexpr int64_t kSumNarrow = 1024;
 
 // How the activation pass cuts the rows: into spans of so many, each group's

@@ -315,7 +315,8 @@ def test_large_tiles_over_uneven_groups_are_exact(rows, G, N, K):
 # Few rows a group through an N x K stack over a long K: chunks of four and eight
 # rows, more rows than a chunk, columns by fours (N = 300) and by sixteens.
 @pytest.mark.gpu
-@pytest.mark.parametrize("counts", [[1, 3, 0, 2, 0, 0, 4, 1], [3, 8, 0, 1, 5, 2], [11, 1, 4, 0]])
+@pytest.mark.parametrize("counts", [[1, 3, 0, 2, 0, 0, 4, 1], [3, 8, 0, 1, 5, 2], [11, 1, 4, 0],
+                                    [9, 1, 0, 1, 0, 2]])
 @pytest.mark.parametrize("N", [300, 2100])
 @pytest.mark.parametrize("K", [2048, 2051, 4099])
 def test_few_rows_a_group_over_a_long_k(counts, N, K):

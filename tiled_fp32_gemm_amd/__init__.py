@@ -10,7 +10,8 @@ marshal arguments: every step of the product runs in the HIP kernels.
 dimensions and the stream and calls ``sgemm_ex``.  ``epilogue`` (products
 with an epilogue and their gradients) and ``moe`` (expert routing and the experts'
 products) are the same for ``include/sgemm_linear.h`` and
-``include/sgemm_moe.h``; their functions are names of this module too.
+``include/sgemm_moe.h``, ``norm`` (layer norm) for ``include/sgemm_norm.h``;
+their functions are names of this module too.
 
 There is no fallback: if ``libsgemm.so`` has not been built, or does not load,
 importing the binding's functions raises.  Build it with
@@ -38,7 +39,8 @@ __all__ = ["sgemm", "sgemm_ex", "sgemm_plan_query", "sgemm_status_string",
            "linear_backward", "activation_backward", "MOE_SYMBOLS",
            "MOE_MAX_EXPERTS", "moe_sort", "moe_permute", "moe_unpermute",
            "moe_unpermute_backward", "grouped_linear",
-           "grouped_linear_backward"]
+           "grouped_linear_backward", "NORM_SYMBOLS", "layer_norm",
+           "layer_norm_backward"]
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_LAUNCH, ERR_SCRATCH_LIMIT = 0, 1, 2, 3, 4
 NOALLOC_MAX_BYTES = 32 << 20   # SGEMM_NOALLOC_MAX_BYTES
@@ -124,9 +126,9 @@ def load():
     lib.sgemm_workspace_bytes.restype = i64
     lib.sgemm_plan_query_ws.argtypes = common + [i64, ctypes.POINTER(SgemmPlan)]
     lib.sgemm_plan_query_ws.restype = i32
-    from . import epilogue, moe
-    epilogue.prototypes(lib)
-    moe.prototypes(lib)
+    from . import epilogue, moe, norm
+    for module in (epilogue, moe, norm):
+        module.prototypes(lib)
     _lib = lib
     return lib
 
@@ -323,7 +325,9 @@ _LATER = {
             "sgemm_grouped_act_backward_workspace_bytes", "sgemm_grouped_wgrad",
             "sgemm_grouped_wgrad_workspace_bytes", "sgemm_grouped_workspace_bytes",
             "sgemm_moe_permute", "sgemm_moe_sort", "sgemm_moe_sort_workspace_bytes",
-            "sgemm_moe_unpermute", "sgemm_moe_unpermute_backward")}
+            "sgemm_moe_unpermute", "sgemm_moe_unpermute_backward"),
+    "norm": ("NORM_SYMBOLS", "layer_norm", "layer_norm_backward", "sgemm_layer_norm",
+             "sgemm_layer_norm_backward", "sgemm_layer_norm_backward_workspace_bytes")}
 
 
 def __getattr__(name: str):

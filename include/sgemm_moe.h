@@ -5,6 +5,7 @@
  *
  * The path.  T tokens choose `top` of E experts each, which makes T·top rows:
  *
+ *      sgemm_moe_route      a router's logits -> choices and their weights
  *      sgemm_moe_sort       choices -> offsets, order, place
  *      sgemm_moe_permute    each token's row to its places, in expert order
  *      sgemm_grouped        expert e's product over rows offsets[e] ..
@@ -20,6 +21,7 @@
  *      permute    dX[t] = sum over t's rows of dXp: sgemm_moe_unpermute
  *                 without weights
  *      unpermute  sgemm_moe_unpermute_backward
+ *      route      sgemm_moe_route_backward
  *      grouped    dZ and dbias: sgemm_grouped_act_backward; dA: sgemm_grouped
  *                 with trans_b flipped; dB: sgemm_grouped_wgrad
  *
@@ -39,6 +41,59 @@ extern "C" {
 #endif
 
 #define SGEMM_MOE_MAX_EXPERTS 1024
+#define SGEMM_MOE_MAX_TOP 32       /* sgemm_moe_route's choices a token */
+#define SGEMM_MOE_MAX_GROUPS 32    /* and groups of experts */
+
+#define SGEMM_SCORE_SOFTMAX 0
+#define SGEMM_SCORE_SIGMOID 1
+
+/* How a router chooses.  With l a token's E logits:
+ *
+ *      s = softmax(l), or 1 / (1 + exp(-l)) for each expert
+ *      c = s + bias       (the bias balances the choice, the weights are of s)
+ *
+ * With groups > 1 the experts are `groups` equal groups of neighbours; a group's
+ * score is its best c, or with group_best 2 the sum of its best two (of the best
+ * one where only one can be chosen), and the experts outside the best
+ * `top_groups` groups cannot be chosen.  The best `top` c's are the choices, the
+ * best first; equal scores go to the lowest expert (group).  The weights are s of
+ * the choices, divided by their sum with renormalize, times scale. */
+typedef struct sgemm_moe_router {
+    int scoring;            /* SGEMM_SCORE_* */
+    int renormalize;        /* 0 or 1 */
+    float scale;            /* finite, not 0 */
+    const float *bias;      /* E floats, or NULL */
+    int groups;             /* 1 .. SGEMM_MOE_MAX_GROUPS, dividing E */
+    int top_groups;         /* 1 .. groups */
+    int group_best;         /* 1 or 2, at most E / groups */
+} sgemm_moe_router;
+
+/* experts and weights (T x top, contiguous) from logits (T x E, leading dimension
+ * ldl).
+ *   top   1 .. SGEMM_MOE_MAX_TOP, at most the experts of top_groups groups.
+ * An expert whose logit or whose c is -infinity is never chosen: where fewer than
+ * top remain, the rest of a token's choices are -1 with weight 0, which
+ * sgemm_moe_sort drops.  A NaN score counts as infinite, and makes NaN weights.
+ * The choice is that of the scores in exact arithmetic: what FP32 cannot tell apart
+ * is computed again in FP64.  Experts over SGEMM_MOE_MAX_EXPERTS, top or groups over
+ * their limits are SGEMM_ERR_UNSUPPORTED.  T == 0 is a no-op. */
+int sgemm_moe_route(int64_t T, int64_t E, int64_t top, const float *logits,
+                    int64_t ldl, const sgemm_moe_router *router,
+                    int32_t *experts, float *weights, hipStream_t stream);
+
+/* dlogits (T x E) for the gradient dweights of the weights, both T x top like
+ * experts and weights, which are what sgemm_moe_route gave for these logits and
+ * this router (scoring, renormalize and scale are read).  weights is read with
+ * renormalize only, and logits are not read with renormalize and a softmax; they
+ * may be NULL otherwise.  A choice outside 0 .. E-1 has no gradient; the terms of
+ * an expert chosen twice add up.  The bias has no gradient.  dlogits may be logits
+ * itself (same pointer, same leading dimension), or must not overlap it. */
+int sgemm_moe_route_backward(int64_t T, int64_t E, int64_t top,
+                             const float *logits, int64_t ldl,
+                             const sgemm_moe_router *router,
+                             const int32_t *experts, const float *weights,
+                             const float *dweights, float *dlogits,
+                             int64_t lddl, hipStream_t stream);
 
 /* Sorts n = T·top choices by expert, keeping the order of equal ones.
  *   experts   n expert ids, id_bytes 4 (int32) or 8 (int64) bytes each.

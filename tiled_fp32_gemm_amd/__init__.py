@@ -37,7 +37,8 @@ __all__ = ["sgemm", "sgemm_ex", "sgemm_plan_query", "sgemm_status_string",
            "sgemm_plan_query_ws", "sgemm_ws_noalloc", "ERR_SCRATCH_LIMIT",
            "NOALLOC_MAX_BYTES", "ACTIVATIONS", "LINEAR_SYMBOLS", "linear",
            "linear_backward", "activation_backward", "MOE_SYMBOLS",
-           "MOE_MAX_EXPERTS", "moe_sort", "moe_permute", "moe_unpermute",
+           "MOE_MAX_EXPERTS", "MOE_MAX_TOP", "MOE_MAX_GROUPS", "SCORINGS",
+           "moe_route", "moe_route_backward", "moe_sort", "moe_permute", "moe_unpermute",
            "moe_unpermute_backward", "grouped_linear",
            "grouped_linear_backward", "NORM_SYMBOLS", "layer_norm",
            "layer_norm_backward"]
@@ -319,13 +320,15 @@ _LATER = {
     "epilogue": ("ACTIVATIONS", "LINEAR_SYMBOLS", "Epilogue", "activation_backward", "linear",
                  "linear_backward", "sgemm_act_backward", "sgemm_act_backward_workspace_bytes",
                  "sgemm_linear", "sgemm_linear_plan_query", "sgemm_linear_workspace_bytes"),
-    "moe": ("MOE_MAX_EXPERTS", "MOE_SYMBOLS", "grouped_linear", "grouped_linear_backward",
-            "moe_permute", "moe_sort", "moe_unpermute", "moe_unpermute_backward",
+    "moe": ("MOE_MAX_EXPERTS", "MOE_MAX_GROUPS", "MOE_MAX_TOP", "MOE_SYMBOLS", "Router",
+            "SCORINGS", "grouped_linear", "grouped_linear_backward", "moe_permute", "moe_route",
+            "moe_route_backward", "moe_sort", "moe_unpermute", "moe_unpermute_backward",
             "sgemm_grouped", "sgemm_grouped_act_backward",
             "sgemm_grouped_act_backward_workspace_bytes", "sgemm_grouped_wgrad",
             "sgemm_grouped_wgrad_workspace_bytes", "sgemm_grouped_workspace_bytes",
-            "sgemm_moe_permute", "sgemm_moe_sort", "sgemm_moe_sort_workspace_bytes",
-            "sgemm_moe_unpermute", "sgemm_moe_unpermute_backward"),
+            "sgemm_moe_permute", "sgemm_moe_route", "sgemm_moe_route_backward",
+            "sgemm_moe_sort", "sgemm_moe_sort_workspace_bytes", "sgemm_moe_unpermute",
+            "sgemm_moe_unpermute_backward"),
     "norm": ("NORM_SYMBOLS", "layer_norm", "layer_norm_backward", "sgemm_layer_norm",
              "sgemm_layer_norm_backward", "sgemm_layer_norm_backward_workspace_bytes")}
 

@@ -1,6 +1,7 @@
 """Mixture-of-experts routing and the experts' products
 (``include/sgemm_moe.h``), over torch tensors.
 
+    experts, weights = moe_route(logits, top)             # logits: T x E
     offsets, order, place = moe_sort(experts, E)          # experts: T x top ids
     xp = moe_permute(x, place)                            # T·top rows, by expert
     hp = grouped_linear(xp, W1, offsets, b1, "silu")
@@ -20,20 +21,34 @@ import torch
 import tiled_fp32_gemm_amd as sg
 
 from .epilogue import (Epilogue, _act, _check, _device, _epilogue, _float, _matrix, _on, _own,
-                       _sized, _workspace)
+                       _sized, _vector, _workspace)
 
 MOE_SYMBOLS = ("sgemm_moe_sort", "sgemm_moe_sort_workspace_bytes", "sgemm_moe_permute",
                "sgemm_moe_unpermute", "sgemm_moe_unpermute_backward", "sgemm_grouped",
                "sgemm_grouped_workspace_bytes", "sgemm_grouped_wgrad",
                "sgemm_grouped_wgrad_workspace_bytes", "sgemm_grouped_act_backward",
-               "sgemm_grouped_act_backward_workspace_bytes")
+               "sgemm_grouped_act_backward_workspace_bytes", "sgemm_moe_route",
+               "sgemm_moe_route_backward")
 MOE_MAX_EXPERTS = 1024     # SGEMM_MOE_MAX_EXPERTS
+MOE_MAX_TOP = 32           # SGEMM_MOE_MAX_TOP
+MOE_MAX_GROUPS = 32        # SGEMM_MOE_MAX_GROUPS
+SCORINGS = {"softmax": 0, "sigmoid": 1}
+
+
+class Router(ctypes.Structure):
+    """``sgemm_moe_router``."""
+    _fields_ = [("scoring", ctypes.c_int), ("renormalize", ctypes.c_int),
+                ("scale", ctypes.c_float), ("bias", ctypes.c_void_p), ("groups", ctypes.c_int),
+                ("top_groups", ctypes.c_int), ("group_best", ctypes.c_int)]
 
 
 def prototypes(lib) -> None:
     i64, ptr, i32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int
-    ep = ctypes.POINTER(Epilogue)
+    ep, router = ctypes.POINTER(Epilogue), ctypes.POINTER(Router)
     for name, args in {
+            "sgemm_moe_route": [i64, i64, i64, ptr, i64, router, ptr, ptr, ptr],
+            "sgemm_moe_route_backward": [i64, i64, i64, ptr, i64, router, ptr, ptr, ptr, ptr, i64,
+                                         ptr],
             "sgemm_moe_sort": [i64, i64, ptr, i32, ptr, ptr, ptr, ptr, ptr, i64],
             "sgemm_moe_permute": [i64, i64, i64, ptr, i64, ptr, ptr, i64, ptr],
             "sgemm_moe_unpermute": [i64, i64, i64, ptr, i64, ptr, ptr, ptr, i64, ptr],
@@ -66,7 +81,8 @@ def _caller(name: str):
 (sgemm_moe_sort, sgemm_moe_sort_workspace_bytes, sgemm_moe_permute, sgemm_moe_unpermute,
  sgemm_moe_unpermute_backward, sgemm_grouped, sgemm_grouped_workspace_bytes,
  sgemm_grouped_wgrad, sgemm_grouped_wgrad_workspace_bytes, sgemm_grouped_act_backward,
- sgemm_grouped_act_backward_workspace_bytes) = map(_caller, MOE_SYMBOLS)
+ sgemm_grouped_act_backward_workspace_bytes, sgemm_moe_route,
+ sgemm_moe_route_backward) = map(_caller, MOE_SYMBOLS)
 
 
 def _index(t, name: str, dev: int, shape=None) -> int:
@@ -95,6 +111,74 @@ def _weights(weights, dev: int, place):
     if _float(weights, "weights", dev).shape != place.shape or not weights.is_contiguous():
         raise ValueError(f"weights must be contiguous and shaped like place: {tuple(place.shape)}")
     return weights.data_ptr()
+
+
+def _router(scoring, renormalize, scale, bias=None, groups=1, top_groups=1, group_best=1):
+    try:
+        kind = SCORINGS[scoring]
+    except (KeyError, TypeError):
+        raise ValueError(f"scoring must be one of {', '.join(SCORINGS)}: got {scoring!r}") from None
+    for n, name in ((groups, "groups"), (top_groups, "top_groups"), (group_best, "group_best")):
+        if not 1 <= n < 1 << 31:     # the library's are ints
+            raise ValueError(f"{name} must be positive: got {n}")
+    return Router(kind, bool(renormalize), scale, bias, groups, top_groups, group_best)
+
+
+def moe_route(logits, top, scoring="softmax", bias=None, *, groups=1, top_groups=1, group_best=1,
+              renormalize=True, scale=1.0, stream=None):
+    """``(experts, weights)``, T x top each: the ids (int32, the best first) of
+    the experts a token chooses by its ``logits`` (T x E), and their weights.
+
+    The scores are the logits' softmax, or with ``scoring="sigmoid"`` each
+    logit's sigmoid.  ``bias`` (E values) is added to them for the choice alone.
+    With ``groups`` > 1 only experts of the best ``top_groups`` groups of E /
+    ``groups`` neighbours are chosen, a group's score being its best, or with
+    ``group_best=2`` the sum of its best two.  Equal scores go to the lowest id.
+    A weight is the expert's score, over the sum of the chosen ones' with
+    ``renormalize``, times ``scale``.  Experts with a logit of -inf are never
+    chosen; a token with fewer than ``top`` others has ids -1, weights 0.
+    """
+    dev = _device(logits, "logits")
+    T, E, ldl = _matrix(logits, "logits", dev)
+    top = int(top)
+    router = _router(scoring, renormalize, float(scale),
+                     None if bias is None else _vector(bias, "bias", dev, E), int(groups),
+                     int(top_groups), int(group_best))
+
+    def call(s):
+        # No choice is made of refused sizes: the library says so first.
+        shape = (T, min(max(top, 0), MOE_MAX_TOP))
+        experts, weights = logits.new_empty(shape, dtype=torch.int32), logits.new_empty(shape)
+        _check(sg.load().sgemm_moe_route(T, E, top, logits.data_ptr(), ldl, router,
+                                         experts.data_ptr(), weights.data_ptr(), s),
+               "sgemm_moe_route")
+        return experts, weights
+    return _on(dev, stream, call)
+
+
+def moe_route_backward(dweights, logits, experts, weights, scoring="softmax", *, renormalize=True,
+                       scale=1.0, out=None, stream=None):
+    """``dlogits`` (T x E) of ``moe_route`` for the gradient ``dweights`` (T x
+    top) of its weights, with the experts and weights it gave for these logits
+    and the same ``scoring``, ``renormalize`` and ``scale``.  ``out`` receives
+    dlogits and may be ``logits``.  A choice of -1 has no gradient."""
+    dev = _device(dweights, "dweights")
+    T, E, ldl = _matrix(logits, "logits", dev)
+    top = _float(dweights, "dweights", dev).shape[-1] if dweights.dim() == 2 else 0
+    for t, name in ((dweights, "dweights"), (_float(weights, "weights", dev), "weights")):
+        if t.shape != (T, top) or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous and {T} x choices")
+    ids = _index(experts, "experts", dev, (T, top))
+    router = _router(scoring, renormalize, float(scale))
+    ld = max(E, 1) if out is None else _sized(out, "out", dev, T, E)
+
+    def call(s):
+        d = logits.new_empty(T, E) if out is None else out
+        _check(sg.load().sgemm_moe_route_backward(
+            T, E, top, logits.data_ptr(), ldl, router, ids, weights.data_ptr(),
+            dweights.data_ptr(), d.data_ptr(), ld, s), "sgemm_moe_route_backward")
+        return d
+    return _on(dev, stream, call)
 
 
 def moe_sort(experts, num_experts, *, stream=None, workspace=None):

@@ -10,8 +10,9 @@ marshal arguments: every step of the product runs in the HIP kernels.
 dimensions and the stream and calls ``sgemm_ex``.  ``epilogue`` (products
 with an epilogue and their gradients) and ``moe`` (expert routing and the experts'
 products) are the same for ``include/sgemm_linear.h`` and
-``include/sgemm_moe.h``, ``norm`` (layer norm) for ``include/sgemm_norm.h``;
-their functions are names of this module too.
+``include/sgemm_moe.h``, ``norm`` (layer norm) for ``include/sgemm_norm.h`` and
+``xent`` (cross entropy over a vocabulary) for ``include/sgemm_xent.h``; their
+functions are names of this module too.
 
 There is no fallback: if ``libsgemm.so`` has not been built, or does not load,
 importing the binding's functions raises.  Build it with
@@ -41,7 +42,8 @@ __all__ = ["sgemm", "sgemm_ex", "sgemm_plan_query", "sgemm_status_string",
            "moe_route", "moe_route_backward", "moe_sort", "moe_permute", "moe_unpermute",
            "moe_unpermute_backward", "grouped_linear",
            "grouped_linear_backward", "NORM_SYMBOLS", "layer_norm",
-           "layer_norm_backward"]
+           "layer_norm_backward", "XENT_SYMBOLS", "linear_cross_entropy",
+           "linear_cross_entropy_backward"]
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_LAUNCH, ERR_SCRATCH_LIMIT = 0, 1, 2, 3, 4
 NOALLOC_MAX_BYTES = 32 << 20   # SGEMM_NOALLOC_MAX_BYTES
@@ -127,8 +129,8 @@ def load():
     lib.sgemm_workspace_bytes.restype = i64
     lib.sgemm_plan_query_ws.argtypes = common + [i64, ctypes.POINTER(SgemmPlan)]
     lib.sgemm_plan_query_ws.restype = i32
-    from . import epilogue, moe, norm
-    for module in (epilogue, moe, norm):
+    from . import epilogue, moe, norm, xent
+    for module in (epilogue, moe, norm, xent):
         module.prototypes(lib)
     _lib = lib
     return lib
@@ -330,7 +332,11 @@ _LATER = {
             "sgemm_moe_sort", "sgemm_moe_sort_workspace_bytes", "sgemm_moe_unpermute",
             "sgemm_moe_unpermute_backward"),
     "norm": ("NORM_SYMBOLS", "layer_norm", "layer_norm_backward", "sgemm_layer_norm",
-             "sgemm_layer_norm_backward", "sgemm_layer_norm_backward_workspace_bytes")}
+             "sgemm_layer_norm_backward", "sgemm_layer_norm_backward_workspace_bytes"),
+    "xent": ("XENT_SYMBOLS", "linear_cross_entropy", "linear_cross_entropy_backward",
+             "sgemm_linear_xent", "sgemm_linear_xent_backward",
+             "sgemm_linear_xent_backward_least_bytes",
+             "sgemm_linear_xent_backward_workspace_bytes", "sgemm_linear_xent_workspace_bytes")}
 
 
 def __getattr__(name: str):

@@ -48,7 +48,8 @@
 // costs 6 us, GELU 10, a residual 12, all of them and the stored
 // pre-activation 27 (192 MiB more to move).  Split K (splits > 1) stores the
 // partial sums instead; kernel_product_reduce.hpp adds them and applies the
-// epilogue.
+// epilogue.  Another epilogue (FINISH, kernel_xent.hpp) takes the accumulators'
+// rows from LDS the same way.
 #pragma once
 
 #include <type_traits>
@@ -249,11 +250,48 @@ __device__ __forceinline__ void sum_group(const ProductArgs& g, int place, int l
   }
 }
 
-// AFAST: A is M x K.  BFAST: B is N x K.
-template <int BM, int BN, int WM, int WN, int BK_, int KS_, int STAGES_, bool AFAST, bool BFAST>
+// 32 rows of a wave's accumulators into its own part of LDS, 32 TB floats a row.
+template <bool PAIR, int TB>
+__device__ __forceinline__ void put_rows(const f32x16 (&acc)[TB], float* rows, int ln) {
+  const int li = ln & 31, lh = ln >> 5;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    float* p = rows + (8 * (r >> 2) + 4 * lh + (r & 3)) * (32 * TB);
+    if constexpr (PAIR) {
+      const f32x2 v = {acc[0][r], acc[TB - 1][r]};
+      *reinterpret_cast<f32x2*>(p + 2 * li) = v;
+    } else {
+#pragma unroll
+      for (int j = 0; j < TB; ++j) p[32 * j + li] = acc[j][r];
+    }
+  }
+}
+
+// The wave's own LDS: its writes before, its reads after.
+__device__ __forceinline__ void own_lds() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// The epilogue of include/sgemm_linear.h.
+struct LinearFinish {
+  using Args = ProductArgs;
+};
+
+// AFAST: A is M x K.  BFAST: B is N x K.  FINISH: LinearFinish, or a type that
+// takes the rows of A·B instead (then there is no bias, residual, pre-activation or
+// split): its Args derive from ProductArgs; load(g, at, row0, m_left) loads what it
+// needs for rows row0 + at[it] (at[it] < m_left), ahead of row<LPR>(g, it, v, row0,
+// at, col, cols, l) for each `it` with four columns of that row (at: -1 when it is
+// none of C's; cols: how many columns are left, perhaps none), whose lanes
+// l = 0 .. LPR-1 call it together.
+template <int BM, int BN, int WM, int WN, int BK_, int KS_, int STAGES_, bool AFAST, bool BFAST,
+          class FINISH = LinearFinish>
 __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN) * KS_)
-product_kernel(ProductArgs g) {
+product_kernel(typename FINISH::Args g) {
   using Cfg = ProductCfg<BM, BN, WM, WN, BK_, KS_, STAGES_>;
+  constexpr bool kLinear = std::is_same_v<FINISH, LinearFinish>;
   constexpr int S = Cfg::STAGES;
   constexpr int BK = Cfg::BK, NT = Cfg::NT, TA = Cfg::TA, TB = Cfg::TB, CPR = Cfg::CPR;
   constexpr int KS = Cfg::KS, SUB_G = Cfg::SUB_G;
@@ -348,7 +386,7 @@ product_kernel(ProductArgs g) {
         add[it] = load_upto(res + (uint32_t)row * (uint32_t)g.ldr + (uint32_t)col, cols);
     }
   };
-  if (kEarly && grp == 0) {
+  if (kLinear && kEarly && grp == 0) {
     load_bias(lane);
     load_residual(0, lane);
   }
@@ -637,6 +675,25 @@ product_kernel(ProductArgs g) {
   const int col = 4 * (ln % LPR);              // from the wave's first column
   const int cols = n_left - wn0 - col;         // left of this lane's column
   float* const rows = lds + sw * 32 * WN;
+  if constexpr (!kLinear) {
+#pragma unroll
+    for (int i = 0; i < TA; ++i) {
+      int at[IT];
+#pragma unroll
+      for (int it = 0; it < IT; ++it) at[it] = row_of(i, it * RPI + ln / LPR);
+      FINISH finish;
+      finish.template load<IT>(g, at, row0, m_left);
+      put_rows<kPairB>(acc[i], rows, ln);
+      own_lds();
+      f32x4* const mine = reinterpret_cast<f32x4*>(rows) + ln;
+#pragma unroll
+      for (int it = 0; it < IT; ++it)
+        finish.template row<LPR>(g, it, mine[it * 64], row0, at[it] < m_left ? at[it] : -1,
+                                 n0 + wn0 + col, cols, ln % LPR);
+      own_lds();
+    }
+    return;
+  }
   float* out;
   int ld_out;
   if (partial) {
@@ -654,23 +711,9 @@ product_kernel(ProductArgs g) {
   const int act = partial ? SGEMM_ACT_NONE : g.act;
 #pragma unroll
   for (int i = 0; i < TA; ++i) {
-    const int li_c = ln & 31, lh_c = ln >> 5;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      float* p = rows + (8 * (r >> 2) + 4 * lh_c + (r & 3)) * WN;
-      if constexpr (kPairB) {
-        const f32x2 v = {acc[i][0][r], acc[i][TB - 1][r]};
-        *reinterpret_cast<f32x2*>(p + 2 * li_c) = v;
-      } else {
-#pragma unroll
-        for (int j = 0; j < TB; ++j) p[32 * j + li_c] = acc[i][j][r];
-      }
-    }
+    put_rows<kPairB>(acc[i], rows, ln);
     if (!kEarly) load_residual(i, ln);
-    // This wave's own part of LDS: its writes above, then its reads below.
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    own_lds();
     f32x4* const mine = reinterpret_cast<f32x4*>(rows) + ln;
     // A bias alone is added with the residual.
     const bool through = act != SGEMM_ACT_NONE || pre;
@@ -705,9 +748,7 @@ product_kernel(ProductArgs g) {
         else store_upto_once(p, cols, v);
       }
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    own_lds();
   }
 }
 

@@ -1,0 +1,388 @@
+// xent.hip -- the C ABI of include/sgemm_xent.h: argument checks, the plan and its
+// launches.
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+#include <string.h>
+
+#include "../../include/sgemm_linear.h"
+#include "../../include/sgemm_moe.h"
+#include "../../include/sgemm_xent.h"
+#include "kernel_xent.hpp"
+
+namespace {
+
+using namespace sg::host;
+using sg::Targets;
+using sg::XentGatherArgs;
+using sg::XentLossArgs;
+using sg::XentProductArgs;
+using sg::XentRows;
+using sg::XentVariant;
+
+struct Span {
+  const void* p;
+  int64_t bytes;   // 0: not touched; -1: beyond int64
+};
+
+bool overlaps(const Span& a, const Span& b) {
+  return sg::host::overlaps(a.p, a.bytes, b.p, b.bytes);
+}
+
+bool bad(const Span& s) { return s.bytes != 0 && (s.p == nullptr || ((uintptr_t)s.p & 3u)); }
+
+int64_t at_least_one(int64_t n) { return n > 1 ? n : 1; }
+int64_t round_up(int64_t n, int64_t to) { return cdiv(n, to) * to; }
+
+// A leading dimension only matters past the first row.
+int64_t leading(int64_t rows, int64_t width, int64_t ld) {
+  return rows > 1 ? ld : at_least_one(width);
+}
+
+bool sizes_ok(int64_t T, int64_t V, int64_t H) {
+  return T >= 0 && V >= 0 && H >= 0 && T <= kMaxDim && V <= SGEMM_XENT_MAX_LD &&
+         H <= SGEMM_XENT_MAX_LD;
+}
+
+// The tile with the least estimated time for T x V over H; null: no grid holds it.
+const XentVariant* choose(bool trans_b, int64_t T, int64_t V, int64_t H) {
+  const XentVariant* table = trans_b ? sg::xent_variants_ff() : sg::xent_variants_fs();
+  const XentVariant* best = nullptr;
+  double t_best = 0.0;
+  for (int i = 0; i < sg::kXentVariants; ++i) {
+    const TileCost& c = table[i].cost;
+    const int64_t tiles = cdiv(T, c.tile_m) * cdiv(V, c.tile_n);
+    if (!grid_fits(tiles, c.threads)) continue;
+    const double t = estimate_grid(c, tiles, H);
+    if (best == nullptr || t < t_best * 0.995) {
+      best = &table[i];
+      t_best = t;
+    }
+  }
+  return best;
+}
+
+// A workspace handed out front to back, each part on 16 bytes of it.
+struct Room {
+  char* p;
+  int64_t used;
+  template <class T>
+  T* take(int64_t n) {
+    T* at = p ? reinterpret_cast<T*>(p + used) : nullptr;
+    used += round_up(n * (int64_t)sizeof(T), 16);
+    return at;
+  }
+};
+
+XentRows take_rows(Room& room, int64_t T, int64_t H, bool backward) {
+  XentRows r = {};
+  r.offsets = room.take<int32_t>(2);
+  r.order = room.take<int32_t>(T);
+  r.place = room.take<int32_t>(T);
+  r.target = room.take<int32_t>(T);
+  if (backward) {
+    r.lse = room.take<float>(T);
+    r.grad = room.take<float>(T);
+  }
+  r.X = room.take<float>(T * H);
+  return r;
+}
+
+// Copying the rows together takes some 10 us and their traffic, a hundredth of a
+// product that takes this long, and saves the products of the rows left out.
+constexpr double kGatherSeconds = 200e-6;
+
+struct Forward {
+  const XentVariant* v;
+  bool gathered;
+  int strips;
+  XentRows rows;
+  float *max, *sum, *hit;
+  int64_t bytes;
+};
+
+Forward plan_forward(bool trans_b, int64_t T, int64_t V, int64_t H, void* ws) {
+  Forward f = {};
+  f.v = choose(trans_b, T, V, H);
+  if (f.v == nullptr) return f;
+  f.gathered = 2.0 * T * V * H / 150e12 > kGatherSeconds;
+  f.strips = (int)cdiv(V, f.v->strip);
+  Room room = {static_cast<char*>(ws), 0};
+  if (f.gathered) f.rows = take_rows(room, T, H, false);
+  f.max = room.take<float>(f.strips * T);
+  f.sum = room.take<float>(f.strips * T);
+  f.hit = room.take<float>(T);
+  f.bytes = room.used;
+  return f;
+}
+
+// Backward, dZ of a piece takes at most this much where that leaves 1024 columns.
+constexpr int64_t kPieceBytes = int64_t(512) << 20;
+constexpr int64_t kPieceStep = 256;   // columns, the widest tile
+
+int64_t piece_columns(int64_t T, int64_t V, int64_t bytes) {
+  const int64_t n = T > 0 ? bytes / (4 * T) : V;
+  return n >= V ? V : n / kPieceStep * kPieceStep;
+}
+
+struct Backward {
+  XentRows rows;
+  float* dX;       // of the kept rows
+  float* dZ;       // T x columns
+  int64_t columns;
+  int64_t fixed, bytes;   // without dZ; with it
+  int64_t split;   // bytes the products take behind it for their fastest plans
+};
+
+// The plan for `bytes` of workspace, columns 0: too little; bytes < 0: the fastest.
+Backward plan_backward(bool trans_b, int64_t T, int64_t V, int64_t H, void* ws, int64_t bytes) {
+  Backward b = {};
+  Room room = {static_cast<char*>(ws), 0};
+  b.rows = take_rows(room, T, H, true);
+  b.dX = room.take<float>(T * H);
+  b.fixed = room.used;
+  const int64_t least = 4 * at_least_one(T) * 1024;
+  int64_t columns = piece_columns(T, V, kPieceBytes > least ? kPieceBytes : least);
+  if (bytes >= 0) {
+    const int64_t most = piece_columns(T, V, bytes > b.fixed ? bytes - b.fixed : 0);
+    if (most < columns) columns = most;
+  }
+  if (columns > 0) {   // equal pieces
+    const int64_t pieces = cdiv(V, columns);
+    if (pieces > 1) columns = round_up(cdiv(V, pieces), kPieceStep);
+  }
+  b.columns = columns;
+  b.dZ = room.take<float>(T * columns);
+  b.bytes = room.used;
+  const int64_t x = sgemm_grouped_workspace_bytes(!trans_b, T, H, columns, 1);
+  const int64_t w = sgemm_grouped_wgrad_workspace_bytes(trans_b, T, columns, H, 1);
+  b.split = x > w ? x : w;
+  return b;
+}
+
+int launch(const void* fn, int64_t wgs, int threads, void* args, hipStream_t stream) {
+  void* kargs[] = {args};
+  return hipLaunchKernel(fn, dim3((unsigned)wgs), dim3(threads), kargs, 0, stream) == hipSuccess
+             ? SGEMM_OK : SGEMM_ERR_LAUNCH;
+}
+
+int launch_gather(const Targets& targets, const XentRows& rows, int64_t T, int64_t H,
+                  const float* X, int64_t ldx, const float* lse, const float* dloss,
+                  hipStream_t stream) {
+  XentGatherArgs a = {};
+  a.targets = targets;
+  a.rows = rows;
+  a.X = X;
+  a.lse = lse;
+  a.dloss = dloss;
+  a.ldx = ldx;
+  a.T = T;
+  a.H = (int)H;
+  // Up to 512 workgroups: each counts all the targets before its own.
+  a.chunk = (int)round_up(at_least_one(cdiv(T, 512)), sg::kXentBlock);
+  return launch(reinterpret_cast<const void*>(sg::xent_gather_kernel),
+                at_least_one(cdiv(T, a.chunk)), 256, &a, stream);
+}
+
+// Tiles of columns column .. column + V - 1 of op(B).
+int launch_product(const XentVariant& v, XentProductArgs& a, bool grad, hipStream_t stream) {
+  const TileCost& c = v.cost;
+  a.tiles_m = (int)cdiv(a.M, c.tile_m);
+  a.tiles_n = (int)cdiv(a.N, c.tile_n);
+  a.group_m = a.tiles_m < 8 ? a.tiles_m : 8;
+  a.splits = 1;
+  return launch(reinterpret_cast<const void*>(grad ? v.grad : v.stats),
+                (int64_t)a.tiles_m * a.tiles_n, c.threads, &a, stream);
+}
+
+XentProductArgs product_args(int64_t T, int64_t V, int64_t H, const float* X, int64_t ldx,
+                             const float* B, int64_t ldb, const int32_t* offsets) {
+  XentProductArgs a;
+  memset(&a, 0, sizeof(a));
+  a.A = X;
+  a.B = B;
+  a.M = (int)T;
+  a.N = (int)V;
+  a.K = (int)H;
+  a.lda = (int)ldx;
+  a.ldb = (int)ldb;
+  a.ldc = 1;
+  a.mode = offsets ? sg::kRowGroups : sg::kDense;
+  a.groups = 1;
+  a.rows = (int)T;
+  a.offsets = offsets;
+  return a;
+}
+
+// Checks of both calls: sizes, leading dimensions, targets.
+int check(int trans_b, int64_t T, int64_t V, int64_t H, int64_t ldx, int64_t ldb, int id_bytes,
+          const void* targets, int64_t ws_bytes) {
+  if ((trans_b & ~1) || T < 0 || V < 0 || H < 0 || ldx < at_least_one(H) ||
+      ldb < at_least_one(trans_b ? H : V) || (id_bytes != 4 && id_bytes != 8) || ws_bytes < 0 ||
+      ((uintptr_t)targets & (uintptr_t)(id_bytes - 1)))
+    return SGEMM_ERR_INVALID_ARG;
+  if (!sizes_ok(T, V, H) || leading(T, H, ldx) > SGEMM_XENT_MAX_LD ||
+      leading(trans_b ? V : H, trans_b ? H : V, ldb) > SGEMM_XENT_MAX_LD)
+    return SGEMM_ERR_UNSUPPORTED;
+  return SGEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t sgemm_linear_xent_workspace_bytes(int trans_b, int64_t T, int64_t V, int64_t H) {
+  if ((trans_b & ~1) || !sizes_ok(T, V, H) || T == 0) return 0;
+  return plan_forward(trans_b, T, V, H, nullptr).bytes;
+}
+
+int sgemm_linear_xent(int trans_b, int64_t T, int64_t V, int64_t H, const float* X, int64_t ldx,
+                      const float* B, int64_t ldb, const void* targets, int id_bytes, float* loss,
+                      float* lse, hipStream_t stream, void* workspace, int64_t workspace_bytes) {
+  int st = check(trans_b, T, V, H, ldx, ldb, id_bytes, targets, workspace_bytes);
+  if (st == SGEMM_ERR_INVALID_ARG) return st;
+  if (T == 0) return st;
+  const Span in[] = {{X, V > 0 ? span_bytes(T, H, ldx) : 0},
+                     {B, trans_b ? span_bytes(V, H, ldb) : span_bytes(H, V, ldb)},
+                     {targets, T * id_bytes}};
+  const Span out[] = {{loss, 4 * T}, {lse, lse ? 4 * T : 0}};
+  for (const Span& s : in)
+    if (bad(s)) return SGEMM_ERR_INVALID_ARG;
+  for (const Span& s : out)
+    if (bad(s)) return SGEMM_ERR_INVALID_ARG;
+  if (st != SGEMM_OK) return st;
+  const Forward f = plan_forward(trans_b, T, V, H, workspace);
+  if (f.v == nullptr || !grid_fits(cdiv(T, sg::kXentLossRows), 1024)) return SGEMM_ERR_UNSUPPORTED;
+  const Span ws = {workspace, f.bytes};
+  if (workspace_bytes < f.bytes || bad(ws)) return SGEMM_ERR_INVALID_ARG;
+  for (const Span& s : in)
+    if (overlaps(s, out[0]) || overlaps(s, out[1]) || overlaps(s, ws)) return SGEMM_ERR_INVALID_ARG;
+  if (overlaps(out[0], out[1]) || overlaps(out[0], ws) || overlaps(out[1], ws))
+    return SGEMM_ERR_INVALID_ARG;
+
+  ldx = leading(T, H, ldx);
+  ldb = leading(trans_b ? V : H, trans_b ? H : V, ldb);
+  const Targets t = {targets, id_bytes == 8, (int)V};
+  if (V > 0 && f.gathered)
+    st = launch_gather(t, f.rows, T, H, X, ldx, nullptr, nullptr, stream);
+  if (V > 0 && st == SGEMM_OK) {
+    XentProductArgs a = f.gathered
+                            ? product_args(T, V, H, f.rows.X, at_least_one(H), B, ldb, f.rows.offsets)
+                            : product_args(T, V, H, X, ldx, B, ldb, nullptr);
+    a.targets = t;
+    a.order = f.gathered ? f.rows.order : nullptr;
+    a.max = f.max;
+    a.sum = f.sum;
+    a.hit = f.hit;
+    a.ld_strip = (int)T;
+    st = launch_product(*f.v, a, false, stream);
+  }
+  if (st != SGEMM_OK) return st;
+  XentLossArgs l = {};
+  l.targets = t;
+  l.place = f.gathered ? f.rows.place : nullptr;
+  l.max = f.max;
+  l.sum = f.sum;
+  l.hit = f.hit;
+  l.loss = loss;
+  l.lse = lse;
+  l.T = T;
+  l.strips = f.strips;
+  l.ld_strip = (int)T;
+  return launch(reinterpret_cast<const void*>(sg::xent_loss_kernel), cdiv(T, sg::kXentLossRows),
+                1024, &l, stream);
+}
+
+int64_t sgemm_linear_xent_backward_workspace_bytes(int trans_b, int64_t T, int64_t V, int64_t H) {
+  if ((trans_b & ~1) || !sizes_ok(T, V, H)) return 0;
+  const Backward b = plan_backward(trans_b, T, V, H, nullptr, -1);
+  return b.bytes + b.split;
+}
+
+int64_t sgemm_linear_xent_backward_least_bytes(int trans_b, int64_t T, int64_t V, int64_t H) {
+  if ((trans_b & ~1) || !sizes_ok(T, V, H)) return 0;
+  const Backward b = plan_backward(trans_b, T, V, H, nullptr, -1);
+  return b.fixed + round_up(4 * T * (V < kPieceStep ? V : kPieceStep), 16);
+}
+
+int sgemm_linear_xent_backward(int trans_b, int64_t T, int64_t V, int64_t H, const float* X,
+                               int64_t ldx, const float* B, int64_t ldb, const void* targets,
+                               int id_bytes, const float* lse, const float* dloss, float* dX,
+                               int64_t lddx, float* dB, int64_t lddb, hipStream_t stream,
+                               void* workspace, int64_t workspace_bytes) {
+  int st = check(trans_b, T, V, H, ldx, ldb, id_bytes, targets, workspace_bytes);
+  if (st == SGEMM_ERR_INVALID_ARG || (dX && lddx < at_least_one(H)) ||
+      (dB && lddb < at_least_one(trans_b ? H : V)))
+    return SGEMM_ERR_INVALID_ARG;
+  if (H == 0 || (!dX && !dB)) return st;
+  const int64_t br = trans_b ? V : H, bc = trans_b ? H : V;
+  const Span in[] = {{X, V > 0 ? span_bytes(T, H, ldx) : 0},
+                     {B, span_bytes(br, bc, ldb)},
+                     {targets, T * id_bytes},
+                     {lse, 4 * T},
+                     {dloss, 4 * T}};
+  const Span out[] = {{dX, dX ? span_bytes(T, H, lddx) : 0}, {dB, dB ? span_bytes(br, bc, lddb) : 0}};
+  for (const Span& s : in)
+    if (bad(s)) return SGEMM_ERR_INVALID_ARG;
+  for (const Span& s : out)
+    if (bad(s)) return SGEMM_ERR_INVALID_ARG;
+  if (st != SGEMM_OK) return st;
+  if (out[0].bytes < 0 || (dB && leading(br, bc, lddb) > SGEMM_XENT_MAX_LD))
+    return SGEMM_ERR_UNSUPPORTED;
+  const Backward b = plan_backward(trans_b, T, V, H, workspace, workspace_bytes);
+  if (V > 0 && (b.columns == 0 || workspace_bytes < b.bytes)) return SGEMM_ERR_INVALID_ARG;
+  if (workspace_bytes < b.fixed) return SGEMM_ERR_INVALID_ARG;
+  int64_t used = b.bytes + b.split;
+  if (used > workspace_bytes) used = workspace_bytes;
+  const Span ws = {workspace, used};
+  if (bad(ws)) return SGEMM_ERR_INVALID_ARG;
+  for (const Span& s : in)
+    if (overlaps(s, out[0]) || overlaps(s, out[1]) || overlaps(s, ws)) return SGEMM_ERR_INVALID_ARG;
+  if (overlaps(out[0], out[1]) || overlaps(out[0], ws) || overlaps(out[1], ws))
+    return SGEMM_ERR_INVALID_ARG;
+  const XentVariant* v = V > 0 ? choose(trans_b, T, b.columns, H) : nullptr;
+  if ((V > 0 && v == nullptr) || !grid_fits(cdiv(T * cdiv(H, 4), 256), 256))
+    return SGEMM_ERR_UNSUPPORTED;
+
+  ldx = leading(T, H, ldx);
+  ldb = leading(br, bc, ldb);
+  if (dB) lddb = leading(br, bc, lddb);
+  const Targets t = {targets, id_bytes == 8, (int)V};
+  const XentRows& r = b.rows;
+  st = launch_gather(t, r, T, V > 0 ? H : 0, X, ldx, lse, dloss, stream);
+  char* const split = static_cast<char*>(workspace) + b.bytes;
+  const int64_t split_bytes = used - b.bytes;
+  for (int64_t c0 = 0; c0 < V && st == SGEMM_OK; c0 += b.columns) {
+    const int64_t n = V - c0 < b.columns ? V - c0 : b.columns;
+    const float* const Bp = B + (trans_b ? c0 * ldb : c0);
+    if (T > 0) {
+      XentProductArgs a = product_args(T, n, H, r.X, H, Bp, ldb, r.offsets);
+      a.C = b.dZ;
+      a.ldc = (int)b.columns;
+      a.target = r.target;
+      a.lse = r.lse;
+      a.grad = r.grad;
+      a.column0 = (int)c0;
+      st = launch_product(*v, a, true, stream);
+    }
+    if (st == SGEMM_OK && dB)
+      st = sgemm_grouped_wgrad(trans_b, T, n, H, 1, r.offsets, r.X, H, b.dZ, b.columns,
+                               dB + (trans_b ? c0 * lddb : c0), lddb,
+                               span_bytes(trans_b ? n : H, trans_b ? H : n, lddb) / 4, stream,
+                               split, split_bytes);
+    if (st == SGEMM_OK && dX && T > 0) {
+      // The pieces' parts of dX add up in place.
+      sgemm_epilogue add = {};
+      add.residual = c0 > 0 ? b.dX : nullptr;
+      add.ldr = H;
+      st = sgemm_grouped(!trans_b, T, H, n, 1, r.offsets, b.dZ, b.columns, Bp, ldb,
+                         span_bytes(trans_b ? n : H, trans_b ? H : n, ldb) / 4, b.dX, H, &add,
+                         stream, split, split_bytes);
+    }
+  }
+  if (st == SGEMM_OK && dX && T > 0)
+    st = sgemm_moe_unpermute(T, 1, H, b.dX, H, r.place, nullptr, dX, lddx, stream);
+  return st;
+}
+
+}  // extern "C"

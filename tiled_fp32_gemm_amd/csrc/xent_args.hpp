@@ -1,0 +1,83 @@
+// xent_args.hpp -- kernel arguments of the cross entropy over a product.
+#pragma once
+
+#include "host.hpp"
+#include "product_args.hpp"
+
+namespace sg {
+
+// A token's target, or -1 where it has none.
+struct Targets {
+  const void* ids;
+  int wide;        // int64, else int32
+  int V;
+
+  __device__ __forceinline__ int of(int64_t t) const {
+    const int64_t id = wide ? static_cast<const int64_t*>(ids)[t]
+                            : (int64_t)static_cast<const int32_t*>(ids)[t];
+    return id >= 0 && id < V ? (int)id : -1;
+  }
+};
+
+// The rows with a target, one after another ("kept" rows), made on the device.
+// Row r is token order[r]; token t is row place[t], or -1.
+struct XentRows {
+  int32_t* offsets;   // 0 and how many: one group of kRowGroups
+  int32_t* order;
+  int32_t* place;
+  int32_t* target;    // of each kept row
+  float* lse;         // backward: as given
+  float* grad;        // backward: dloss
+  float* X;           // the rows, T x H
+};
+
+struct XentProductArgs : ProductArgs {
+  // Forward.
+  Targets targets;
+  const int32_t* order;   // null: row r is token r
+  float* max;             // [strip][row]: a row's largest logit in a strip of columns
+  float* sum;             // and the sum of exp(logit - it)
+  float* hit;             // [row]: the target's logit
+  int ld_strip;           // rows
+  // Backward.
+  const int32_t* target;
+  const float* lse;
+  const float* grad;
+  int column0;            // the first column's number in the vocabulary
+};
+
+struct XentGatherArgs {
+  Targets targets;
+  XentRows rows;
+  const float* X;
+  const float* lse;      // null: forward
+  const float* dloss;
+  int64_t ldx, T;
+  int H, chunk;          // tokens of a workgroup, a multiple of kXentBlock
+};
+
+struct XentLossArgs {
+  Targets targets;
+  const int32_t* place;   // null: token t is row t
+  const float* max;
+  const float* sum;
+  const float* hit;
+  float* loss;
+  float* lse;             // null: not wanted
+  int64_t T;
+  int strips, ld_strip;
+};
+
+// A tile of the product with either epilogue.
+struct XentVariant {
+  host::TileCost cost;
+  int strip;                            // columns of a wave
+  void (*stats)(XentProductArgs);
+  void (*grad)(XentProductArgs);
+};
+
+constexpr int kXentVariants = 6;
+const XentVariant* xent_variants_ff();   // B is V x H
+const XentVariant* xent_variants_fs();   // B is H x V
+
+}  // namespace sg

@@ -3,7 +3,7 @@ definition in 64 bits.  The ids have to be equal.
 
 Tolerances of the weights, relative, from FP32 arithmetic (u = 2^-24): an
 exponential is within 8 u and its argument's rounding, u times the distance d from
-the largest logit; a softmax's sum adds 28 u and the same of its terms, a quotient
+the largest logit; a softmax's sum adds 31 u and the same of its terms, a quotient
 or reciprocal 3 u, the scale u; a sum over the chosen 32 u.
   softmax              (d + 48) u          softmax, renormalised   (d + D + 64) u
   sigmoid              16 u                sigmoid, renormalised   (d + D + 80) u

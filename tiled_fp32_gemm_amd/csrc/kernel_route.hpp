@@ -13,8 +13,9 @@
 // The choice is that of exact scores.  Without a bias, and without groups that
 // count two scores, it goes by the logits themselves, whose order is the scores'.
 // Otherwise FP32 scores decide unless two that matter are closer than their
-// errors (near() below); then the wave computes that token's scores and choice
-// again in FP64 (refine), which happens to one token in some hundreds.
+// errors (near() below), as for one token in about a thousand; then the wave
+// computes the scores again in FP64, those that may be chosen (reorder), or all
+// where the groups are open or there are too many (refine).
 #pragma once
 
 #include "../../include/sgemm_moe.h"
@@ -42,7 +43,7 @@ struct RouteArgs {
 
 // The group of an expert, without a division: exact below 1024.
 __device__ __forceinline__ int group_of(const RouteArgs& a, int expert) {
-  return (int)((uint32_t)expert * (uint32_t)a.per >> 20);
+  return (int)(__umul24((uint32_t)expert, (uint32_t)a.per) >> 20);
 }
 
 // Lane exchange within groups of G lanes: step s of the butterfly.  The mirrors
@@ -92,28 +93,31 @@ __device__ __forceinline__ float group_max(float v) {
 }
 
 // A float's bits as an unsigned number of the same order; NaN is infinity, and -0
-// is 0.  0 is no float's: an expert that cannot be chosen.
-__device__ __forceinline__ uint32_t ordered(float f) {
-  f = f != f ? INFINITY : f + 0.0f;
+// is 0.  An expert that cannot be chosen has -infinity's, which is the least.
+__device__ __forceinline__ uint32_t ordered_bits(float f) {
   const uint32_t b = __builtin_bit_cast(uint32_t, f);
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ uint32_t ordered(float f) {
+  return ordered_bits(fminf(f, INFINITY) + 0.0f);
 }
 __device__ __forceinline__ float unordered(uint32_t k) {
   return __builtin_bit_cast(float, k ^ ((uint32_t)((int32_t)~k >> 31) | 0x80000000u));
 }
+constexpr uint32_t kNever = 0x007FFFFFu;   // ordered(-INFINITY)
 
 __device__ __forceinline__ double packed(uint32_t key, int expert) {
-  const uint32_t hi = key >> 21 | 0x40000000u, lo = key << 11 | (uint32_t)(2047 - expert);
-  return key == 0u ? 0.0 : __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+  const uint32_t hi = __builtin_amdgcn_alignbit(0x200u, key, 21);   // an exponent before it
+  const uint32_t lo = key << 11 | (uint32_t)(2047 - expert);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
-// -1: none.
+__device__ __forceinline__ uint32_t packed_key(double d) {
+  return (uint32_t)(__builtin_bit_cast(uint64_t, d) >> 11);
+}
+// -1: none (0.0 is a place of a list that is not full).
 __device__ __forceinline__ int packed_expert(double d) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, d);
-  return b == 0 ? -1 : 2047 - (int)((uint32_t)b & 2047u);
-}
-__device__ __forceinline__ float packed_score(double d) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, d);
-  return unordered((uint32_t)(b >> 11));
+  return packed_key(d) <= kNever ? -1
+                                 : 2047 - (int)((uint32_t)__builtin_bit_cast(uint64_t, d) & 2047u);
 }
 
 __device__ __forceinline__ void larger_first(double& a, double& b) {
@@ -156,85 +160,151 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-__device__ __forceinline__ bool choosable(double v) { return !(v == -(double)INFINITY); }
+// Over a whole wave, all lanes with the same bits.
+template <class F>
+__device__ __forceinline__ double over_wave(double v, F f) {
+  butterfly<16>([&](auto s) { v = f(v, exchanged<decltype(s)::value>(v)); });
+  auto of = [&](int lane) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+  };
+  return f(f(of(0), of(16)), f(of(32), of(48)));
+}
 
-// One token's choice from scores in FP64, by a whole wave; `score` has room for E.
-__device__ __forceinline__ void refine(const RouteArgs& a, int64_t t, double* score, int* ids) {
+// A token's scores in FP64, by a whole wave: `top` and `sum` of its softmax.
+struct Exact {
+  double top, sum;
+
+  template <int Q>
+  __device__ __forceinline__ void prepare(const RouteArgs& a, const float* row) {
+    top = sum = 0.0;
+    if (a.scoring != SGEMM_SCORE_SOFTMAX) return;
+    const int lane = (int)threadIdx.x & 63;
+    double l[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      l[q] = lane + 64 * q < a.E ? (double)row[lane + 64 * q] : -(double)INFINITY;
+    top = l[0];
+#pragma unroll
+    for (int q = 1; q < Q; ++q) top = fmax(top, l[q]);
+    top = over_wave(top, [](double x, double y) { return fmax(x, y); });
+#pragma unroll
+    for (int q = 0; q < Q; ++q) sum += exp(l[q] - top);
+    sum = over_wave(sum, [](double x, double y) { return x + y; });
+  }
+  // What an expert is chosen by; -infinity: not to be chosen.
+  __device__ __forceinline__ double of(const RouteArgs& a, const float* row, int e) const {
+    const double l = (double)row[e], b = a.bias ? (double)a.bias[e] : 0.0;
+    const double s = (a.scoring == SGEMM_SCORE_SOFTMAX ? exp(l - top) / sum
+                                                       : 1.0 / (1.0 + exp(-l))) + b;
+    return l == -(double)INFINITY ? l : s != s ? (double)INFINITY : s;
+  }
+};
+
+// The two ways back for a token that FP32 leaves open, each by a whole wave.  A
+// launch ends with a wave that is here, so their chains are short.
+//
+// The order of `n` candidates, one a lane, among which the choice is.
+template <int Q>
+__device__ __forceinline__ void reorder(const RouteArgs& a, int64_t t, const int* list, int n,
+                                        int* ids) {
+  const int lane = (int)threadIdx.x & 63;
+  const float* const row = a.logits + t * a.ld;
+  const int e = lane < n ? list[lane] : 0;
+  Exact exact;
+  exact.prepare<Q>(a, row);
+  const double c = exact.of(a, row, e);
+  int rank = 0;
+  for (int i = 0; i < n; ++i) {
+    const double other = __shfl(c, i);
+    const int o = __shfl(e, i);
+    rank += other > c || (other == c && o < e) ? 1 : 0;
+  }
+  if (lane < n && rank < a.top) ids[rank] = e;
+}
+
+// The whole choice; Q experts a lane, `room` for all of them.
+template <int Q>
+__device__ __forceinline__ void refine(const RouteArgs& a, int64_t t, double* room, int* ids) {
   const int lane = (int)threadIdx.x & 63;
   const float* const row = a.logits + t * a.ld;
   const double none = -(double)INFINITY;
-  double top = none, sum = 0.0;
-  if (a.scoring == SGEMM_SCORE_SOFTMAX) {
-    for (int e = lane; e < a.E; e += 64) top = fmax(top, (double)row[e]);
-    for (int d = 32; d > 0; d >>= 1) top = fmax(top, __shfl_xor(top, d));
-    for (int e = lane; e < a.E; e += 64) sum += exp((double)row[e] - top);
-    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
-  }
-  for (int e = lane; e < a.E; e += 64) {
-    const double x = (double)row[e];
-    double c = a.scoring == SGEMM_SCORE_SOFTMAX ? exp(x - top) / sum : 1.0 / (1.0 + exp(-x));
-    if (a.bias) c += (double)a.bias[e];
-    score[e] = !choosable(x) ? none : c != c ? (double)INFINITY : c;
-  }
-  wave_lds_fence();
-  uint32_t stays = ~0u;
+  Exact exact;
+  exact.prepare<Q>(a, row);
+  double c[Q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+    c[q] = lane + 64 * q < a.E ? exact.of(a, row, lane + 64 * q) : none;
   if (a.groups > 1) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      if (lane + 64 * q < a.E) room[lane + 64 * q] = c[q];
+    wave_lds_fence();
     double best = none, second = none;
-    if (lane < a.groups)
-      for (int e = lane * a.size; e < (lane + 1) * a.size; ++e) {
-        const double v = score[e];
+    if (lane < a.groups) {
+#pragma unroll 8
+      for (int i = 0; i < a.size; ++i) {
+        const double v = room[lane * a.size + i];
         second = fmax(second, fmin(v, best));
         best = fmax(best, v);
       }
-    if (a.group_best == 2 && choosable(second)) best += second;
+    }
+    if (a.group_best == 2 && second != none) best += second;
     int rank = 0;
     for (int q = 0; q < a.groups; ++q) {
       const double other = __shfl(best, q);
       rank += other > best || (other == best && q < lane) ? 1 : 0;
     }
-    stays = (uint32_t)__ballot(lane < a.groups && rank < a.top_groups);
+    const uint32_t stays = (uint32_t)__ballot(lane < a.groups && rank < a.top_groups);
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      if (!(stays >> group_of(a, min(lane + 64 * q, a.E - 1)) & 1)) c[q] = none;
+    wave_lds_fence();   // `room` is read before another token's scores
   }
   for (int j = 0; j < a.top; ++j) {
-    double best = none;
-    int at = a.E;
-    for (int e = lane; e < a.E; e += 64) {
-      const double v = score[e];
-      if (v > best && (stays >> group_of(a, e) & 1)) {
-        best = v;
-        at = e;
+    double best = c[0];
+#pragma unroll
+    for (int q = 1; q < Q; ++q) best = fmax(best, c[q]);
+    best = over_wave(best, [](double x, double y) { return fmax(x, y); });
+    int at = -1;
+    if (best != none) {
+#pragma unroll
+      for (int q = Q - 1; q >= 0; --q) {
+        const uint64_t hit = __ballot(c[q] == best);
+        if (hit != 0) at = 64 * q + __ffsll((unsigned long long)hit) - 1;
       }
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+        if (at == lane + 64 * q) c[q] = none;
     }
-    for (int d = 32; d > 0; d >>= 1) {
-      const double v = __shfl_xor(best, d);
-      const int e = __shfl_xor(at, d);
-      if (v > best || (v == best && e < at)) {
-        best = v;
-        at = e;
-      }
-    }
-    if (lane == 0) {
-      ids[j] = at < a.E ? at : -1;
-      if (at < a.E) score[at] = none;
-    }
-    wave_lds_fence();
+    if (lane == 0) ids[j] = at;
   }
 }
 
-// What FP32 scores may be off, in half steps of 2^-24.  exp_accurate and the
-// reciprocal are within 8 of their value, a softmax's exponent adds its own
-// distance from the largest (0.37 of the largest score at most) and the sum of
-// the exponentials 28 (13 additions in a row, 8 of each term, ln E of the
-// exponents), which all scores share but which moves them against the bias.  Two
-// such errors, rounded up; beside them the addition of the bias rounds once.
+// What FP32 scores may be off, in half steps of 2^-24.  quick_exp(x) is within 2 + 2
+// |x| of its value (the product rounds, and so does log2 e).
+//   sigmoid  s (1 - s) (2 + 2 |x|) <= 0.95, and three more of s: 4
+//   softmax  d from the largest, s (2 + 2 d) <= 2.74 of the largest score; the sum
+//            of the exponentials (13 additions in a row, 2 + 2 d of each term,
+//            where the mean of d is at most ln 1024) 29, and its reciprocal 2, which
+//            all scores share but which moves them against the bias: 34
+// Two such errors, rounded up; beside them the addition of the bias rounds once.
 constexpr float kHalfStep = 5.9604645e-8f;
-constexpr float kSoftmaxOff = 96.0f * kHalfStep, kSigmoidOff = 24.0f * kHalfStep;
+constexpr float kSoftmaxOff = 80.0f * kHalfStep, kSigmoidOff = 10.0f * kHalfStep;
+
+__device__ __forceinline__ float quick_exp(float x) {
+  return __builtin_amdgcn_exp2f(x * 1.44269502f);
+}
 
 template <int G, int V, int K>
-__global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
+__global__ void __launch_bounds__(256, K <= 8 ? 4 : 2) route_kernel(RouteArgs a) {
   constexpr int TOKENS = 256 / G, N = 4 * V;
   // Each wave has its tokens' part of both.
   __shared__ __attribute__((aligned(16))) uint32_t keys[TOKENS * N * G];
   __shared__ int ids[TOKENS][kRouteTop];
+  __shared__ int candidates[TOKENS];
   static_assert(64 / G * N * G * 4 >= N * G * 8, "a wave's keys hold one token's FP64 scores");
   const int lane = (int)threadIdx.x & 63, g = (int)threadIdx.x % G;
   const int sub = (int)threadIdx.x / G;
@@ -245,59 +315,74 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
   const bool by_score = a.bias || (a.groups > 1 && a.group_best > 1);
   const bool whole = a.scoring == SGEMM_SCORE_SOFTMAX && (by_score || !a.renormalize);
 
-  float c[N];   // the logits, then what the choice goes by
-  bool can[N];
+  // The logits; -infinity: not to be chosen.
+  float c[N];
+  const int last = 4 * ((a.E - 1) / 4);   // where the last group of four begins
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int col = 4 * (g + i * G), left = a.E - col;
-    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (left > 0) v = load_upto(row + col, left);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      c[4 * i + e] = v[e];
-      can[4 * i + e] = e < left && !(v[e] == -INFINITY);
+    const int col = 4 * (g + i * G);
+    f32x4 v;
+    if (a.E % 4 == 0) {   // without a branch for each
+      v = *reinterpret_cast<const f32x4u*>(row + min(col, last));
+    } else {
+      v = load_upto(row + min(col, last), a.E - min(col, last));
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[4 * i + e] = col + e < a.E ? v[e] : -INFINITY;
   }
   float top = -INFINITY, inv = 1.0f;   // of the whole softmax
   float off = kSigmoidOff;
   if (whole) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (can[i]) top = fmaxf(top, c[i]);
+    for (int i = 0; i < N; ++i) top = fmaxf(top, c[i]);
     top = group_max<G>(top);
     f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float p = exp_accurate(c[i] - top);
-      if (by_score) c[i] = p;
-      if (can[i]) sum[i & 3] += p;
+      const float p = quick_exp(c[i] - top);   // 0 for -infinity
+      sum[i & 3] += p;
+      if (by_score) c[i] = c[i] == -INFINITY ? c[i] : p;
     }
     inv = 1.0f / group_sum<G>((sum[0] + sum[1]) + (sum[2] + sum[3]));
     off = kSoftmaxOff * inv;
   }
+  uint32_t key[N];
   if (by_score) {
+    f32x4 b[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int col = 4 * (g + i * G), left = a.E - col;
-      f32x4 b = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (a.bias && left > 0) b = load_upto(a.bias + col, left);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float s = whole ? c[4 * i + e] * inv : sigmoid(c[4 * i + e]);
-        c[4 * i + e] = s + b[e];
-        can[4 * i + e] = can[4 * i + e] && !(c[4 * i + e] == -INFINITY);
+      const int col = min(4 * (g + i * G), last);
+      b[i] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (a.bias) {
+        if (a.E % 4 == 0) b[i] = *reinterpret_cast<const f32x4u*>(a.bias + col);
+        else b[i] = load_upto(a.bias + col, a.E - col);
       }
     }
+    // A score and a bias are -0 together only, where the score is 0.
+    auto score_key = [&](int i, float s) {
+      s += b[i >> 2][i & 3];
+      uint32_t k = ordered_bits(fminf(s, INFINITY));
+      asm("" : "+v"(k));   // made for every lane, not in a branch of its own
+      key[i] = c[i] == -INFINITY ? kNever : k;
+    };
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) score_key(i, c[i] * inv);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        score_key(i, __builtin_amdgcn_rcpf(1.0f + quick_exp(-c[i])));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) key[i] = ordered(c[i]);
   }
   // Whether two scores are too near each other to tell which is larger.
   auto near = [&](float x, float y) {
     return x - y <= off + 2.0f * kHalfStep * (fabsf(x) + fabsf(y));
   };
-  bool unsure = false;
+  bool regroup = false, unsure = false;   // of the groups, of the experts
 
-  uint32_t key[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) key[i] = can[i] ? ordered(c[i]) : 0u;
   if (a.groups > 1) {
     // Lane g looks at groups g, g + G ..: the best and second best of each, then
     // how many groups come before it.
@@ -316,17 +401,32 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
 #pragma unroll
     for (int r = 0; r < ROUNDS; ++r) {
       const int q = r * G + g;
-      total[r] = 0u;
+      total[r] = kNever;
       if (r * G < a.groups && q < a.groups) {
-        uint32_t best = 0u, second = 0u;
-        int at = g % size;   // neighbouring groups may begin on the same bank
-        for (int i = 0; i < size; ++i) {
-          const uint32_t k = mine[q * size + at];
-          at = at + 1 == size ? 0 : at + 1;
-          second = max(second, min(k, best));
-          best = max(best, k);
+        uint32_t best = kNever, second = kNever;
+        // Neighbouring groups may begin on the same bank: lanes start apart.
+        if (size % 4 == 0) {
+          int at = 4 * g % size;
+#pragma unroll 4
+          for (int i = 0; i < size; i += 4) {
+            const u32x4 k = *reinterpret_cast<const u32x4*>(mine + q * size + at);
+            at = at + 4 == size ? 0 : at + 4;
+            const uint32_t h0 = max(k[0], k[1]), l0 = min(k[0], k[1]);
+            const uint32_t h1 = max(k[2], k[3]), l1 = min(k[2], k[3]);
+            const uint32_t h = max(h0, h1);
+            second = max(max(second, min(best, h)), max(max(l0, l1), min(h0, h1)));
+            best = max(best, h);
+          }
+        } else {
+          int at = g % size;
+          for (int i = 0; i < size; ++i) {
+            const uint32_t k = mine[q * size + at];
+            at = at + 1 == size ? 0 : at + 1;
+            second = max(second, min(k, best));
+            best = max(best, k);
+          }
         }
-        total[r] = a.group_best == 2 && second != 0u
+        total[r] = a.group_best == 2 && second != kNever
                        ? ordered(unordered(best) + unordered(second)) : best;
       }
     }
@@ -336,7 +436,7 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
       if (r * G < a.groups && r * G + g < a.groups) mine[r * G + g] = total[r];
     wave_lds_fence();
     uint32_t stays = 0;
-    uint32_t last = 0u, next = 0u;   // the last group that stays, the first that does not
+    uint32_t least = 0u, next = 0u;   // the last group that stays, the first that does not
 #pragma unroll
     for (int r = 0; r < ROUNDS; ++r) {
       if (r * G < a.groups) {
@@ -346,7 +446,7 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
           const uint32_t other = mine[o];
           rank += other > total[r] || (other == total[r] && o < q) ? 1 : 0;
         }
-        if (rank == a.top_groups - 1) last = total[r];
+        if (rank == a.top_groups - 1) least = total[r];
         if (rank == a.top_groups) next = total[r];
         const uint64_t bits = __ballot(rank < a.top_groups) >> (lane - g);
         stays |= (uint32_t)(bits & ((uint64_t(1) << G) - 1)) << (r * G);
@@ -354,26 +454,33 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
     }
     if (by_score && a.top_groups < a.groups) {
       butterfly<G>([&](auto s) {
-        last = max(last, (uint32_t)exchanged<decltype(s)::value>((int)last));
+        least = max(least, (uint32_t)exchanged<decltype(s)::value>((int)least));
         next = max(next, (uint32_t)exchanged<decltype(s)::value>((int)next));
       });
       // Two scores a group: twice the errors.
-      if (next != 0u) {
-        const float x = unordered(last), y = unordered(next);
-        unsure = x - y <= 2.0f * off + 8.0f * kHalfStep * (fabsf(x) + fabsf(y));
+      if (next > kNever) {
+        const float x = unordered(least), y = unordered(next);
+        regroup = x - y <= 2.0f * off + 8.0f * kHalfStep * (fabsf(x) + fabsf(y));
       }
     }
+    if (size % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int e = 4 * (g + (i >> 2) * G) + (i & 3);
-      if (e < a.E && !(stays >> group_of(a, e) & 1)) key[i] = 0u;
+      for (int i = 0; i < V; ++i) {
+        const bool gone = !(stays >> group_of(a, min(4 * (g + i * G), last)) & 1);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) key[4 * i + e] = gone ? kNever : key[4 * i + e];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int e = min(4 * (g + (i >> 2) * G) + (i & 3), a.E - 1);
+        key[i] = stays >> group_of(a, e) & 1 ? key[i] : kNever;
+      }
     }
   }
 
   // This lane's best K, then all lanes'.
   double best[K];
-#pragma unroll
-  for (int j = 0; j < K; ++j) best[j] = 0.0;
 #pragma unroll
   for (int i0 = 0; i0 < N; i0 += K) {
     double v[K];
@@ -401,34 +508,60 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
     if (j % G == g && j < a.top) ids[sub][j] = packed_expert(best[j]);
 
   if (by_score) {
-    float least = -INFINITY;   // the last one chosen
-    bool full = false;
+    uint32_t chosen = 0u;   // the last one's key
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-      if (j + 1 < K && j + 1 < a.top && packed_expert(best[j + 1 < K ? j + 1 : 0]) >= 0 &&
-          near(packed_score(best[j]), packed_score(best[j + 1 < K ? j + 1 : 0])))
-        unsure = true;
-      if (j == a.top - 1 && packed_expert(best[j]) >= 0) {
-        least = packed_score(best[j]);
-        full = true;
+      const uint32_t k = packed_key(best[j]);
+      if (j + 1 < K && j + 1 < a.top) {
+        const uint32_t after = packed_key(best[j + 1 < K ? j + 1 : 0]);
+        unsure = unsure || (after > kNever && near(unordered(k), unordered(after)));
       }
+      if (j == a.top - 1) chosen = k;
     }
-    // No other may be near the last one.
+    // No other may be near the last one: from its score down to where near() ends
+    // (a little below, as |y| is |x| but for that).
+    const float x = unordered(chosen);
+    const uint32_t from = ordered(x - 1.01f * (off + 4.0f * kHalfStep * fabsf(x)));
     int close = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      close += key[i] != 0u && near(least, unordered(key[i])) ? 1 : 0;
+    for (int i = 0; i < N; ++i) close += key[i] >= from ? 1 : 0;
     close = group_sum<G>(close);
-    if (full && close > a.top) unsure = true;
-    uint64_t again = __ballot(unsure && live);
-    double* const room = reinterpret_cast<double*>(keys + (sub - lane / G) * (N * G));
-    wave_lds_fence();
-    while (again != 0) {
-      const int first = __ffsll((unsigned long long)again) - 1;
-      const int of = first / G;   // of the wave's tokens
-      const int64_t token = (int64_t)blockIdx.x * TOKENS + (sub - lane / G) + of;
-      refine(a, token, room, ids[sub - lane / G + of]);
-      again &= ~(((uint64_t(1) << G) - 1) << (of * G));
+    unsure = unsure || (chosen > kNever && close > a.top);
+    // A token's lanes agree on both.
+    if (__ballot((unsure || regroup) && live) != 0) {
+      constexpr int MOST = N * G < 64 ? N * G : 64;
+      const int first = sub - lane / G;   // the wave's first token
+      int* const list = reinterpret_cast<int*>(keys + sub * (N * G));
+      if (g == 0) candidates[sub] = 0;
+      wave_lds_fence();
+      if (unsure && !regroup) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          if (key[i] >= from && key[i] > kNever) {
+            const int slot = atomicAdd(&candidates[sub], 1);
+            if (slot < MOST) list[slot] = 4 * (g + (i >> 2) * G) + (i & 3);
+          }
+        }
+      }
+      wave_lds_fence();
+      const bool whole_choice = regroup || candidates[sub] > MOST;
+      constexpr int Q = (N * G + 63) / 64;
+      auto each = [&](bool mine, auto f) {
+        for (uint64_t left = __ballot(mine && live); left != 0;) {
+          const int of = (__ffsll((unsigned long long)left) - 1) / G;   // of the wave's tokens
+          f(first + of, (int64_t)blockIdx.x * TOKENS + first + of);
+          left &= ~(((uint64_t(1) << G) - 1) << (of * G));
+        }
+      };
+      each(unsure && !whole_choice, [&](int at, int64_t token) {
+        reorder<Q>(a, token, reinterpret_cast<const int*>(keys + at * (N * G)), candidates[at],
+                   ids[at]);
+      });
+      wave_lds_fence();
+      // These need the lists' room.
+      each(whole_choice, [&](int at, int64_t token) {
+        refine<Q>(a, token, reinterpret_cast<double*>(keys + first * (N * G)), ids[at]);
+      });
     }
   }
   wave_lds_fence();

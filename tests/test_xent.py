@@ -3,14 +3,17 @@
 
 Tolerances, from FP32 arithmetic (u = 2^-24; S(n) = min(1e-5, (n + 3) u)):
   z     S(H) (|A|·|B|), called e
-  lse   moves by no more than the largest e of its row; an exponential is within 8 u
-        and its argument's rounding, u (lse - z), whose mean under the softmax is at
-        most ln V (the entropy); the sum of V of them goes by 4 columns, 4 steps over
-        lanes, strips of 32 or 64 columns in 64 parts eight at a time, and 6 halves:
-        (40 + V / 2048) u; m and log s are rounded once each and added
+  lse   moves by no more than the largest e of its row; an exponential is within 2 u
+        and 1.22 u times its distance from its reference, twice (in its strip, and its
+        strip's among the others), whose means under the softmax are at most ln V (the
+        entropy) in sum; the sum of V of them goes by 4 columns, 4 steps over lanes,
+        strips of 32 or 64 columns in 64 parts sixteen at a time, and 6 halves: with
+        that (40 + V / 2048 + 8 + ln V) u, as 1.22 ln V <= ln V + 4 below 2^20; m and
+        log s are rounded once each and added
   loss  the same, and e at the target
-  dz    relative to |dloss| p, e at its place, u |z - lse| and 8 u; 2 u of p and of
-        the target's 1
+  dz    relative to |dloss| p, e at its place, and an exponential by a power of two:
+        its argument (z - lse) log2 e is rounded twice, u |z - lse| each, log2 e is off
+        by 0.22 u of it, the power by 2 u; 2 u of p and of the target's 1
   dA, dB   dz's error carried over, S of the products' lengths over |dz|·|B| and
         |A|·|dz|; a vocabulary in n pieces adds n roundings of dA's partial sums
 FP32 has no normal number below 2^-126 (probabilities of 1e-305 that FP64 has are 0
@@ -69,7 +72,7 @@ def grads64(dloss, A, B, targets, lse, tb, pieces=64):
     hit = torch.zeros_like(p)
     hit[kept, targets[kept].long()] = 1.0
     dz = (p - hit) * g
-    rel = e + U * (z - l).abs() + 10 * U
+    rel = e + 2.3 * U * (z - l).abs() + 10 * U
     tiny = 2.0 ** -126
     dtol = g.abs() * (p * (rel + rel * rel) + 2 * U * (p + hit) + tiny) + tiny
     a, b = a.double(), (B.t() if tb else B).double()

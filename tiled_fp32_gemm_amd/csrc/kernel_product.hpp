@@ -282,10 +282,9 @@ struct LinearFinish {
 // AFAST: A is M x K.  BFAST: B is N x K.  FINISH: LinearFinish, or a type that
 // takes the rows of A·B instead (then there is no bias, residual, pre-activation or
 // split): its Args derive from ProductArgs; load(g, at, row0, m_left) loads what it
-// needs for rows row0 + at[it] (at[it] < m_left), ahead of row<LPR>(g, it, v, row0,
-// at, col, cols, l) for each `it` with four columns of that row (at: -1 when it is
-// none of C's; cols: how many columns are left, perhaps none), whose lanes
-// l = 0 .. LPR-1 call it together.
+// needs for rows row0 + at[it] (at[it] < m_left), ahead of rows<LPR>(g, v, at, row0,
+// m_left, col, cols, l) with four columns of each of those rows (cols: how many are
+// left, perhaps none), which lanes l = 0 .. LPR-1 of a row call together.
 template <int BM, int BN, int WM, int WN, int BK_, int KS_, int STAGES_, bool AFAST, bool BFAST,
           class FINISH = LinearFinish>
 __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN) * KS_)
@@ -685,11 +684,10 @@ product_kernel(typename FINISH::Args g) {
       finish.template load<IT>(g, at, row0, m_left);
       put_rows<kPairB>(acc[i], rows, ln);
       own_lds();
-      f32x4* const mine = reinterpret_cast<f32x4*>(rows) + ln;
+      f32x4 v[IT];
 #pragma unroll
-      for (int it = 0; it < IT; ++it)
-        finish.template row<LPR>(g, it, mine[it * 64], row0, at[it] < m_left ? at[it] : -1,
-                                 n0 + wn0 + col, cols, ln % LPR);
+      for (int it = 0; it < IT; ++it) v[it] = reinterpret_cast<f32x4*>(rows)[ln + it * 64];
+      finish.template rows<LPR, IT>(g, v, at, row0, m_left, n0 + wn0 + col, cols, ln % LPR);
       own_lds();
     }
     return;

@@ -20,19 +20,18 @@
 
 #include <float.h>
 
-#include "activation.hpp"
 #include "rows.hpp"
 #include "xent_args.hpp"
 
 namespace sg {
 
 // A workgroup takes a chunk of tokens, kXentBlock at a time: counts the rows with a
-// target before its chunk, numbers its own, and its waves copy their rows of X.
-constexpr int kXentBlock = 32;
+// target before its chunk, numbers its own, and its waves copy their rows of X, two
+// each.
+constexpr int kXentBlock = 8;
 
 __global__ void __launch_bounds__(256) xent_gather_kernel(XentGatherArgs a) {
   __shared__ int part[4];
-  __shared__ int row_of[kXentBlock];
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t first = (int64_t)blockIdx.x * a.chunk, last = min(first + a.chunk, a.T);
   int before = 0;
@@ -43,35 +42,43 @@ __global__ void __launch_bounds__(256) xent_gather_kernel(XentGatherArgs a) {
   __syncthreads();
   before = part[0] + part[1] + part[2] + part[3];
   for (int64_t t0 = first; t0 < last; t0 += kXentBlock) {
+    // Every wave numbers the block's rows for itself.
     const int64_t t = t0 + lane;
     const int target = lane < kXentBlock && t < last ? a.targets.of(t) : -1;
-    const uint64_t kept = __ballot(target >= 0);   // the same in every wave
+    const uint64_t kept = __ballot(target >= 0);
     const int row = target >= 0 ? before + __popcll(kept & ((uint64_t(1) << lane) - 1)) : -1;
     if (wave == 0 && lane < kXentBlock && t < last) {
-      row_of[lane] = row;
       a.rows.place[t] = row;
       if (row >= 0) {
-        a.rows.order[row] = (int)t;
-        a.rows.target[row] = target;
         if (a.lse) {
-          a.rows.lse[row] = a.lse[t];
-          a.rows.grad[row] = a.dloss[t];
+          const float ref = a.lse[t] * kLog2e;
+          a.rows.row[row] = {target, ref, fmaf(a.lse[t], kLog2e, -ref), a.dloss[t]};
+        } else {
+          a.rows.target[row] = target;
         }
       }
     }
-    __syncthreads();
-    for (int i = wave; i < kXentBlock && t0 + i < last; i += 4) {
-      const int to = row_of[i];
-      if (to < 0) continue;
-      const float* const x = a.X + (t0 + i) * a.ldx;
-      float* const y = a.rows.X + (int64_t)to * a.H;
-#pragma unroll 4
-      for (int64_t col = 4 * lane; col < a.H; col += 256)
-        store_upto(y + col, (int)min((int64_t)4, a.H - col),
-                   load_upto_once(x + col, (int)min((int64_t)4, a.H - col)));
+    const int to0 = __shfl(row, 2 * wave), to1 = __shfl(row, 2 * wave + 1);
+    const float* const x = a.X + (t0 + 2 * wave) * a.ldx;
+    constexpr int U = 4;   // groups of each row in flight
+    for (int64_t c0 = 4 * lane; c0 < a.H; c0 += U * 256) {
+      f32x4 v[2][U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t col = c0 + u * 256;
+        const int n = (int)min((int64_t)4, a.H - col);
+        if (n > 0 && to0 >= 0) v[0][u] = load_upto_once(x + col, n);
+        if (n > 0 && to1 >= 0) v[1][u] = load_upto_once(x + a.ldx + col, n);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t col = c0 + u * 256;
+        const int n = (int)min((int64_t)4, a.H - col);
+        if (n > 0 && to0 >= 0) store_upto(a.rows.X + (int64_t)to0 * a.H + col, n, v[0][u]);
+        if (n > 0 && to1 >= 0) store_upto(a.rows.X + (int64_t)to1 * a.H + col, n, v[1][u]);
+      }
     }
     before += __popcll(kept);
-    __syncthreads();   // row_of is read before it is written again
   }
   if (tid == 0 && last == a.T) {
     a.rows.offsets[0] = 0;
@@ -80,30 +87,26 @@ __global__ void __launch_bounds__(256) xent_gather_kernel(XentGatherArgs a) {
 }
 
 // The strips of kXentLossRows tokens' rows: part p of a token takes strips p,
-// p + kXentLossParts .., eight at a time, and the parts meet by halves.
+// p + kXentLossParts .., sixteen at a time, and the parts meet by halves.
 constexpr int kXentLossRows = 16, kXentLossParts = 64;
 
 __global__ void __launch_bounds__(kXentLossRows * kXentLossParts)
 xent_loss_kernel(XentLossArgs a) {
-  constexpr int U = 8;
+  constexpr int U = 16;
   __shared__ float all_m[kXentLossParts][kXentLossRows], all_s[kXentLossParts][kXentLossRows];
   const int i = (int)threadIdx.x % kXentLossRows, p = (int)threadIdx.x / kXentLossRows;
   const int64_t t = (int64_t)blockIdx.x * kXentLossRows + i;
   const bool kept = t < a.T && a.targets.of(t) >= 0;
   const int64_t row = !kept ? 0 : a.place ? a.place[t] : t;
-  float m = -FLT_MAX, s = 0.0f;
-  auto join = [&](float m2, float s2) {
-    const float top = fmaxf(m, m2);
-    s = s * exp_accurate(m - top) + s2 * exp_accurate(m2 - top);
-    m = top;
-  };
+  const float hit = kept && p == 0 ? a.hit[row] : 0.0f;
+  float m = -INFINITY, s = 0.0f;   // the sum relative to m's reference
   if (kept) {
     for (int j0 = p; j0 < a.strips; j0 += U * kXentLossParts) {
       float mm[U], ss[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int j = j0 + u * kXentLossParts;
-        mm[u] = -FLT_MAX;
+        mm[u] = -INFINITY;
         ss[u] = 0.0f;
         if (j < a.strips) {
           mm[u] = a.max[(int64_t)j * a.ld_strip + row];
@@ -113,9 +116,11 @@ xent_loss_kernel(XentLossArgs a) {
       float top = m;
 #pragma unroll
       for (int u = 0; u < U; ++u) top = fmaxf(top, mm[u]);
-      s *= exp_accurate(m - top);
+      const float ref = xent_reference(top);
+      s *= __builtin_amdgcn_exp2f(xent_reference(m) - ref);
 #pragma unroll
-      for (int u = 0; u < U; ++u) s += ss[u] * exp_accurate(mm[u] - top);
+      for (int u = 0; u < U; ++u)
+        s += ss[u] * __builtin_amdgcn_exp2f(xent_reference(mm[u]) - ref);
       m = top;
     }
   }
@@ -124,15 +129,21 @@ xent_loss_kernel(XentLossArgs a) {
   for (int half = kXentLossParts / 2; half > 0; half /= 2) {
     __syncthreads();
     if (p < half) {
-      join(all_m[p + half][i], all_s[p + half][i]);
+      const float m2 = all_m[p + half][i], s2 = all_s[p + half][i], top = fmaxf(m, m2);
+      const float ref = xent_reference(top);
+      s = s * __builtin_amdgcn_exp2f(xent_reference(m) - ref) +
+          s2 * __builtin_amdgcn_exp2f(xent_reference(m2) - ref);
+      m = top;
       all_m[p][i] = m;
       all_s[p][i] = s;
     }
   }
   if (p > 0 || t >= a.T) return;
-  const float rest = logf(s);
-  // Before m and log s are rounded together.
-  a.loss[t] = kept ? (m - a.hit[row]) + rest : 0.0f;
+  // log s, and what the rounding of m's reference moved s by.
+  m = fminf(fmaxf(m, -FLT_MAX), FLT_MAX);
+  const float rest = (log2f(s) - fmaf(m, kLog2e, -xent_reference(m))) * 0.693147182f;
+  // Before m and the rest are rounded together.
+  a.loss[t] = kept ? (m - hit) + rest : 0.0f;
   if (a.lse) a.lse[t] = kept ? m + rest : 0.0f;
 }
 

@@ -77,13 +77,9 @@ struct Room {
 XentRows take_rows(Room& room, int64_t T, int64_t H, bool backward) {
   XentRows r = {};
   r.offsets = room.take<int32_t>(2);
-  r.order = room.take<int32_t>(T);
   r.place = room.take<int32_t>(T);
-  r.target = room.take<int32_t>(T);
-  if (backward) {
-    r.lse = room.take<float>(T);
-    r.grad = room.take<float>(T);
-  }
+  if (backward) r.row = room.take<sg::XentRow>(T);
+  else r.target = room.take<int32_t>(T);
   r.X = room.take<float>(T * H);
   return r;
 }
@@ -178,8 +174,8 @@ int launch_gather(const Targets& targets, const XentRows& rows, int64_t T, int64
   a.ldx = ldx;
   a.T = T;
   a.H = (int)H;
-  // Up to 512 workgroups: each counts all the targets before its own.
-  a.chunk = (int)round_up(at_least_one(cdiv(T, 512)), sg::kXentBlock);
+  // Up to 2048 workgroups: each counts all the targets before its own.
+  a.chunk = (int)round_up(at_least_one(cdiv(T, 2048)), sg::kXentBlock);
   return launch(reinterpret_cast<const void*>(sg::xent_gather_kernel),
                 at_least_one(cdiv(T, a.chunk)), 256, &a, stream);
 }
@@ -270,7 +266,7 @@ int sgemm_linear_xent(int trans_b, int64_t T, int64_t V, int64_t H, const float*
                             ? product_args(T, V, H, f.rows.X, at_least_one(H), B, ldb, f.rows.offsets)
                             : product_args(T, V, H, X, ldx, B, ldb, nullptr);
     a.targets = t;
-    a.order = f.gathered ? f.rows.order : nullptr;
+    a.target = f.gathered ? f.rows.target : nullptr;
     a.max = f.max;
     a.sum = f.sum;
     a.hit = f.hit;
@@ -359,9 +355,7 @@ int sgemm_linear_xent_backward(int trans_b, int64_t T, int64_t V, int64_t H, con
       XentProductArgs a = product_args(T, n, H, r.X, H, Bp, ldb, r.offsets);
       a.C = b.dZ;
       a.ldc = (int)b.columns;
-      a.target = r.target;
-      a.lse = r.lse;
-      a.grad = r.grad;
+      a.row = r.row;
       a.column0 = (int)c0;
       st = launch_product(*v, a, true, stream);
     }

@@ -1,10 +1,20 @@
 // xent_args.hpp -- kernel arguments of the cross entropy over a product.
 #pragma once
 
+#include <float.h>
+
 #include "host.hpp"
 #include "product_args.hpp"
 
 namespace sg {
+
+constexpr float kLog2e = 1.44269502f;
+
+// What a row's powers of two are relative to, from its largest logit: finite, so that
+// a row of infinities subtracts no infinity from itself.
+__device__ __forceinline__ float xent_reference(float m) {
+  return fminf(fmaxf(m * kLog2e, -FLT_MAX), FLT_MAX);
+}
 
 // A token's target, or -1 where it has none.
 struct Targets {
@@ -19,30 +29,33 @@ struct Targets {
   }
 };
 
+// What the gradient needs of a row: one load (workspaces are aligned to 4 bytes).
+struct XentRow {
+  int target;
+  float ref, rest;   // lse times log2 e, rounded, and what that left
+  float grad;        // dloss
+};
+
 // The rows with a target, one after another ("kept" rows), made on the device.
-// Row r is token order[r]; token t is row place[t], or -1.
+// Token t is row place[t], or -1.
 struct XentRows {
   int32_t* offsets;   // 0 and how many: one group of kRowGroups
-  int32_t* order;
   int32_t* place;
-  int32_t* target;    // of each kept row
-  float* lse;         // backward: as given
-  float* grad;        // backward: dloss
+  int32_t* target;    // forward: of each kept row
+  XentRow* row;       // backward
   float* X;           // the rows, T x H
 };
 
 struct XentProductArgs : ProductArgs {
   // Forward.
   Targets targets;
-  const int32_t* order;   // null: row r is token r
+  const int32_t* target;  // of each row; null: row r is token r, see targets
   float* max;             // [strip][row]: a row's largest logit in a strip of columns
-  float* sum;             // and the sum of exp(logit - it)
+  float* sum;             // and the sum of exp(logit) over its exp, both as powers of two
   float* hit;             // [row]: the target's logit
   int ld_strip;           // rows
   // Backward.
-  const int32_t* target;
-  const float* lse;
-  const float* grad;
+  const XentRow* row;
   int column0;            // the first column's number in the vocabulary
 };
 
@@ -76,7 +89,7 @@ struct XentVariant {
   void (*grad)(XentProductArgs);
 };
 
-constexpr int kXentVariants = 6;
+constexpr int kXentVariants = 7;
 const XentVariant* xent_variants_ff();   // B is V x H
 const XentVariant* xent_variants_fs();   // B is H x V
 

@@ -185,6 +185,23 @@ def test_rows_without_a_target_reach_nothing(T):
 
 
 @pytest.mark.gpu
+def test_more_rows_than_one_workgroup_numbers_at_a_time():
+    """Rows with a target in every pattern: 200000 tokens, 1024 a workgroup."""
+    g = gen(55)
+    T, H, V = 200000, 8, 40
+    A, B, targets, _ = make(T, H, V, True, g, ignored=0.5)
+    targets[3000:9000] = -1
+    targets[20000:27000] = 3
+    lse, dloss = torch.empty(T, device="cuda"), torch.randn(T, device="cuda", generator=g)
+    loss = sg.linear_cross_entropy(A, B, targets, transpose_b=True, lse=lse)
+    check_loss(loss, lse, A, B, targets, True)
+    dA, dB = sg.linear_cross_entropy_backward(dloss, A, B, targets, lse, transpose_b=True)
+    wA, wB, tA, tB = grads64(dloss, A, B, targets, lse, True)
+    near(dA, wA, tA, "dA")
+    near(dB, wB, tB, "dB")
+
+
+@pytest.mark.gpu
 def test_empty_sizes():
     for tb in (False, True):
         A, B = torch.randn(5, 8, device="cuda"), torch.randn(8, 6, device="cuda")

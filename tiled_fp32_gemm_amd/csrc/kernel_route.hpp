@@ -283,13 +283,14 @@ __device__ __forceinline__ void refine(const RouteArgs& a, int64_t t, double* ro
   }
 }
 
-// What FP32 scores may be off, in half steps of 2^-24.  quick_exp(x) is within 2 + 2
-// |x| of its value (the product rounds, and so does log2 e).
-//   sigmoid  s (1 - s) (2 + 2 |x|) <= 0.95, and three more of s: 4
-//   softmax  d from the largest, s (2 + 2 d) <= 2.74 of the largest score; the sum
-//            of the exponentials (13 additions in a row, 2 + 2 d of each term,
-//            where the mean of d is at most ln 1024) 29, and its reciprocal 2, which
-//            all scores share but which moves them against the bias: 34
+// What FP32 scores may be off, in half steps of 2^-24.  quick_exp(x) is within 2 +
+// 1.3 |x| of its value (the product rounds, and so does log2 e).
+//   sigmoid  s (1 - s) (2 + 1.3 |x|) <= 0.8, and three more of s: 4
+//   softmax  d from the largest, which rounds too: s (2 + 2.3 d) <= 2.85 of the
+//            largest score; the sum of the exponentials (13 additions in a row, 2 +
+//            2.3 d of each term, where the mean of d is at most ln 1024) 31, and its
+//            reciprocal 2, which all scores share but which moves them against the
+//            bias: 36
 // Two such errors, rounded up; beside them the addition of the bias rounds once.
 constexpr float kHalfStep = 5.9604645e-8f;
 constexpr float kSoftmaxOff = 80.0f * kHalfStep, kSigmoidOff = 10.0f * kHalfStep;
@@ -318,17 +319,40 @@ __global__ void __launch_bounds__(256, K <= 8 ? 4 : 2) route_kernel(RouteArgs a)
   // The logits; -infinity: not to be chosen.
   float c[N];
   const int last = 4 * ((a.E - 1) / 4);   // where the last group of four begins
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int col = 4 * (g + i * G);
-    f32x4 v;
+  auto row_of = [&](const float* p, f32x4 (&v)[V]) {
     if (a.E % 4 == 0) {   // without a branch for each
-      v = *reinterpret_cast<const f32x4u*>(row + min(col, last));
-    } else {
-      v = load_upto(row + min(col, last), a.E - min(col, last));
-    }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) c[4 * i + e] = col + e < a.E ? v[e] : -INFINITY;
+      for (int i = 0; i < V; ++i)
+        v[i] = *reinterpret_cast<const f32x4u*>(p + min(4 * (g + i * G), last));
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int col = min(4 * (g + i * G), last);
+        v[i] = load_upto(p + col, a.E - col);
+      }
+    }
+  };
+  {
+    f32x4 v[V];
+    row_of(row, v);
+#pragma unroll
+    for (int i = 0; i < N; ++i) c[i] = v[i >> 2][i & 3];
+  }
+  if (a.E < N * G) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      c[i] = 4 * (g + (i >> 2) * G) + (i & 3) < a.E ? c[i] : -INFINITY;
+  }
+  float lowest = c[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) lowest = fminf(lowest, c[i]);
+  // Rarely any of the wave's: one bit each, so that the logits need not be kept.
+  const bool masked = __ballot(lowest == -INFINITY) != 0;
+  static_assert(N <= 32, "a bit for each of a lane's experts");
+  uint32_t never = 0u;
+  if (masked) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) never |= c[i] == -INFINITY ? 1u << i : 0u;
   }
   float top = -INFINITY, inv = 1.0f;   // of the whole softmax
   float off = kSigmoidOff;
@@ -341,7 +365,7 @@ __global__ void __launch_bounds__(256, K <= 8 ? 4 : 2) route_kernel(RouteArgs a)
     for (int i = 0; i < N; ++i) {
       const float p = quick_exp(c[i] - top);   // 0 for -infinity
       sum[i & 3] += p;
-      if (by_score) c[i] = c[i] == -INFINITY ? c[i] : p;
+      if (by_score) c[i] = p;
     }
     inv = 1.0f / group_sum<G>((sum[0] + sum[1]) + (sum[2] + sum[3]));
     off = kSoftmaxOff * inv;
@@ -350,28 +374,23 @@ __global__ void __launch_bounds__(256, K <= 8 ? 4 : 2) route_kernel(RouteArgs a)
   if (by_score) {
     f32x4 b[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int col = min(4 * (g + i * G), last);
-      b[i] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (a.bias) {
-        if (a.E % 4 == 0) b[i] = *reinterpret_cast<const f32x4u*>(a.bias + col);
-        else b[i] = load_upto(a.bias + col, a.E - col);
-      }
-    }
-    // A score and a bias are -0 together only, where the score is 0.
-    auto score_key = [&](int i, float s) {
-      s += b[i >> 2][i & 3];
-      uint32_t k = ordered_bits(fminf(s, INFINITY));
-      asm("" : "+v"(k));   // made for every lane, not in a branch of its own
-      key[i] = c[i] == -INFINITY ? kNever : k;
+    for (int i = 0; i < V; ++i) b[i] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (a.bias) row_of(a.bias, b);
+    // A score and a bias are -0 together only where the score is 0.
+    auto score_key = [&](float s, int i) {
+      return ordered_bits(fminf(s + b[i >> 2][i & 3], INFINITY));
     };
     if (whole) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) score_key(i, c[i] * inv);
+      for (int i = 0; i < N; ++i) key[i] = score_key(c[i] * inv, i);
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        score_key(i, __builtin_amdgcn_rcpf(1.0f + quick_exp(-c[i])));
+        key[i] = score_key(__builtin_amdgcn_rcpf(1.0f + quick_exp(-c[i])), i);
+    }
+    if (masked) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) key[i] = never >> i & 1 ? kNever : key[i];
     }
   } else {
 #pragma unroll
@@ -514,7 +533,7 @@ __global__ void __launch_bounds__(256, K <= 8 ? 4 : 2) route_kernel(RouteArgs a)
       const uint32_t k = packed_key(best[j]);
       if (j + 1 < K && j + 1 < a.top) {
         const uint32_t after = packed_key(best[j + 1 < K ? j + 1 : 0]);
-        unsure = unsure || (after > kNever && near(unordered(k), unordered(after)));
+        unsure |= (after > kNever) & near(unordered(k), unordered(after));
       }
       if (j == a.top - 1) chosen = k;
     }
@@ -526,7 +545,7 @@ __global__ void __launch_bounds__(256, K <= 8 ? 4 : 2) route_kernel(RouteArgs a)
 #pragma unroll
     for (int i = 0; i < N; ++i) close += key[i] >= from ? 1 : 0;
     close = group_sum<G>(close);
-    unsure = unsure || (chosen > kNever && close > a.top);
+    unsure |= (chosen > kNever) & (close > a.top);
     // A token's lanes agree on both.
     if (__ballot((unsure || regroup) && live) != 0) {
       constexpr int MOST = N * G < 64 ? N * G : 64;

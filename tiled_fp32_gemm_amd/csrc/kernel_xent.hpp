@@ -12,100 +12,87 @@
 // ends in XentGrad, which stores the piece's dz; two products of the library take
 // it on to dX and dB.
 //
-// Rows without a target are left out of the products altogether: xent_gather_kernel
-// copies the others' rows of X together, and how many there are stays on the
-// device.  A padded or masked row costs nothing and, whatever it holds, reaches no
+// Rows without a target are left out of the products altogether: xent_place_kernel
+// numbers the others, whose rows of X are copied together; how many there are stays
+// on the device.  A padded or masked row costs nothing and, whatever it holds, reaches no
 // gradient.
 #pragma once
 
 #include <float.h>
 
-#include "rows.hpp"
 #include "xent_args.hpp"
 
 namespace sg {
 
-// A workgroup takes a chunk of tokens, kXentBlock at a time: counts the rows with a
-// target before its chunk, numbers its own, and its waves copy their rows of X, two
-// each.
-constexpr int kXentBlock = 8;
+// Numbers the rows with a target.  A workgroup takes a chunk of tokens, a token a
+// thread at a time, after it has counted the rows of all the chunks before its own.
+constexpr int kXentPlaceThreads = 256;
 
-__global__ void __launch_bounds__(256) xent_gather_kernel(XentGatherArgs a) {
-  __shared__ int part[4];
+__global__ void __launch_bounds__(kXentPlaceThreads) xent_place_kernel(XentPlaceArgs a) {
+  constexpr int NT = kXentPlaceThreads, WAVES = NT / 64;
+  __shared__ int before[WAVES], own[2][WAVES];
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t first = (int64_t)blockIdx.x * a.chunk, last = min(first + a.chunk, a.T);
-  int before = 0;
-#pragma unroll 8
-  for (int64_t t = tid; t < first; t += 256) before += a.targets.of(t) >= 0 ? 1 : 0;
-  for (int d = 32; d > 0; d >>= 1) before += __shfl_xor(before, d);
-  if (lane == 0) part[wave] = before;
+  int n = 0;
+  auto count = [&](auto* ids) {
+#pragma unroll 16
+    for (int64_t i = tid; i < first; i += NT) n += ids[i] >= 0 && ids[i] < a.targets.V ? 1 : 0;
+  };
+  if (a.targets.wide) count(static_cast<const int64_t*>(a.targets.ids));
+  else count(static_cast<const int32_t*>(a.targets.ids));
+  for (int d = 32; d > 0; d >>= 1) n += __shfl_xor(n, d);
+  if (lane == 0) before[wave] = n;
   __syncthreads();
-  before = part[0] + part[1] + part[2] + part[3];
-  for (int64_t t0 = first; t0 < last; t0 += kXentBlock) {
-    // Every wave numbers the block's rows for itself.
-    const int64_t t = t0 + lane;
-    const int target = lane < kXentBlock && t < last ? a.targets.of(t) : -1;
+  int next = 0;   // the row after those so far
+  for (int w = 0; w < WAVES; ++w) next += before[w];
+  int odd = 0;    // a wave may still read the counts of the time before
+  for (int64_t t0 = first; t0 < last; t0 += NT, odd ^= 1) {
+    const int64_t t = t0 + tid;
+    const int target = t < last ? a.targets.of(t) : -1;
     const uint64_t kept = __ballot(target >= 0);
-    const int row = target >= 0 ? before + __popcll(kept & ((uint64_t(1) << lane) - 1)) : -1;
-    if (wave == 0 && lane < kXentBlock && t < last) {
-      a.rows.place[t] = row;
-      if (row >= 0) {
-        if (a.lse) {
-          const float ref = a.lse[t] * kLog2e;
-          a.rows.row[row] = {target, ref, fmaf(a.lse[t], kLog2e, -ref), a.dloss[t]};
-        } else {
-          a.rows.target[row] = target;
-        }
-      }
+    if (lane == 0) own[odd][wave] = __popcll(kept);
+    __syncthreads();
+    int row = next + __popcll(kept & ((uint64_t(1) << lane) - 1));
+    for (int w = 0; w < WAVES; ++w) {
+      if (w < wave) row += own[odd][w];
+      next += own[odd][w];
     }
-    const int to0 = __shfl(row, 2 * wave), to1 = __shfl(row, 2 * wave + 1);
-    const float* const x = a.X + (t0 + 2 * wave) * a.ldx;
-    constexpr int U = 4;   // groups of each row in flight
-    for (int64_t c0 = 4 * lane; c0 < a.H; c0 += U * 256) {
-      f32x4 v[2][U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t col = c0 + u * 256;
-        const int n = (int)min((int64_t)4, a.H - col);
-        if (n > 0 && to0 >= 0) v[0][u] = load_upto_once(x + col, n);
-        if (n > 0 && to1 >= 0) v[1][u] = load_upto_once(x + a.ldx + col, n);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t col = c0 + u * 256;
-        const int n = (int)min((int64_t)4, a.H - col);
-        if (n > 0 && to0 >= 0) store_upto(a.rows.X + (int64_t)to0 * a.H + col, n, v[0][u]);
-        if (n > 0 && to1 >= 0) store_upto(a.rows.X + (int64_t)to1 * a.H + col, n, v[1][u]);
-      }
+    if (t < last) a.rows.place[t] = target >= 0 ? row : -1;
+    if (target < 0) continue;
+    if (a.lse) {
+      const float lse = a.lse[t], ref = lse * kLog2e;
+      a.rows.row[row] = {target, ref, fmaf(lse, kLog2e, -ref), a.dloss[t]};
+    } else {
+      a.rows.target[row] = target;
     }
-    before += __popcll(kept);
   }
-  if (tid == 0 && last == a.T) {
+  if (last == a.T && tid == 0) {
     a.rows.offsets[0] = 0;
-    a.rows.offsets[1] = before;
+    a.rows.offsets[1] = next;
   }
 }
 
-// The strips of kXentLossRows tokens' rows: part p of a token takes strips p,
-// p + kXentLossParts .., sixteen at a time, and the parts meet by halves.
-constexpr int kXentLossRows = 16, kXentLossParts = 64;
+// The strips of ROWS tokens' rows: part p of a token takes strips p, p + PARTS ..,
+// sixteen at a time, and the parts meet by halves.  Many tokens: 32, which read whole
+// cache lines (8192 tokens of 512 strips: 18 us with 16).
+constexpr int kXentLossThreads = 1024;
 
-__global__ void __launch_bounds__(kXentLossRows * kXentLossParts)
-xent_loss_kernel(XentLossArgs a) {
-  constexpr int U = 16;
-  __shared__ float all_m[kXentLossParts][kXentLossRows], all_s[kXentLossParts][kXentLossRows];
-  const int i = (int)threadIdx.x % kXentLossRows, p = (int)threadIdx.x / kXentLossRows;
-  const int64_t t = (int64_t)blockIdx.x * kXentLossRows + i;
+template <int ROWS>
+__global__ void __launch_bounds__(kXentLossThreads) xent_loss_kernel(XentLossArgs a) {
+  constexpr int U = 16, PARTS = kXentLossThreads / ROWS;
+  __shared__ float all_m[PARTS][ROWS], all_s[PARTS][ROWS];
+  const int i = (int)threadIdx.x % ROWS, p = (int)threadIdx.x / ROWS;
+  const int64_t t = (int64_t)blockIdx.x * ROWS + i;
   const bool kept = t < a.T && a.targets.of(t) >= 0;
   const int64_t row = !kept ? 0 : a.place ? a.place[t] : t;
   const float hit = kept && p == 0 ? a.hit[row] : 0.0f;
   float m = -INFINITY, s = 0.0f;   // the sum relative to m's reference
   if (kept) {
-    for (int j0 = p; j0 < a.strips; j0 += U * kXentLossParts) {
+    for (int j0 = p; j0 < a.strips; j0 += U * PARTS) {
       float mm[U], ss[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int j = j0 + u * kXentLossParts;
+        const int j = j0 + u * PARTS;
         mm[u] = -INFINITY;
         ss[u] = 0.0f;
         if (j < a.strips) {
@@ -126,7 +113,7 @@ xent_loss_kernel(XentLossArgs a) {
   }
   all_m[p][i] = m;
   all_s[p][i] = s;
-  for (int half = kXentLossParts / 2; half > 0; half /= 2) {
+  for (int half = PARTS / 2; half > 0; half /= 2) {
     __syncthreads();
     if (p < half) {
       const float m2 = all_m[p + half][i], s2 = all_s[p + half][i], top = fmaxf(m, m2);

@@ -14,8 +14,8 @@ namespace {
 
 using namespace sg::host;
 using sg::Targets;
-using sg::XentGatherArgs;
 using sg::XentLossArgs;
+using sg::XentPlaceArgs;
 using sg::XentProductArgs;
 using sg::XentRows;
 using sg::XentVariant;
@@ -87,6 +87,8 @@ XentRows take_rows(Room& room, int64_t T, int64_t H, bool backward) {
 // Copying the rows together takes some 10 us and their traffic, a hundredth of a
 // product that takes this long, and saves the products of the rows left out.
 constexpr double kGatherSeconds = 200e-6;
+
+constexpr int64_t kLossRowsFrom = 1024;   // tokens
 
 struct Forward {
   const XentVariant* v;
@@ -162,22 +164,21 @@ int launch(const void* fn, int64_t wgs, int threads, void* args, hipStream_t str
              ? SGEMM_OK : SGEMM_ERR_LAUNCH;
 }
 
-int launch_gather(const Targets& targets, const XentRows& rows, int64_t T, int64_t H,
-                  const float* X, int64_t ldx, const float* lse, const float* dloss,
-                  hipStream_t stream) {
-  XentGatherArgs a = {};
+// The rows with a target numbered and copied together.
+int gather(const Targets& targets, const XentRows& rows, int64_t T, int64_t H, const float* X,
+           int64_t ldx, const float* lse, const float* dloss, hipStream_t stream) {
+  XentPlaceArgs a = {};
   a.targets = targets;
   a.rows = rows;
-  a.X = X;
   a.lse = lse;
   a.dloss = dloss;
-  a.ldx = ldx;
   a.T = T;
-  a.H = (int)H;
-  // Up to 2048 workgroups: each counts all the targets before its own.
-  a.chunk = (int)round_up(at_least_one(cdiv(T, 2048)), sg::kXentBlock);
-  return launch(reinterpret_cast<const void*>(sg::xent_gather_kernel),
-                at_least_one(cdiv(T, a.chunk)), 256, &a, stream);
+  // Up to 256 workgroups, as each reads all the targets before its own.
+  a.chunk = round_up(at_least_one(cdiv(T, 256)), sg::kXentPlaceThreads);
+  const int st = launch(reinterpret_cast<const void*>(sg::xent_place_kernel),
+                        at_least_one(cdiv(T, a.chunk)), sg::kXentPlaceThreads, &a, stream);
+  return st != SGEMM_OK ? st : sgemm_moe_permute(T, 1, H, X, ldx, rows.place, rows.X,
+                                                 at_least_one(H), stream);
 }
 
 // Tiles of columns column .. column + V - 1 of op(B).
@@ -248,7 +249,9 @@ int sgemm_linear_xent(int trans_b, int64_t T, int64_t V, int64_t H, const float*
     if (bad(s)) return SGEMM_ERR_INVALID_ARG;
   if (st != SGEMM_OK) return st;
   const Forward f = plan_forward(trans_b, T, V, H, workspace);
-  if (f.v == nullptr || !grid_fits(cdiv(T, sg::kXentLossRows), 1024)) return SGEMM_ERR_UNSUPPORTED;
+  const int rows = T >= kLossRowsFrom ? 32 : 16;   // a workgroup of xent_loss_kernel
+  if (f.v == nullptr || !grid_fits(cdiv(T, rows), sg::kXentLossThreads))
+    return SGEMM_ERR_UNSUPPORTED;
   const Span ws = {workspace, f.bytes};
   if (workspace_bytes < f.bytes || bad(ws)) return SGEMM_ERR_INVALID_ARG;
   for (const Span& s : in)
@@ -260,7 +263,7 @@ int sgemm_linear_xent(int trans_b, int64_t T, int64_t V, int64_t H, const float*
   ldb = leading(trans_b ? V : H, trans_b ? H : V, ldb);
   const Targets t = {targets, id_bytes == 8, (int)V};
   if (V > 0 && f.gathered)
-    st = launch_gather(t, f.rows, T, H, X, ldx, nullptr, nullptr, stream);
+    st = gather(t, f.rows, T, H, X, ldx, nullptr, nullptr, stream);
   if (V > 0 && st == SGEMM_OK) {
     XentProductArgs a = f.gathered
                             ? product_args(T, V, H, f.rows.X, at_least_one(H), B, ldb, f.rows.offsets)
@@ -285,8 +288,9 @@ int sgemm_linear_xent(int trans_b, int64_t T, int64_t V, int64_t H, const float*
   l.T = T;
   l.strips = f.strips;
   l.ld_strip = (int)T;
-  return launch(reinterpret_cast<const void*>(sg::xent_loss_kernel), cdiv(T, sg::kXentLossRows),
-                1024, &l, stream);
+  return launch(rows == 32 ? reinterpret_cast<const void*>(sg::xent_loss_kernel<32>)
+                           : reinterpret_cast<const void*>(sg::xent_loss_kernel<16>),
+                cdiv(T, rows), sg::kXentLossThreads, &l, stream);
 }
 
 int64_t sgemm_linear_xent_backward_workspace_bytes(int trans_b, int64_t T, int64_t V, int64_t H) {
@@ -345,7 +349,7 @@ int sgemm_linear_xent_backward(int trans_b, int64_t T, int64_t V, int64_t H, con
   if (dB) lddb = leading(br, bc, lddb);
   const Targets t = {targets, id_bytes == 8, (int)V};
   const XentRows& r = b.rows;
-  st = launch_gather(t, r, T, V > 0 ? H : 0, X, ldx, lse, dloss, stream);
+  st = gather(t, r, T, V > 0 ? H : 0, X, ldx, lse, dloss, stream);
   char* const split = static_cast<char*>(workspace) + b.bytes;
   const int64_t split_bytes = used - b.bytes;
   for (int64_t c0 = 0; c0 < V && st == SGEMM_OK; c0 += b.columns) {

@@ -59,14 +59,12 @@ struct XentProductArgs : ProductArgs {
   int column0;            // the first column's number in the vocabulary
 };
 
-struct XentGatherArgs {
+struct XentPlaceArgs {
   Targets targets;
   XentRows rows;
-  const float* X;
   const float* lse;      // null: forward
   const float* dloss;
-  int64_t ldx, T;
-  int H, chunk;          // tokens of a workgroup, a multiple of kXentBlock
+  int64_t T, chunk;      // tokens of a workgroup
 };
 
 struct XentLossArgs {

@@ -13,7 +13,7 @@
 // The choice is that of exact scores.  Without a bias, and without groups that
 // count two scores, it goes by the logits themselves, whose order is the scores'.
 // Otherwise FP32 scores decide unless two that matter are closer than their
-// errors (near() below), as for one token in about a thousand; then the wave
+// errors (kSoftmaxOff below), as for one token in about a thousand; then the wave
 // computes the scores again in FP64, those that may be chosen (reorder), or all
 // where the groups are open or there are too many (refine).
 #pragma once
@@ -396,10 +396,6 @@ __global__ void __launch_bounds__(256, K <= 8 ? 4 : 2) route_kernel(RouteArgs a)
 #pragma unroll
     for (int i = 0; i < N; ++i) key[i] = ordered(c[i]);
   }
-  // Whether two scores are too near each other to tell which is larger.
-  auto near = [&](float x, float y) {
-    return x - y <= off + 2.0f * kHalfStep * (fabsf(x) + fabsf(y));
-  };
   bool regroup = false, unsure = false;   // of the groups, of the experts
 
   if (a.groups > 1) {
@@ -522,25 +518,40 @@ __global__ void __launch_bounds__(256, K <= 8 ? 4 : 2) route_kernel(RouteArgs a)
     for (int j = 0; j < K; ++j) other[j] = exchanged<decltype(s)::value>(best[j]);
     merge_down(best, other);
   });
+  constexpr int J = (K + G - 1) / G;   // lane g has choices g, g + G ..
 #pragma unroll
-  for (int j = 0; j < K; ++j)
-    if (j % G == g && j < a.top) ids[sub][j] = packed_expert(best[j]);
+  for (int r = 0; r < J; ++r) {
+    double mine = best[r * G];
+#pragma unroll
+    for (int j = 1; j < G && r * G + j < K; ++j) mine = g == j ? best[r * G + j] : mine;
+    if (r * G + g < a.top) ids[sub][r * G + g] = packed_expert(mine);
+  }
 
   if (by_score) {
-    uint32_t chosen = 0u;   // the last one's key
+    // How far below a score another may be and yet be the larger one, for the largest
+    // of the list: both errors, and each one's rounding (a little more, as the lower
+    // one's size may exceed the other's by as much).
+    float far = 0.0f;
 #pragma unroll
     for (int j = 0; j < K; ++j) {
       const uint32_t k = packed_key(best[j]);
+      far = fmaxf(far, k > kNever ? fabsf(unordered(k)) : 0.0f);
+    }
+    const float reach = 1.01f * (off + 4.0f * kHalfStep * far);
+    uint32_t from = 0u, chosen = 0u;   // of the last one chosen
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      const uint32_t k = packed_key(best[j]), down_to = ordered(unordered(k) - reach);
       if (j + 1 < K && j + 1 < a.top) {
         const uint32_t after = packed_key(best[j + 1 < K ? j + 1 : 0]);
-        unsure |= (after > kNever) & near(unordered(k), unordered(after));
+        unsure |= (after > kNever) & (after >= down_to);
       }
-      if (j == a.top - 1) chosen = k;
+      if (j == a.top - 1) {
+        chosen = k;
+        from = down_to;
+      }
     }
-    // No other may be near the last one: from its score down to where near() ends
-    // (a little below, as |y| is |x| but for that).
-    const float x = unordered(chosen);
-    const uint32_t from = ordered(x - 1.01f * (off + 4.0f * kHalfStep * fabsf(x)));
+    // No other may be within reach of the last one.
     int close = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) close += key[i] >= from ? 1 : 0;
@@ -585,8 +596,7 @@ __global__ void __launch_bounds__(256, K <= 8 ? 4 : 2) route_kernel(RouteArgs a)
   }
   wave_lds_fence();
 
-  // Weights: lane g those of choices g, g + G ..
-  constexpr int J = (K + G - 1) / G;
+  // Weights.
   int id[J];
   float l[J], w[J], most = -INFINITY, total = 0.0f;
 #pragma unroll

@@ -135,6 +135,21 @@ def test_many_rows_of_which_some_count(T, H, V, tb):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,H,V", [(19, 2894, 3306), (3, 2647, 111), (300, 4096, 500),
+                                   (1, 1024, 32768), (8, 1030, 20001), (4, 1305, 142),
+                                   (14, 1330, 2235), (1000, 4096, 300), (2, 5000, 3)])
+@pytest.mark.parametrize("tb", [False, True])
+def test_few_tiles_over_a_long_k_and_few_rows(T, H, V, tb):
+    """The product is left in planes."""
+    run(T, H, V, tb, seed=T + V)
+    run(T, H, V, tb, pad=3, off=1, ignored=0.4, dtype=torch.int32, seed=T + V + 1)
+    # in pieces, where a smaller one may have no planes
+    least = sg.sgemm_linear_xent_backward_least_bytes(tb, T, V, H)
+    run(T, H, V, tb, ignored=0.3, ws=least)
+    run(T, H, V, tb, ignored=0.3, ws=least + 4 * T * 700)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,H,V", [(5, 30, 3000), (300, 64, 5000), (1500, 512, 2600)])
 @pytest.mark.parametrize("tb", [False, True])
 def test_a_vocabulary_in_pieces(T, H, V, tb):
@@ -151,10 +166,10 @@ def test_a_vocabulary_in_pieces(T, H, V, tb):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [40, 2048])
+@pytest.mark.parametrize("T", [20, 40, 2048])
 def test_rows_without_a_target_reach_nothing(T):
     """Whatever they hold; and targets of every kind that is none."""
-    H, V = 1024 if T > 1000 else 50, 8200
+    H, V = {2048: 1024, 40: 50, 20: 3000}[T], 8200 if T > 20 else 300
     g = gen(T)
     for tb in (False, True):
         for dtype in (torch.int32, torch.int64):
@@ -311,6 +326,7 @@ def test_gradients_against_differences(tb):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,H,V,tb", [(1, 64, 500, True), (200, 100, 3000, False),
+                                      (19, 2894, 3306, False), (4, 1024, 32768, True),
                                       (2048, 1024, 8192, True)])
 def test_replays_from_a_graph_with_other_targets(T, H, V, tb):
     g = gen(T + V)

@@ -12,6 +12,10 @@
 // ends in XentGrad, which stores the piece's dz; two products of the library take
 // it on to dX and dB.
 //
+// Where tiles of all of K are too few to fill the chip, or a few rows are faster
+// without tiles, the product is left in planes, one for each part of a split K, and a
+// pass over them (xent_planes_*) adds them up and does the same.
+//
 // Rows without a target are left out of the products altogether: xent_place_kernel
 // numbers the others, whose rows of X are copied together; how many there are stays
 // on the device.  A padded or masked row costs nothing and, whatever it holds, reaches no
@@ -20,6 +24,8 @@
 
 #include <float.h>
 
+#include "lanes.hpp"
+#include "rows.hpp"
 #include "xent_args.hpp"
 
 namespace sg {
@@ -70,6 +76,74 @@ __global__ void __launch_bounds__(kXentPlaceThreads) xent_place_kernel(XentPlace
     a.rows.offsets[0] = 0;
     a.rows.offsets[1] = next;
   }
+}
+
+// A wave takes 256 columns of a row of the planes, four a lane.
+constexpr int kXentPlanesCols = 1024;   // of a workgroup
+
+// Where this lane is: false, nowhere.  (A wave's lanes agree on the row.)
+__device__ __forceinline__ bool xent_planes_at(const XentPlanesArgs& a, int& row, int& col) {
+  const int blocks = (a.N + kXentPlanesCols - 1) / kXentPlanesCols;
+  row = (int)(blockIdx.x / (unsigned)blocks);
+  col = (int)(blockIdx.x % (unsigned)blocks) * kXentPlanesCols + 4 * (int)threadIdx.x;
+  return col < a.N;
+}
+__device__ __forceinline__ f32x4 xent_planes_sum(const XentPlanesArgs& a, int row, int col) {
+  constexpr int U = 8;   // planes in flight
+  const int left = a.N - col;
+  const int64_t plane = (int64_t)a.rows * a.N;
+  const float* const p = a.planes + (int64_t)row * a.N + col;
+  f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s0 = 0; s0 < a.count; s0 += U) {
+    f32x4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (s0 + u < a.count) v[u] = load_upto(p + (s0 + u) * plane, left);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (s0 + u < a.count) z += v[u];
+  }
+  return z;
+}
+
+__global__ void __launch_bounds__(256) xent_planes_stats_kernel(XentPlanesArgs a) {
+  int row, col;
+  const bool in = xent_planes_at(a, row, col);
+  const int target = a.targets.of(row);
+  if (target < 0 || __ballot(in) == 0) return;   // whole waves
+  f32x4 z = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  if (in) {
+    const f32x4 v = xent_planes_sum(a, row, col);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (col + e < a.N) z[e] = v[e];
+      if (col + e == target) a.hit[row] = v[e];   // a target is one of the columns
+    }
+  }
+  float m = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
+  for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+  const float ref = xent_reference(m);
+  float s = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) s += __builtin_amdgcn_exp2f(fmaf(z[e], kLog2e, -ref));
+  s = sum64(s);
+  if ((threadIdx.x & 63) != 0) return;
+  const int64_t at = (int64_t)(col / 256) * a.rows + row;
+  a.max[at] = m;
+  a.sum[at] = s;
+}
+
+__global__ void __launch_bounds__(256) xent_planes_grad_kernel(XentPlanesArgs a) {
+  int row, col;
+  if (!xent_planes_at(a, row, col) || row >= a.offsets[1]) return;
+  const XentRow info = a.row[row];
+  f32x4 z = xent_planes_sum(a, row, col);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float p = __builtin_amdgcn_exp2f(fmaf(z[e], kLog2e, -info.ref) - info.rest);
+    z[e] = (p - (info.target - a.column0 == col + e ? 1.0f : 0.0f)) * info.grad;
+  }
+  store_upto(a.dZ + (int64_t)row * a.N + col, a.N - col, z);
 }
 
 // The strips of ROWS tokens' rows: part p of a token takes strips p, p + PARTS ..,

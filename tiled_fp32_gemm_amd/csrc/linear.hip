@@ -11,6 +11,7 @@
 #include "host.hpp"
 #include "kernel_act_backward.hpp"
 #include "kernel_product_reduce.hpp"
+#include "product_planes.hpp"
 #include "product_variants.hpp"
 
 namespace {
@@ -467,7 +468,8 @@ Cut find_cut(const Product& p, const Step& whole, int64_t ws_bytes) {
   return best;
 }
 
-int launch_step(Product& p, const Step& s, hipStream_t stream, void* ws) {
+// `reduce`: a split's second launch too, which puts its planes in ws together in C.
+int launch_step(Product& p, const Step& s, hipStream_t stream, void* ws, bool reduce = true) {
   ProductArgs& g = p.g;
   void* args[] = {&g};
   const int tile_m = s.rows.rows > 0 ? s.rows.rows : s.tile.v->cost.tile_m;
@@ -488,7 +490,7 @@ int launch_step(Product& p, const Step& s, hipStream_t stream, void* ws) {
   hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(s.tile.v->fn),
                                  dim3((unsigned)s.tile.workgroups), dim3(s.tile.v->cost.threads),
                                  args, 0, stream);
-  if (e == hipSuccess && s.tile.splits > 1) {
+  if (e == hipSuccess && s.tile.splits > 1 && reduce) {
     const int64_t rows = (int64_t)g.M * (g.mode == sg::kSumGroups ? g.groups : 1);
     e = hipLaunchKernel(reinterpret_cast<const void*>(sg::product_reduce_kernel),
                         dim3((unsigned)(rows * cdiv(g.N, sg::kProductReduceCols))), dim3(64), args,
@@ -697,6 +699,43 @@ int act_backward(int64_t M, int64_t N, int64_t groups, const int32_t* offsets, b
 }
 
 }  // namespace
+
+// The internal products of product_planes.hpp.
+namespace sg {
+namespace host {
+
+static Step planes_step(const Product& p, int64_t room, PlanesPlan& plan) {
+  const Step s = decide(p, room);
+  plan.possible = possible(s);
+  plan.rows = s.rows.rows > 0 && p.g.M <= s.rows.rows;
+  plan.count = s.rows.rows > 0 ? 1 : s.tile.splits;
+  plan.seconds = plan.possible ? step_seconds(p, s) : 0.0;
+  return s;
+}
+
+PlanesPlan plan_planes(bool grouped, bool trans_b, int64_t M, int64_t N, int64_t K, int64_t room) {
+  PlanesPlan plan = {};
+  const Product p = shape_only(grouped ? kRowGroups : kDense, false, trans_b, M, N, K, 1, M);
+  if (p.launch) planes_step(p, room, plan);
+  return plan;
+}
+
+int launch_planes(bool trans_b, int64_t M, int64_t N, int64_t K, const float* A, int64_t lda,
+                  const float* B, int64_t ldb, const int32_t* offsets, float* planes,
+                  int64_t room, hipStream_t stream, int& count) {
+  Product p;
+  const int st = check_product(offsets ? kRowGroups : kDense, 0, trans_b, M, N, K, 1, offsets, M,
+                               A, lda, B, ldb, 0, planes, N, 0, nullptr, nullptr, 0, p);
+  if (st != SGEMM_OK || !p.launch) return st;
+  PlanesPlan plan;
+  const Step s = planes_step(p, room, plan);
+  if (!plan.possible) return SGEMM_ERR_UNSUPPORTED;
+  count = plan.count;
+  return launch_step(p, s, stream, planes, false);
+}
+
+}  // namespace host
+}  // namespace sg
 
 extern "C" {
 

@@ -88,7 +88,13 @@ int64_t norm_spans(int64_t M, int64_t N) {
   const Variant<NormBackwardFn>* v = variant_for(kBackward, N);
   const int64_t beside = v ? v->threads / v->lanes : 1;
   const int64_t all = cdiv(M, beside), least = cdiv(all, sg::kNormRun);
-  int64_t most = v ? kCUs * 4 * 256 / v->threads : cdiv(4 * kCUs, cdiv(N, sg::kNormWideCols));
+  // More of them fill the chip better, fewer leave less to write and to add up: by
+  // 64 lanes and more than 512 columns, or 256 lanes, two a CU (us, both kernels, with
+  // 256, 512 and 1024 of them: 8192 x 1024 26.5 / 23.4 / 27.3, 4096 x 4096 49.9 / 43.2 /
+  // 52.2, 1000 x 4096 20.6 / 21.4 / 29.3), of narrower rows four (60000 x 256 69 / 41 / 36,
+  // 200000 x 64 57 / 34 / 30), of wider ones one (3000 x 8192 62 / 71 / 87).
+  int64_t most = kCUs * (N <= 512 ? 4 : N <= 4096 ? 2 : 1);
+  if (!v) most = cdiv(4 * kCUs, cdiv(N, sg::kNormWideCols));
   if (most < least) most = least;
   return all < most ? all : most;
 }

@@ -9,6 +9,7 @@
 #include "../../include/sgemm_moe.h"
 #include "../../include/sgemm_xent.h"
 #include "kernel_xent.hpp"
+#include "product_planes.hpp"
 
 namespace {
 
@@ -16,6 +17,7 @@ using namespace sg::host;
 using sg::Targets;
 using sg::XentLossArgs;
 using sg::XentPlaceArgs;
+using sg::XentPlanesArgs;
 using sg::XentProductArgs;
 using sg::XentRows;
 using sg::XentVariant;
@@ -90,12 +92,39 @@ constexpr double kGatherSeconds = 200e-6;
 
 constexpr int64_t kLossRowsFrom = 1024;   // tokens
 
+// How many planes (product_planes.hpp) T x V over H is best left in; 0: rather tiles
+// that end in a row's statistics or gradient.  Planes win where K has to be split to
+// fill the chip, and where up to eight rows over a large B need no tiles.  Measured
+// (forward us, tiles / planes; T, H, V, B stored V x H or H x V):
+//      split        19, 2894, 3306 H x V 43 / 22, 3, 2647, 111 H x V 28 / 18,
+//                   300, 4096, 500 V x H 40 / 24, 1000, 4096, 300 V x H 41 / 34
+//      by rows      1, 1024, 32768 V x H 39 / 31, 8 rows 38 / 37, H x V 34 / 32,
+//                   1, 4096, 65536 V x H 213 / 174, 1, 512, 1000 V x H 12.6 / 14.9
+//      16 rows (B twice)  1024, 32768 V x H 38 / 43;  one plane by tiles  200, 1024,
+//                   2000 V x H 18 / 20
+constexpr int64_t kPlanesOne = int64_t(16) << 20, kPlanesAll = int64_t(64) << 20;   // bytes
+
+int choose_planes(const XentVariant* v, bool grouped, bool trans_b, int64_t T, int64_t V,
+                  int64_t H) {
+  const int64_t one = 4 * T * V;
+  if (v == nullptr || one == 0 || H == 0 || one > kPlanesOne) return 0;
+  const PlanesPlan plan = plan_planes(grouped, trans_b, T, V, H, kPlanesAll);
+  if (!plan.possible || (plan.count == 1 && !plan.rows)) return 0;
+  const int64_t tiles = cdiv(T, v->cost.tile_m) * cdiv(V, v->cost.tile_n);
+  const double b = 4.0 * V * H, by_tiles = estimate_grid(v->cost, tiles, H);
+  // A split's time has a second pass already; after rows it is a launch more.
+  if (plan.count > 1) return plan.seconds + 1e-6 < 0.95 * by_tiles ? plan.count : 0;
+  const double read = 4e-6 + b / 3.9e12, slow = by_tiles > read ? by_tiles : read;
+  return 9e-6 + b / 5.0e12 < 0.95 * slow ? 1 : 0;
+}
+
 struct Forward {
   const XentVariant* v;
   bool gathered;
   int strips;
+  int planes;   // 0: by tiles
   XentRows rows;
-  float *max, *sum, *hit;
+  float *z, *max, *sum, *hit;
   int64_t bytes;
 };
 
@@ -104,9 +133,11 @@ Forward plan_forward(bool trans_b, int64_t T, int64_t V, int64_t H, void* ws) {
   f.v = choose(trans_b, T, V, H);
   if (f.v == nullptr) return f;
   f.gathered = 2.0 * T * V * H / 150e12 > kGatherSeconds;
-  f.strips = (int)cdiv(V, f.v->strip);
+  f.planes = f.gathered ? 0 : choose_planes(f.v, false, trans_b, T, V, H);
+  f.strips = (int)cdiv(V, f.planes > 0 ? sg::kXentPlanesCols / 4 : f.v->strip);
   Room room = {static_cast<char*>(ws), 0};
   if (f.gathered) f.rows = take_rows(room, T, H, false);
+  if (f.planes > 0) f.z = room.take<float>(f.planes * T * V);
   f.max = room.take<float>(f.strips * T);
   f.sum = room.take<float>(f.strips * T);
   f.hit = room.take<float>(T);
@@ -127,6 +158,7 @@ struct Backward {
   XentRows rows;
   float* dX;       // of the kept rows
   float* dZ;       // T x columns
+  int planes;      // 0: by tiles; dZ is the first plane
   int64_t columns;
   int64_t fixed, bytes;   // without dZ; with it
   int64_t split;   // bytes the products take behind it for their fastest plans
@@ -150,7 +182,11 @@ Backward plan_backward(bool trans_b, int64_t T, int64_t V, int64_t H, void* ws, 
     if (pieces > 1) columns = round_up(cdiv(V, pieces), kPieceStep);
   }
   b.columns = columns;
-  b.dZ = room.take<float>(T * columns);
+  if (columns > 0 && T > 0) {
+    b.planes = choose_planes(choose(trans_b, T, columns, H), true, trans_b, T, columns, H);
+    if (bytes >= 0 && bytes - b.fixed < 4 * b.planes * T * columns) b.planes = 0;
+  }
+  b.dZ = room.take<float>((b.planes > 1 ? b.planes : 1) * T * columns);
   b.bytes = room.used;
   const int64_t x = sgemm_grouped_workspace_bytes(!trans_b, T, H, columns, 1);
   const int64_t w = sgemm_grouped_wgrad_workspace_bytes(trans_b, T, columns, H, 1);
@@ -264,7 +300,21 @@ int sgemm_linear_xent(int trans_b, int64_t T, int64_t V, int64_t H, const float*
   const Targets t = {targets, id_bytes == 8, (int)V};
   if (V > 0 && f.gathered)
     st = gather(t, f.rows, T, H, X, ldx, nullptr, nullptr, stream);
-  if (V > 0 && st == SGEMM_OK) {
+  if (V > 0 && st == SGEMM_OK && f.planes > 0) {
+    XentPlanesArgs a = {};
+    st = launch_planes(trans_b, T, V, H, X, ldx, B, ldb, nullptr, f.z, 4 * f.planes * T * V, stream,
+                       a.count);
+    a.planes = f.z;
+    a.targets = t;
+    a.max = f.max;
+    a.sum = f.sum;
+    a.hit = f.hit;
+    a.rows = (int)T;
+    a.N = (int)V;
+    if (st == SGEMM_OK)
+      st = launch(reinterpret_cast<const void*>(sg::xent_planes_stats_kernel),
+                  T * cdiv(V, sg::kXentPlanesCols), 256, &a, stream);
+  } else if (V > 0 && st == SGEMM_OK) {
     XentProductArgs a = f.gathered
                             ? product_args(T, V, H, f.rows.X, at_least_one(H), B, ldb, f.rows.offsets)
                             : product_args(T, V, H, X, ldx, B, ldb, nullptr);
@@ -355,16 +405,31 @@ int sgemm_linear_xent_backward(int trans_b, int64_t T, int64_t V, int64_t H, con
   for (int64_t c0 = 0; c0 < V && st == SGEMM_OK; c0 += b.columns) {
     const int64_t n = V - c0 < b.columns ? V - c0 : b.columns;
     const float* const Bp = B + (trans_b ? c0 * ldb : c0);
-    if (T > 0) {
+    const int64_t ldz = b.planes > 0 ? n : b.columns;
+    if (b.planes > 0) {
+      XentPlanesArgs a = {};
+      st = launch_planes(trans_b, T, n, H, r.X, H, Bp, ldb, r.offsets, b.dZ,
+                         4 * b.planes * T * b.columns, stream, a.count);
+      a.planes = b.dZ;
+      a.dZ = b.dZ;
+      a.offsets = r.offsets;
+      a.row = r.row;
+      a.rows = (int)T;
+      a.N = (int)n;
+      a.column0 = (int)c0;
+      if (st == SGEMM_OK)
+        st = launch(reinterpret_cast<const void*>(sg::xent_planes_grad_kernel),
+                    T * cdiv(n, sg::kXentPlanesCols), 256, &a, stream);
+    } else if (T > 0) {
       XentProductArgs a = product_args(T, n, H, r.X, H, Bp, ldb, r.offsets);
       a.C = b.dZ;
-      a.ldc = (int)b.columns;
+      a.ldc = (int)ldz;
       a.row = r.row;
       a.column0 = (int)c0;
       st = launch_product(*v, a, true, stream);
     }
     if (st == SGEMM_OK && dB)
-      st = sgemm_grouped_wgrad(trans_b, T, n, H, 1, r.offsets, r.X, H, b.dZ, b.columns,
+      st = sgemm_grouped_wgrad(trans_b, T, n, H, 1, r.offsets, r.X, H, b.dZ, ldz,
                                dB + (trans_b ? c0 * lddb : c0), lddb,
                                span_bytes(trans_b ? n : H, trans_b ? H : n, lddb) / 4, stream,
                                split, split_bytes);
@@ -373,7 +438,7 @@ int sgemm_linear_xent_backward(int trans_b, int64_t T, int64_t V, int64_t H, con
       sgemm_epilogue add = {};
       add.residual = c0 > 0 ? b.dX : nullptr;
       add.ldr = H;
-      st = sgemm_grouped(!trans_b, T, H, n, 1, r.offsets, b.dZ, b.columns, Bp, ldb,
+      st = sgemm_grouped(!trans_b, T, H, n, 1, r.offsets, b.dZ, ldz, Bp, ldb,
                          span_bytes(trans_b ? n : H, trans_b ? H : n, ldb) / 4, b.dX, H, &add,
                          stream, split, split_bytes);
     }

@@ -59,6 +59,19 @@ struct XentProductArgs : ProductArgs {
   int column0;            // the first column's number in the vocabulary
 };
 
+// Few rows: from a product's planes (product_planes.hpp).
+struct XentPlanesArgs {
+  const float* planes;    // [plane][rows][N]
+  float* dZ;              // backward: may be the first plane; leading dimension N
+  Targets targets;        // forward: row r is token r
+  float* max;             // [strip of 256 columns][row]
+  float* sum;
+  float* hit;
+  const int32_t* offsets;   // backward: how many rows
+  const XentRow* row;
+  int rows, N, count, column0;
+};
+
 struct XentPlaceArgs {
   Targets targets;
   XentRows rows;

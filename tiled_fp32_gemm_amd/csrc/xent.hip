@@ -146,6 +146,8 @@ Forward plan_forward(bool trans_b, int64_t T, int64_t V, int64_t H, void* ws) {
 }
 
 // Backward, dZ of a piece takes at most this much where that leaves 1024 columns.
+// Smaller ones cost more rounds of tiles and passes over dX (8192 tokens, H = 1024, V =
+// 32768, with 128 MiB, 512 MiB and 1 GiB: 11.38, 11.17, 11.12 ms).
 constexpr int64_t kPieceBytes = int64_t(512) << 20;
 constexpr int64_t kPieceStep = 256;   // columns, the widest tile
 
@@ -177,9 +179,12 @@ Backward plan_backward(bool trans_b, int64_t T, int64_t V, int64_t H, void* ws, 
     const int64_t most = piece_columns(T, V, bytes > b.fixed ? bytes - b.fixed : 0);
     if (most < columns) columns = most;
   }
-  if (columns > 0) {   // equal pieces
-    const int64_t pieces = cdiv(V, columns);
-    if (pieces > 1) columns = round_up(cdiv(V, pieces), kPieceStep);
+  // Equal pieces, of whole fours of tiles if they may be, which more often makes whole
+  // rounds of them (16384 tokens, H = 512, V = 20000: 7.7 -> 7.4 ms).
+  if (columns > 0 && columns < V) {
+    const int64_t equal = cdiv(V, cdiv(V, columns));
+    const int64_t four = round_up(equal, 4 * kPieceStep);
+    columns = four <= columns ? four : round_up(equal, kPieceStep);
   }
   b.columns = columns;
   if (columns > 0 && T > 0) {

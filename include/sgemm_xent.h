@@ -30,7 +30,7 @@
  * same from run to run (no atomics).  Leading dimensions of X and B, V and H are
  * limited to SGEMM_XENT_MAX_LD; more is SGEMM_ERR_UNSUPPORTED.  Infinite and NaN
  * logits follow the formulas: a row with one of +infinity has lse = +infinity, one
- * with a NaN has NaN.
+ * with a NaN has NaN.  Finite ones are taken to be below 2e38 in size.
  */
 #ifndef SGEMM_XENT_H
 #define SGEMM_XENT_H

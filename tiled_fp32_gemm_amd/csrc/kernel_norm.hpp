@@ -15,6 +15,10 @@
 // kNormRun rows: the rounding errors grow with n / 256 + 256 rather than n.
 //
 // Bound by HBM: 8 bytes an element forward, 12 backward (16 with a residual).
+// Measured on MI355X: 32768 x 4096 forward 192 to 200 us (5.4 TB/s), 16 x 1024 3.5; the
+// gradients of 32768 x 1024 with a residual 84 + 5 us (6.0 TB/s), of 1000 x 777 6.3 + 3.8.
+// The wide kernels read a row from the caches for their second and third step: 4000 x
+// 16384 backward 309 us, 2.5 TB/s of what has to move.
 #pragma once
 
 #include "lanes.hpp"

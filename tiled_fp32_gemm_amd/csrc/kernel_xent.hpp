@@ -20,6 +20,13 @@
 // numbers the others, whose rows of X are copied together; how many there are stays
 // on the device.  A padded or masked row costs nothing and, whatever it holds, reaches no
 // gradient.
+//
+// Bound by the matrix pipe for many rows, by reading B for a few.  Measured on MI355X
+// with B stored V x H, H = 1024, V = 32768: 6144 rows forward 2807 us (147 TFLOP/s;
+// the product alone would take 2745), numbering and copying them 6 + 12, joining 512
+// strips of 8192 tokens 12; the gradient of half that vocabulary for 8192 rows 1912 us,
+// 97 more than a product, of which dz's 512 MiB are most; 16 rows forward 34 us (4 TB/s)
+// and 4.6 for their 1024 strips.
 #pragma once
 
 #include <float.h>

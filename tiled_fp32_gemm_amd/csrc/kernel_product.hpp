@@ -454,6 +454,18 @@ product_kernel(typename FINISH::Args g) {
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
   const int nslab = (K + BK - 1) / BK;
+  // Slab t begins at this k.  With another finish the columns' tiles may each begin
+  // at a slab of their own and go round (whole slabs only): in step they read the same
+  // columns of all of B's rows, which with rows of 4 KiB lie on few memory channels.
+  // 16 rows over V x H = 32768 x 1024, 32 x 64 tiles: 39 -> 33 us, 50000 x 2048 94 -> 83.
+  int turn = 0;
+  if constexpr (!kLinear)
+    if (g.turn && K % BK == 0 && nslab > 0)
+      turn = __builtin_amdgcn_readfirstlane((n0 / BN) % nslab);
+  auto slab_k = [&](int t) {
+    if constexpr (kLinear) return t * BK;
+    return (t + turn < nslab ? t + turn : t + turn - nslab) * BK;
+  };
   const bool k_tail = (AFAST || BFAST) && K % BK != 0;
 
   // Zeroes this lane's own words at k >= K of slab t once they have landed
@@ -568,8 +580,8 @@ product_kernel(typename FINISH::Args g) {
     const int st = t % S, nst = (t + 1) % S;
     __amdgpu_buffer_rsrc_t qa = qz, qb = qz;
     if constexpr (kLoads) {
-      qa = rsrc_a((t + S) * BK);
-      qb = rsrc_b((t + S) * BK);
+      qa = rsrc_a(slab_k(t + S));
+      qb = rsrc_b(slab_k(t + S));
     }
     chunks(st);
     if constexpr (KS == 2) __builtin_amdgcn_sched_barrier(0);
@@ -595,10 +607,10 @@ product_kernel(typename FINISH::Args g) {
   if (nslab > 0) {
     // Slabs 0 .. S-2 go out at once; slab 0 is waited for (with those behind it
     // when there are fewer), published, and slab S-1 goes out.
-    issue(rsrc_a(0), rsrc_b(0), 0);
+    issue(rsrc_a(slab_k(0)), rsrc_b(slab_k(0)), 0);
 #pragma unroll
     for (int j = 1; j + 1 < S; ++j)
-      if (j < nslab) issue(rsrc_a(j * BK), rsrc_b(j * BK), j);
+      if (j < nslab) issue(rsrc_a(slab_k(j)), rsrc_b(slab_k(j)), j);
     if (nslab >= S - 1)
       __builtin_amdgcn_s_waitcnt(kWaitLoads<(S - 2) * Cfg::LOADS>);
     else
@@ -606,7 +618,7 @@ product_kernel(typename FINISH::Args g) {
     if (k_tail && nslab == 1) fix_tail(0, 0);
     __builtin_amdgcn_s_waitcnt(kWaitLds);
     asm volatile("s_barrier" ::: "memory");
-    if (nslab > S - 1) issue(rsrc_a((S - 1) * BK), rsrc_b((S - 1) * BK), S - 1);
+    if (nslab > S - 1) issue(rsrc_a(slab_k(S - 1)), rsrc_b(slab_k(S - 1)), S - 1);
     if (works) {
       read_chunk(fr[0], 0, 0);
       int t = 0;
@@ -631,7 +643,7 @@ product_kernel(typename FINISH::Args g) {
         if (k_tail && t + 2 == nslab) fix_tail(t + 1, (t + 1) % S);
         __builtin_amdgcn_s_waitcnt(kWaitLds);
         asm volatile("s_barrier" ::: "memory");
-        if (t + S < nslab) issue(rsrc_a((t + S) * BK), rsrc_b((t + S) * BK), t % S);
+        if (t + S < nslab) issue(rsrc_a(slab_k(t + S)), rsrc_b(slab_k(t + S)), t % S);
       }
     }
   }

@@ -17,7 +17,7 @@
 // computes the scores again in FP64, those that may be chosen (reorder), or all
 // where the groups are open or there are too many (refine).
 //
-// Bound by vector instructions, about 1550 a wave for eight tokens' best 8 of 256 in
+// Bound by vector instructions, about 1610 a wave for eight tokens' best 8 of 256 in
 // groups by sigmoid and bias, where the copies of 32768 such rows would take 7.3 us:
 // measured on MI355X 18.7 us, of which the last waves' FP64 takes 2.5; without bias and
 // groups 10.8, 8191 tokens of 64 experts 3.9.  Sixteen lanes a token instead of eight

@@ -25,8 +25,8 @@
 // with B stored V x H, H = 1024, V = 32768: 6144 rows forward 2807 us (147 TFLOP/s;
 // the product alone would take 2745), numbering and copying them 6 + 12, joining 512
 // strips of 8192 tokens 12; the gradient of half that vocabulary for 8192 rows 1912 us,
-// 97 more than a product, of which dz's 512 MiB are most; 16 rows forward 34 us (4 TB/s)
-// and 4.6 for their 1024 strips.
+// 97 more than a product, of which dz's 512 MiB are most; 16 rows forward 28 us (4.8
+// TB/s) and 4.6 for their 1024 strips.
 #pragma once
 
 #include <float.h>

@@ -229,6 +229,7 @@ int launch_product(const XentVariant& v, XentProductArgs& a, bool grad, hipStrea
   a.tiles_n = (int)cdiv(a.N, c.tile_n);
   a.group_m = a.tiles_m < 8 ? a.tiles_m : 8;
   a.splits = 1;
+  a.turn = a.tiles_m == 1;   // bound by reading B (two rows of tiles: no difference)
   return launch(reinterpret_cast<const void*>(grad ? v.grad : v.stats),
                 (int64_t)a.tiles_m * a.tiles_n, c.threads, &a, stream);
 }

@@ -54,6 +54,7 @@ struct XentProductArgs : ProductArgs {
   float* sum;             // and the sum of exp(logit) over its exp, both as powers of two
   float* hit;             // [row]: the target's logit
   int ld_strip;           // rows
+  int turn;               // tiles begin at slabs of their own
   // Backward.
   const XentRow* row;
   int column0;            // the first column's number in the vocabulary

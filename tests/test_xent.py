@@ -165,6 +165,65 @@ def test_a_vocabulary_in_pieces(T, H, V, tb):
         assert torch.equal(x, y)
 
 
+FEW = [(1, 255, 1000), (2, 256, 4099), (3, 257, 513), (5, 1025, 2047), (6, 130, 1024),
+       (8, 512, 1025), (8, 2049, 129), (7, 1, 3000), (4, 3000, 1), (8, 4, 70000), (1, 1030, 33000),
+       (3, 5000, 700), (9, 300, 900)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,V", FEW)
+@pytest.mark.parametrize("tb", [False, True])
+def test_a_few_rows(T, H, V, tb):
+    """Both gradients from one reading of B, and in pieces where there is no room for
+    that; either alone; rows without a target in every place, whatever they hold."""
+    run(T, H, V, tb, seed=H)
+    run(T, H, V, tb, pad=5, off=3, ignored=0.5, dtype=torch.int32, seed=V)
+    least = sg.sgemm_linear_xent_backward_least_bytes(tb, T, V, H)
+    most = sg.sgemm_linear_xent_backward_workspace_bytes(tb, T, V, H)
+    assert least <= most
+    run(T, H, V, tb, ignored=0.3, ws=least, seed=T)
+    g = gen(T * V)
+    A, B, targets, _ = make(T, H, V, tb, g, pad=1, off=1)
+    dloss, lse = torch.randn(T, device="cuda", generator=g), torch.empty(T, device="cuda")
+    ws = torch.empty(most // 4, device="cuda")
+    sg.linear_cross_entropy(A, B, targets, transpose_b=tb, lse=lse)
+    for none in [()] + [(t,) for t in range(T)] + [tuple(range(T))]:
+        t2, A2, d2, l2 = targets.clone(), A.clone(), dloss.clone(), lse.clone()
+        for t in none:
+            t2[t], A2[t], d2[t], l2[t] = V + t, float("nan"), float("inf"), float("nan")
+        ws.fill_(float("nan"))
+        dA, dB = sg.linear_cross_entropy_backward(d2, A2, B, t2, l2, transpose_b=tb, workspace=ws)
+        wA, wB, tA, tB = grads64(d2, A2, B, t2, l2, tb, max(64, V // 256 + 1))
+        near(dA, wA, tA, "dA")
+        near(dB, wB, tB, "dB")
+        for a, b in ((True, False), (False, True)):
+            got = sg.linear_cross_entropy_backward(d2, A2, B, t2, l2, transpose_b=tb, a_grad=a,
+                                                   b_grad=b, workspace=ws)
+            assert torch.equal(got[1 - a], (dA, dB)[1 - a]) and got[a] is None
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,V", [(5, 70, 900), (8, 300, 2000), (100, 70, 900)])
+@pytest.mark.parametrize("tb", [False, True])
+def test_gradients_into_wider_rows(T, H, V, tb):
+    """Leading dimensions of the outputs: what lies between and behind their rows stays."""
+    g = gen(H)
+    A, B, targets, _ = make(T, H, V, tb, g, pad=2, ignored=0.3)
+    dloss, lse = torch.randn(T, device="cuda", generator=g), torch.empty(T, device="cuda")
+    sg.linear_cross_entropy(A, B, targets, transpose_b=tb, lse=lse)
+    want = sg.linear_cross_entropy_backward(dloss, A, B, targets, lse, transpose_b=tb)
+    outs = [torch.full((w.shape[0] + 1, w.shape[1] + 3), 7.0, device="cuda") for w in want]
+    ws = torch.empty(sg.sgemm_linear_xent_backward_workspace_bytes(tb, T, V, H), device="cuda",
+                     dtype=torch.uint8)
+    st = sg.sgemm_linear_xent_backward(
+        tb, T, V, H, A.data_ptr(), A.stride(0), B.data_ptr(), B.stride(0), targets.data_ptr(), 8,
+        lse.data_ptr(), dloss.data_ptr(), outs[0].data_ptr(), H + 3, outs[1].data_ptr(),
+        outs[1].shape[1], torch.cuda.current_stream().cuda_stream, ws.data_ptr(), ws.numel())
+    assert st == sg.OK
+    for o, w in zip(outs, want):
+        assert torch.equal(o[:-1, :-3], w) and (o[:, -3:] == 7).all() and (o[-1] == 7).all()
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("T", [20, 40, 2048])
 def test_rows_without_a_target_reach_nothing(T):

@@ -73,8 +73,7 @@ __global__ void __launch_bounds__(kXentPlaceThreads) xent_place_kernel(XentPlace
     if (t < last) a.rows.place[t] = target >= 0 ? row : -1;
     if (target < 0) continue;
     if (a.lse) {
-      const float lse = a.lse[t], ref = lse * kLog2e;
-      a.rows.row[row] = {target, ref, fmaf(lse, kLog2e, -ref), a.dloss[t]};
+      a.rows.row[row] = xent_row(target, a.lse[t], a.dloss[t]);
     } else {
       a.rows.target[row] = target;
     }
@@ -142,8 +141,16 @@ __global__ void __launch_bounds__(256) xent_planes_stats_kernel(XentPlanesArgs a
 
 __global__ void __launch_bounds__(256) xent_planes_grad_kernel(XentPlanesArgs a) {
   int row, col;
-  if (!xent_planes_at(a, row, col) || row >= a.offsets[1]) return;
-  const XentRow info = a.row[row];
+  if (!xent_planes_at(a, row, col)) return;
+  XentRow info;
+  if (a.row) {
+    if (row >= a.offsets[1]) return;
+    info = a.row[row];
+  } else {
+    const int target = a.targets.of(row);
+    if (target < 0) return;
+    info = xent_row(target, a.lse[row], a.dloss[row]);
+  }
   f32x4 z = xent_planes_sum(a, row, col);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {

@@ -9,12 +9,15 @@
 #include "../../include/sgemm_moe.h"
 #include "../../include/sgemm_xent.h"
 #include "kernel_xent.hpp"
+#include "kernel_xent_few.hpp"
 #include "product_planes.hpp"
 
 namespace {
 
 using namespace sg::host;
 using sg::Targets;
+using sg::XentFewArgs;
+using sg::XentFewSumArgs;
 using sg::XentLossArgs;
 using sg::XentPlaceArgs;
 using sg::XentPlanesArgs;
@@ -156,6 +159,61 @@ int64_t piece_columns(int64_t T, int64_t V, int64_t bytes) {
   return n >= V ? V : n / kPieceStep * kPieceStep;
 }
 
+// Up to eight rows: the logits in planes, their gradient, and both gradients in one
+// reading of B (kernel_xent_few.hpp).  Sixteen would leave a wave a SIMD (16, 1024, 32768
+// V x H 140 us where the rows' copies, three products and dX's scatter take 135).
+constexpr int64_t kFewRows = 8;
+
+// A launch over B as it is stored, rows x cols.
+struct FewGrid {
+  int part, blocks, parts;
+};
+
+// Down: as many workgroups as their registers let reside, in one round (T = 8, H = 3271, V
+// = 7145 V x H: 40 us, two rounds 44 and more planes to add up).  Across: 2048, so that
+// they end together (8, 1024, 32768: 48; 1024 workgroups 54, 768 50).
+FewGrid few_grid(bool down, bool grad, int64_t T, int64_t rows, int64_t cols) {
+  const int64_t groups = !down ? 2048
+                         : grad ? (T <= 1 ? 1280 : T <= 2 ? 1024 : T <= 4 ? 768 : 512)
+                                : (T <= 4 ? 1280 : 768);
+  const int64_t blocks = cdiv(cols, down ? 256 : 1024);
+  int64_t part = round_up(cdiv(rows, at_least_one(groups / blocks)), down ? 32 : 8);
+  if (!down && part > sg::kXentFewAcross) part = sg::kXentFewAcross;
+  return {(int)part, (int)blocks, (int)cdiv(rows, part)};
+}
+
+struct Few {
+  bool possible;
+  FewGrid z, grad;   // z: B stored H x V
+  int count;         // planes of dX
+  int z_count;       // and of the logits
+  float *z_planes, *planes;
+  int64_t bytes;
+};
+
+Few plan_few(bool trans_b, int64_t T, int64_t V, int64_t H, void* ws) {
+  Few f = {};
+  if (T == 0 || T > kFewRows || V == 0 || H == 0 || 4 * T * V > kPlanesOne) return f;
+  const int64_t rows = trans_b ? V : H, cols = trans_b ? H : V;
+  f.grad = few_grid(trans_b, true, T, rows, cols);
+  f.count = trans_b ? f.grad.parts : f.grad.blocks;
+  if (trans_b) {
+    const PlanesPlan z = plan_planes(false, true, T, V, H, kPlanesAll);
+    if (!z.possible) return f;
+    f.z_count = z.count;
+  } else {
+    f.z = few_grid(true, false, T, rows, cols);
+    f.z_count = f.z.parts;
+  }
+  if (!grid_fits((int64_t)f.grad.blocks * f.grad.parts, sg::kXentFewThreads)) return f;
+  Room room = {static_cast<char*>(ws), 0};
+  f.z_planes = room.take<float>(f.z_count * T * V);
+  f.planes = room.take<float>(f.count * T * H);
+  f.bytes = room.used;
+  f.possible = true;
+  return f;
+}
+
 struct Backward {
   XentRows rows;
   float* dX;       // of the kept rows
@@ -251,6 +309,25 @@ XentProductArgs product_args(int64_t T, int64_t V, int64_t H, const float* X, in
   a.rows = (int)T;
   a.offsets = offsets;
   return a;
+}
+
+// A kernel of the least rows that hold T.
+enum class FewKernel { kLogits, kDown, kAcross };
+
+template <int R>
+const void* few_kernel(FewKernel which, int64_t T) {
+  if constexpr (R < kFewRows)
+    if (T > R) return few_kernel<2 * R>(which, T);
+  return which == FewKernel::kLogits ? reinterpret_cast<const void*>(sg::xent_few_down_kernel<R, false>)
+         : which == FewKernel::kDown ? reinterpret_cast<const void*>(sg::xent_few_down_kernel<R, true>)
+                                     : reinterpret_cast<const void*>(sg::xent_few_across_kernel<R>);
+}
+
+int launch_few(FewKernel which, const FewGrid& grid, XentFewArgs& a, hipStream_t stream) {
+  a.part = grid.part;
+  a.blocks = grid.blocks;
+  return launch(few_kernel<1>(which, a.T), (int64_t)grid.blocks * grid.parts, sg::kXentFewThreads,
+                &a, stream);
 }
 
 // Checks of both calls: sizes, leading dimensions, targets.
@@ -352,7 +429,10 @@ int sgemm_linear_xent(int trans_b, int64_t T, int64_t V, int64_t H, const float*
 int64_t sgemm_linear_xent_backward_workspace_bytes(int trans_b, int64_t T, int64_t V, int64_t H) {
   if ((trans_b & ~1) || !sizes_ok(T, V, H)) return 0;
   const Backward b = plan_backward(trans_b, T, V, H, nullptr, -1);
-  return b.bytes + b.split;
+  const Few f = plan_few(trans_b, T, V, H, nullptr);
+  if (!f.possible) return b.bytes + b.split;
+  const int64_t least = sgemm_linear_xent_backward_least_bytes(trans_b, T, V, H);
+  return f.bytes > least ? f.bytes : least;
 }
 
 int64_t sgemm_linear_xent_backward_least_bytes(int trans_b, int64_t T, int64_t V, int64_t H) {
@@ -388,7 +468,9 @@ int sgemm_linear_xent_backward(int trans_b, int64_t T, int64_t V, int64_t H, con
   const Backward b = plan_backward(trans_b, T, V, H, workspace, workspace_bytes);
   if (V > 0 && (b.columns == 0 || workspace_bytes < b.bytes)) return SGEMM_ERR_INVALID_ARG;
   if (workspace_bytes < b.fixed) return SGEMM_ERR_INVALID_ARG;
-  int64_t used = b.bytes + b.split;
+  const Few f = plan_few(trans_b, T, V, H, workspace);
+  const bool few = f.possible && f.bytes <= workspace_bytes;
+  int64_t used = few ? f.bytes : b.bytes + b.split;
   if (used > workspace_bytes) used = workspace_bytes;
   const Span ws = {workspace, used};
   if (bad(ws)) return SGEMM_ERR_INVALID_ARG;
@@ -404,6 +486,49 @@ int sgemm_linear_xent_backward(int trans_b, int64_t T, int64_t V, int64_t H, con
   ldb = leading(br, bc, ldb);
   if (dB) lddb = leading(br, bc, lddb);
   const Targets t = {targets, id_bytes == 8, (int)V};
+  if (few) {
+    XentFewArgs a = {};
+    a.targets = t;
+    a.B = B;
+    a.T = (int)T;
+    a.rows = (int)br;
+    a.cols = (int)bc;
+    a.ldb = (int)ldb;
+    XentPlanesArgs p = {};
+    if (trans_b) {
+      st = launch_planes(true, T, V, H, X, ldx, B, ldb, nullptr, f.z_planes, kPlanesAll, stream,
+                         p.count);
+    } else {
+      p.count = f.z_count;
+      a.P = X;
+      a.ldp = (int)ldx;
+      a.planes = f.z_planes;
+      st = launch_few(FewKernel::kLogits, f.z, a, stream);
+    }
+    if (st != SGEMM_OK) return st;
+    p.planes = f.z_planes;
+    p.dZ = f.z_planes;
+    p.targets = t;
+    p.lse = lse;
+    p.dloss = dloss;
+    p.rows = (int)T;
+    p.N = (int)V;
+    st = launch(reinterpret_cast<const void*>(sg::xent_planes_grad_kernel),
+                T * cdiv(V, sg::kXentPlanesCols), 256, &p, stream);
+    if (st != SGEMM_OK) return st;
+    a.P = trans_b ? f.z_planes : X;
+    a.ldp = (int)(trans_b ? V : ldx);
+    a.Q = trans_b ? X : f.z_planes;
+    a.ldq = (int)(trans_b ? ldx : V);
+    a.D = dB;
+    a.ldd = dB ? (int)lddb : 0;
+    a.planes = dX ? f.planes : nullptr;
+    st = launch_few(trans_b ? FewKernel::kDown : FewKernel::kAcross, f.grad, a, stream);
+    if (st != SGEMM_OK || !dX) return st;
+    XentFewSumArgs sum = {t, f.planes, dX, leading(T, H, lddx), (int)T, (int)H, f.count};
+    return launch(reinterpret_cast<const void*>(sg::xent_few_sum_kernel),
+                  T * cdiv(H, sg::kXentFewSumCols), sg::kXentFewThreads, &sum, stream);
+  }
   const XentRows& r = b.rows;
   st = gather(t, r, T, V > 0 ? H : 0, X, ldx, lse, dloss, stream);
   char* const split = static_cast<char*>(workspace) + b.bytes;

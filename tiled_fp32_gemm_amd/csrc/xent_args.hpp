@@ -35,6 +35,10 @@ struct XentRow {
   float ref, rest;   // lse times log2 e, rounded, and what that left
   float grad;        // dloss
 };
+__device__ __forceinline__ XentRow xent_row(int target, float lse, float dloss) {
+  const float ref = lse * kLog2e;
+  return {target, ref, fmaf(lse, kLog2e, -ref), dloss};
+}
 
 // The rows with a target, one after another ("kept" rows), made on the device.
 // Token t is row place[t], or -1.
@@ -69,8 +73,32 @@ struct XentPlanesArgs {
   float* sum;
   float* hit;
   const int32_t* offsets;   // backward: how many rows
-  const XentRow* row;
+  const XentRow* row;       // null: row r is token r, see targets and
+  const float* lse;
+  const float* dloss;
   int rows, N, count, column0;
+};
+
+// Up to eight rows (kernel_xent_few.hpp).  In rows without a target P and Q do not
+// count, whatever they hold.
+struct XentFewArgs {
+  Targets targets;
+  const float* B;         // as it is stored, rows x cols
+  const float* P;         // T x rows
+  const float* Q;         // T x cols
+  float* D;               // rows x cols: P'Q; null: not wanted
+  float* planes;          // parts of P·B or Q·B', T x cols or rows; null: not wanted
+  int T, rows, cols, ldb, ldp, ldq, ldd;
+  int part;               // rows of B of a workgroup
+  int blocks;             // workgroups that take the same rows
+};
+
+struct XentFewSumArgs {
+  Targets targets;
+  const float* planes;    // [plane][T][H]
+  float* dX;              // 0 in rows without a target
+  int64_t lddx;
+  int T, H, count;
 };
 
 struct XentPlaceArgs {

@@ -167,7 +167,8 @@ def test_a_vocabulary_in_pieces(T, H, V, tb):
 
 FEW = [(1, 255, 1000), (2, 256, 4099), (3, 257, 513), (5, 1025, 2047), (6, 130, 1024),
        (8, 512, 1025), (8, 2049, 129), (7, 1, 3000), (4, 3000, 1), (8, 4, 70000), (1, 1030, 33000),
-       (3, 5000, 700), (9, 300, 900)]
+       (3, 5000, 700), (9, 300, 900), (16, 333, 2049), (13, 1024, 511), (16, 2, 5),
+       (17, 90, 1030)]
 
 
 @pytest.mark.gpu
@@ -200,6 +201,14 @@ def test_a_few_rows(T, H, V, tb):
             got = sg.linear_cross_entropy_backward(d2, A2, B, t2, l2, transpose_b=tb, a_grad=a,
                                                    b_grad=b, workspace=ws)
             assert torch.equal(got[1 - a], (dA, dB)[1 - a]) and got[a] is None
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 8])
+def test_a_few_rows_over_a_large_weight(T):
+    """B past the caches whose rows begin at any 4 bytes."""
+    run(T, 1100, 70001, False, seed=T)
+    run(T, 1100, 70001, False, pad=2, off=1, ignored=0.4, seed=T + 1)
 
 
 @pytest.mark.gpu

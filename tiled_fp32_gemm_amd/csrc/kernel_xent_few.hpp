@@ -1,5 +1,5 @@
 // kernel_xent_few.hpp -- both gradients of the cross entropy over a product for up to
-// eight rows.
+// eight rows, or sixteen where B is H x V.
 //
 //   dB = sum over tokens of x by dz        dX = dz·op(B)'
 //
@@ -22,6 +22,10 @@
 //           32768  29.7 (4.5) and 2, 2871, 34831  73.5 (5.4), where products by rows or
 //           tiles took 87 to 180
 //   across  8, 1024, 32768  47.8 (5.6), 2, 2871, 34831  163 (4.9)
+//   All of the gradients, against the rows' copies, three products and dX's scatter:
+//   across, sixteen rows 1024, 32768  91 for 114, 4096, 32768  361 for 378, 9, 1030, 20001
+//   60 for 96; down for sixteen keeps two times 64 sums and factors in a lane, which spill
+//   (16, 1024, 32768  185 for 113), and is left out
 //   Columns four together in a lane (16-byte accesses at any alignment) down: 3271 59.5,
 //   1030 87.  dB past the caches down: 49 and 76, as the ends of unaligned rows' pieces
 //   are then written in parts; across, where a workgroup's piece is 4 KB, in them: 149 for
@@ -35,7 +39,7 @@
 namespace sg {
 
 constexpr int kXentFewThreads = 256;
-constexpr int kXentFewAcross = 128;   // most rows of B of a workgroup across
+constexpr int kXentFewAcross = 64;   // most rows of B of a workgroup across
 
 // A lane's four columns of a block of 256: from `first` on, 64 apart, and never past the
 // last, which is repeated there (its sums are dropped), as loads that some lanes leave out
@@ -149,7 +153,7 @@ __global__ void __launch_bounds__(kXentFewThreads) xent_few_down_kernel(XentFewA
 }
 
 template <int R>
-__global__ void __launch_bounds__(kXentFewThreads, 4) xent_few_across_kernel(XentFewArgs a) {
+__global__ void __launch_bounds__(kXentFewThreads, R <= 8 ? 4 : 2) xent_few_across_kernel(XentFewArgs a) {
   constexpr int U = R <= 4 ? 8 : 4;    // rows of B in flight
   constexpr int S = U * R;                   // sums over the lanes at once
   constexpr int ROWS = kXentFewAcross;

@@ -121,11 +121,44 @@ int choose_planes(const XentVariant* v, bool grouped, bool trans_b, int64_t T, i
   return 9e-6 + b / 5.0e12 < 0.95 * slow ? 1 : 0;
 }
 
+// A few rows: the logits in planes, their gradient, and both gradients in one reading of
+// B (kernel_xent_few.hpp).
+constexpr int64_t kFewDown = 8, kFewAcross = 16;
+
+// A launch over B as it is stored, rows x cols.
+struct FewGrid {
+  int part, blocks, parts;
+};
+
+// Down: as many workgroups as their registers let reside, in one round (T = 8, H = 3271, V
+// = 7145 V x H: 40 us, two rounds 44 and more planes to add up).  Across: 2048, so that
+// they end together (8, 1024, 32768: 48; 1024 workgroups 54, 768 50).
+FewGrid few_grid(bool down, bool grad, int64_t T, int64_t rows, int64_t cols) {
+  const int64_t groups = !down ? 2048
+                         : grad ? (T <= 1 ? 1280 : T <= 2 ? 1024 : T <= 4 ? 768 : 512)
+                                : (T <= 4 ? 1280 : 768);
+  const int64_t blocks = cdiv(cols, down ? 256 : 1024);
+  int64_t part = round_up(cdiv(rows, at_least_one(groups / blocks)), down ? 32 : 8);
+  if (!down && part > sg::kXentFewAcross) part = sg::kXentFewAcross;
+  return {(int)part, (int)blocks, (int)cdiv(rows, part)};
+}
+
+// The logits that xent_few_down_kernel makes.
+bool few_logits(bool trans_b, int64_t T, int64_t V, int64_t H) {
+  return !trans_b && T > 0 && T <= kFewDown && V > 0 && H > 0 && 4 * T * V <= kPlanesOne;
+}
+
+// Forward, where rows of B begin at any 4 bytes and B is beyond the caches (us, products /
+// this: 4, 3144, 37682  165 / 99, 8, 4000, 20003  138 / 71, 1, 1100, 90001  88 / 83; smaller
+// 7, 900, 30001  28 / 34, 1, 2000, 9999  27 / 32; aligned 2, 1786, 56588  83 / 85).
+constexpr int64_t kFewForward = int64_t(256) << 20;   // bytes
+
 struct Forward {
   const XentVariant* v;
   bool gathered;
   int strips;
   int planes;   // 0: by tiles
+  FewGrid few;  // part 0: the planes are a product's
   XentRows rows;
   float *z, *max, *sum, *hit;
   int64_t bytes;
@@ -137,6 +170,10 @@ Forward plan_forward(bool trans_b, int64_t T, int64_t V, int64_t H, void* ws) {
   if (f.v == nullptr) return f;
   f.gathered = 2.0 * T * V * H / 150e12 > kGatherSeconds;
   f.planes = f.gathered ? 0 : choose_planes(f.v, false, trans_b, T, V, H);
+  if (!f.gathered && few_logits(trans_b, T, V, H) && V % 4 != 0 && 4 * V * H >= kFewForward) {
+    f.few = few_grid(true, false, T, H, V);
+    f.planes = f.few.parts;
+  }
   f.strips = (int)cdiv(V, f.planes > 0 ? sg::kXentPlanesCols / 4 : f.v->strip);
   Room room = {static_cast<char*>(ws), 0};
   if (f.gathered) f.rows = take_rows(room, T, H, false);
@@ -159,29 +196,6 @@ int64_t piece_columns(int64_t T, int64_t V, int64_t bytes) {
   return n >= V ? V : n / kPieceStep * kPieceStep;
 }
 
-// Up to eight rows: the logits in planes, their gradient, and both gradients in one
-// reading of B (kernel_xent_few.hpp).  Sixteen would leave a wave a SIMD (16, 1024, 32768
-// V x H 140 us where the rows' copies, three products and dX's scatter take 135).
-constexpr int64_t kFewRows = 8;
-
-// A launch over B as it is stored, rows x cols.
-struct FewGrid {
-  int part, blocks, parts;
-};
-
-// Down: as many workgroups as their registers let reside, in one round (T = 8, H = 3271, V
-// = 7145 V x H: 40 us, two rounds 44 and more planes to add up).  Across: 2048, so that
-// they end together (8, 1024, 32768: 48; 1024 workgroups 54, 768 50).
-FewGrid few_grid(bool down, bool grad, int64_t T, int64_t rows, int64_t cols) {
-  const int64_t groups = !down ? 2048
-                         : grad ? (T <= 1 ? 1280 : T <= 2 ? 1024 : T <= 4 ? 768 : 512)
-                                : (T <= 4 ? 1280 : 768);
-  const int64_t blocks = cdiv(cols, down ? 256 : 1024);
-  int64_t part = round_up(cdiv(rows, at_least_one(groups / blocks)), down ? 32 : 8);
-  if (!down && part > sg::kXentFewAcross) part = sg::kXentFewAcross;
-  return {(int)part, (int)blocks, (int)cdiv(rows, part)};
-}
-
 struct Few {
   bool possible;
   FewGrid z, grad;   // z: B stored H x V
@@ -193,17 +207,17 @@ struct Few {
 
 Few plan_few(bool trans_b, int64_t T, int64_t V, int64_t H, void* ws) {
   Few f = {};
-  if (T == 0 || T > kFewRows || V == 0 || H == 0 || 4 * T * V > kPlanesOne) return f;
+  if (T == 0 || T > (trans_b ? kFewDown : kFewAcross) || V == 0 || H == 0 || 4 * T * V > kPlanesOne) return f;
   const int64_t rows = trans_b ? V : H, cols = trans_b ? H : V;
   f.grad = few_grid(trans_b, true, T, rows, cols);
   f.count = trans_b ? f.grad.parts : f.grad.blocks;
-  if (trans_b) {
-    const PlanesPlan z = plan_planes(false, true, T, V, H, kPlanesAll);
-    if (!z.possible) return f;
-    f.z_count = z.count;
-  } else {
+  if (few_logits(trans_b, T, V, H)) {
     f.z = few_grid(true, false, T, rows, cols);
     f.z_count = f.z.parts;
+  } else {
+    const PlanesPlan z = plan_planes(false, trans_b, T, V, H, kPlanesAll);
+    if (!z.possible) return f;
+    f.z_count = z.count;
   }
   if (!grid_fits((int64_t)f.grad.blocks * f.grad.parts, sg::kXentFewThreads)) return f;
   Room room = {static_cast<char*>(ws), 0};
@@ -316,11 +330,15 @@ enum class FewKernel { kLogits, kDown, kAcross };
 
 template <int R>
 const void* few_kernel(FewKernel which, int64_t T) {
-  if constexpr (R < kFewRows)
+  if constexpr (R < kFewAcross)
     if (T > R) return few_kernel<2 * R>(which, T);
-  return which == FewKernel::kLogits ? reinterpret_cast<const void*>(sg::xent_few_down_kernel<R, false>)
-         : which == FewKernel::kDown ? reinterpret_cast<const void*>(sg::xent_few_down_kernel<R, true>)
-                                     : reinterpret_cast<const void*>(sg::xent_few_across_kernel<R>);
+  if constexpr (R <= kFewDown) {
+    if (which == FewKernel::kLogits)
+      return reinterpret_cast<const void*>(sg::xent_few_down_kernel<R, false>);
+    if (which == FewKernel::kDown)
+      return reinterpret_cast<const void*>(sg::xent_few_down_kernel<R, true>);
+  }
+  return reinterpret_cast<const void*>(sg::xent_few_across_kernel<R>);
 }
 
 int launch_few(FewKernel which, const FewGrid& grid, XentFewArgs& a, hipStream_t stream) {
@@ -385,8 +403,23 @@ int sgemm_linear_xent(int trans_b, int64_t T, int64_t V, int64_t H, const float*
     st = gather(t, f.rows, T, H, X, ldx, nullptr, nullptr, stream);
   if (V > 0 && st == SGEMM_OK && f.planes > 0) {
     XentPlanesArgs a = {};
-    st = launch_planes(trans_b, T, V, H, X, ldx, B, ldb, nullptr, f.z, 4 * f.planes * T * V, stream,
-                       a.count);
+    if (f.few.part > 0) {
+      XentFewArgs l = {};
+      l.targets = t;
+      l.B = B;
+      l.P = X;
+      l.planes = f.z;
+      l.T = (int)T;
+      l.rows = (int)H;
+      l.cols = (int)V;
+      l.ldb = (int)ldb;
+      l.ldp = (int)ldx;
+      a.count = f.planes;
+      st = launch_few(FewKernel::kLogits, f.few, l, stream);
+    } else {
+      st = launch_planes(trans_b, T, V, H, X, ldx, B, ldb, nullptr, f.z, 4 * f.planes * T * V,
+                         stream, a.count);
+    }
     a.planes = f.z;
     a.targets = t;
     a.max = f.max;
@@ -495,8 +528,8 @@ int sgemm_linear_xent_backward(int trans_b, int64_t T, int64_t V, int64_t H, con
     a.cols = (int)bc;
     a.ldb = (int)ldb;
     XentPlanesArgs p = {};
-    if (trans_b) {
-      st = launch_planes(true, T, V, H, X, ldx, B, ldb, nullptr, f.z_planes, kPlanesAll, stream,
+    if (f.z.part == 0) {
+      st = launch_planes(trans_b, T, V, H, X, ldx, B, ldb, nullptr, f.z_planes, kPlanesAll, stream,
                          p.count);
     } else {
       p.count = f.z_count;

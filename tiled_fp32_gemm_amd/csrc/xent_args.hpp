@@ -79,7 +79,7 @@ struct XentPlanesArgs {
   int rows, N, count, column0;
 };
 
-// Up to eight rows (kernel_xent_few.hpp).  In rows without a target P and Q do not
+// Few rows (kernel_xent_few.hpp).  In rows without a target P and Q do not
 // count, whatever they hold.
 struct XentFewArgs {
   Targets targets;

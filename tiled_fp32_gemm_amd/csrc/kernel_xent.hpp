@@ -16,10 +16,10 @@
 // without tiles, the product is left in planes, one for each part of a split K, and a
 // pass over them (xent_planes_*) adds them up and does the same.
 //
-// Rows without a target are left out of the products altogether: xent_place_kernel
-// numbers the others, whose rows of X are copied together; how many there are stays
-// on the device.  A padded or masked row costs nothing and, whatever it holds, reaches no
-// gradient.
+// Rows without a target are left out of the products altogether: xent_place_kernel or
+// xent_gather_kernel numbers the others, whose rows of X are copied together; how many
+// there are stays on the device.  A padded or masked row costs nothing and, whatever it
+// holds, reaches no gradient.
 //
 // Bound by the matrix pipe for many rows, by reading B for a few.  Measured on MI355X
 // with B stored V x H, H = 1024, V = 32768: 6144 rows forward 2807 us (147 TFLOP/s;
@@ -82,6 +82,48 @@ __global__ void __launch_bounds__(kXentPlaceThreads) xent_place_kernel(XentPlace
     a.rows.offsets[0] = 0;
     a.rows.offsets[1] = next;
   }
+}
+
+// Up to kXentGatherRows tokens: a wave numbers a token and copies 1024 columns of its row,
+// in one launch (place and copy in two: 9.4 us for 4.9, 104 tokens of H = 1399).
+constexpr int kXentGatherRows = 1024, kXentGatherCols = 1024;
+
+__global__ void __launch_bounds__(256) xent_gather_kernel(XentPlaceArgs a) {
+  const int lane = (int)threadIdx.x & 63;
+  const unsigned chunks = (unsigned)max((a.H + kXentGatherCols - 1) / kXentGatherCols, 1);
+  const unsigned w = (unsigned)__builtin_amdgcn_readfirstlane(
+      (int)(blockIdx.x * 4 + (threadIdx.x >> 6)));
+  const int t = (int)(w / chunks), chunk = (int)(w % chunks);
+  if (t >= (int)a.T) return;
+  int row = 0;
+#pragma unroll 4
+  for (int i0 = 0; i0 < t; i0 += 64) {
+    const int target = a.targets.of(min(i0 + lane, t - 1));
+    row += __popcll(__ballot(target >= 0 && i0 + lane < t));
+  }
+  const int target = a.targets.of(t);
+  if (chunk == 0 && lane == 0) {
+    a.rows.place[t] = target >= 0 ? row : -1;
+    if (target >= 0) {
+      if (a.lse) a.rows.row[row] = xent_row(target, a.lse[t], a.dloss[t]);
+      else a.rows.target[row] = target;
+    }
+    if (t == (int)a.T - 1) {
+      a.rows.offsets[0] = 0;
+      a.rows.offsets[1] = row + (target >= 0 ? 1 : 0);
+    }
+  }
+  if (target < 0) return;
+  const int col = chunk * kXentGatherCols + 4 * lane;
+  const float* const from = a.X + t * a.ldx + col;
+  float* const to = a.rows.X + (int64_t)row * a.H + col;
+  f32x4 v[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (a.H - col > 256 * u) v[u] = load_upto(from + 256 * u, a.H - col - 256 * u);
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (a.H - col > 256 * u) store_upto(to + 256 * u, a.H - col - 256 * u, v[u]);
 }
 
 // A wave takes 256 columns of a row of the planes, four a lane.

@@ -286,6 +286,14 @@ int gather(const Targets& targets, const XentRows& rows, int64_t T, int64_t H, c
   a.lse = lse;
   a.dloss = dloss;
   a.T = T;
+  if (T > 0 && T <= sg::kXentGatherRows) {
+    a.X = X;
+    a.ldx = ldx;
+    a.H = (int)H;
+    const int64_t waves = T * at_least_one(cdiv(H, sg::kXentGatherCols));
+    return launch(reinterpret_cast<const void*>(sg::xent_gather_kernel), cdiv(waves, 4), 256, &a,
+                  stream);
+  }
   // Up to 256 workgroups, as each reads all the targets before its own.
   a.chunk = round_up(at_least_one(cdiv(T, 256)), sg::kXentPlaceThreads);
   const int st = launch(reinterpret_cast<const void*>(sg::xent_place_kernel),

@@ -107,6 +107,9 @@ struct XentPlaceArgs {
   const float* lse;      // null: forward
   const float* dloss;
   int64_t T, chunk;      // tokens of a workgroup
+  const float* X;        // xent_gather_kernel copies its rows too
+  int64_t ldx;
+  int H;
 };
 
 struct XentLossArgs {

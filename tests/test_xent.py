@@ -168,7 +168,7 @@ def test_a_vocabulary_in_pieces(T, H, V, tb):
 FEW = [(1, 255, 1000), (2, 256, 4099), (3, 257, 513), (5, 1025, 2047), (6, 130, 1024),
        (8, 512, 1025), (8, 2049, 129), (7, 1, 3000), (4, 3000, 1), (8, 4, 70000), (1, 1030, 33000),
        (3, 5000, 700), (9, 300, 900), (16, 333, 2049), (13, 1024, 511), (16, 2, 5),
-       (17, 90, 1030)]
+       (17, 90, 1030), (15, 4000, 600), (16, 60, 20000), (11, 129, 641)]
 
 
 @pytest.mark.gpu
@@ -395,6 +395,7 @@ def test_gradients_against_differences(tb):
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,H,V,tb", [(1, 64, 500, True), (200, 100, 3000, False),
                                       (19, 2894, 3306, False), (4, 1024, 32768, True),
+                                      (12, 300, 5000, True), (16, 200, 9001, False),
                                       (2048, 1024, 8192, True)])
 def test_replays_from_a_graph_with_other_targets(T, H, V, tb):
     g = gen(T + V)

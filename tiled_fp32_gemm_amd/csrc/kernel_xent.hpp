@@ -126,6 +126,16 @@ __global__ void __launch_bounds__(256) xent_gather_kernel(XentPlaceArgs a) {
     if (a.H - col > 256 * u) store_upto(to + 256 * u, a.H - col - 256 * u, v[u]);
 }
 
+// A few tokens' rows as they stand; without a target a gradient of 0.
+__global__ void __launch_bounds__(64) xent_rows_kernel(XentPlaceArgs a) {
+  const int64_t t = threadIdx.x;
+  if (t >= a.T) return;
+  const int target = a.targets.of(t);
+  XentRow row = {-1, 0.0f, 0.0f, 0.0f};
+  if (target >= 0) row = xent_row(target, a.lse[t], a.dloss[t]);
+  a.rows.row[t] = row;
+}
+
 // A wave takes 256 columns of a row of the planes, four a lane.
 constexpr int kXentPlanesCols = 1024;   // of a workgroup
 

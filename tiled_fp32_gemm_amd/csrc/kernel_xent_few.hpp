@@ -1,5 +1,5 @@
 // kernel_xent_few.hpp -- both gradients of the cross entropy over a product for up to
-// eight rows, or sixteen where B is H x V.
+// sixteen rows.
 //
 //   dB = sum over tokens of x by dz        dX = dz·op(B)'
 //
@@ -23,9 +23,9 @@
 //           tiles took 87 to 180
 //   across  8, 1024, 32768  47.8 (5.6), 2, 2871, 34831  163 (4.9)
 //   All of the gradients, against the rows' copies, three products and dX's scatter:
-//   across, sixteen rows 1024, 32768  91 for 114, 4096, 32768  361 for 378, 9, 1030, 20001
-//   60 for 96; down for sixteen keeps two times 64 sums and factors in a lane, which spill
-//   (16, 1024, 32768  185 for 113), and is left out
+//   down, sixteen rows 1024, 32768  91 for 111, 64, 60000  31 for 41 (four columns in a lane
+//   would spill: 185 for 113), 12, 2217, 5372  50 for 66; across, 9, 1030, 20001  64 for 96,
+//   sixteen rows 1024, 32768  89 for 114
 //   Columns four together in a lane (16-byte accesses at any alignment) down: 3271 59.5,
 //   1030 87.  dB past the caches down: 49 and 76, as the ends of unaligned rows' pieces
 //   are then written in parts; across, where a workgroup's piece is 4 KB, in them: 149 for
@@ -41,34 +41,37 @@ namespace sg {
 constexpr int kXentFewThreads = 256;
 constexpr int kXentFewAcross = 64;   // most rows of B of a workgroup across
 
-// A lane's four columns of a block of 256: from `first` on, 64 apart, and never past the
+// A lane's C columns of a block of 64 C: from `first` on, 64 apart, and never past the
 // last, which is repeated there (its sums are dropped), as loads that some lanes leave out
 // are waited for one by one.  Rows begin at scalar addresses, so these are all that is
 // held of one.
+template <int C>
 struct FewCols {
-  unsigned at[4];   // bytes
+  unsigned at[C];   // bytes
   int left;         // columns from `first` on
 
   __device__ __forceinline__ FewCols(int first, int cols) : left(cols - first) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) at[e] = 4u * (unsigned)min(first + 64 * e, cols - 1);
+    for (int e = 0; e < C; ++e) at[e] = 4u * (unsigned)min(first + 64 * e, cols - 1);
   }
   template <bool ONCE>
-  __device__ __forceinline__ f32x4 load(const float* row) const {
-    f32x4 v;
+  __device__ __forceinline__ void load(const float* row, float (&v)[C]) const {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const auto* const p = reinterpret_cast<const float*>(reinterpret_cast<const char*>(row) + at[e]);
+    for (int e = 0; e < C; ++e) {
+      const char* const at_e = reinterpret_cast<const char*>(row) + at[e];
+      const float* const p = reinterpret_cast<const float*>(at_e);
       v[e] = ONCE ? __builtin_nontemporal_load(p) : *p;
     }
-    return v;
   }
-  __device__ __forceinline__ void store(float* row, f32x4 v) const {
+  __device__ __forceinline__ void store(float* row, const float (&v)[C]) const {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < C; ++e)
       if (64 * e < left) *reinterpret_cast<float*>(reinterpret_cast<char*>(row) + at[e]) = v[e];
   }
 };
+
+// Columns of a lane down: two for sixteen rows, whose factors and sums would spill.
+constexpr int xent_few_cols(int R) { return R <= 8 ? 4 : 2; }
 
 // The tokens with a target, a bit each.
 __device__ __forceinline__ unsigned xent_few_kept(const XentFewArgs& a) {
@@ -79,20 +82,22 @@ __device__ __forceinline__ unsigned xent_few_kept(const XentFewArgs& a) {
 template <int R, bool GRAD>
 __global__ void __launch_bounds__(kXentFewThreads) xent_few_down_kernel(XentFewArgs a) {
   constexpr int U = 8;                 // rows of B in flight
+  constexpr int C = xent_few_cols(R);
   constexpr int CHUNK = 128, NUMBERS = CHUNK * R;
-  __shared__ __attribute__((aligned(16))) float room[2 * R * 256];   // numbers, then sums
+  __shared__ __attribute__((aligned(16))) float room[2 * R * 64 * C];   // numbers, then sums
   const int tid = (int)threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const unsigned place = (unsigned)xcd_order((int)blockIdx.x, (int)gridDim.x);
   const int block = (int)(place % (unsigned)a.blocks), part = (int)(place / (unsigned)a.blocks);
   const int first = part * a.part, last = min(first + a.part, a.rows);
-  const FewCols cols(block * 256 + lane, a.cols);
+  const FewCols<C> cols(block * (64 * C) + lane, a.cols);
   const unsigned kept = xent_few_kept(a);
-  f32x4 q[R], acc[R];
+  float q[R][C], acc[R][C];
 #pragma unroll
   for (int t = 0; t < R; ++t) {
-    q[t] = acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (GRAD && (kept >> t & 1)) q[t] = cols.load<false>(a.Q + (int64_t)t * a.ldq);
+#pragma unroll
+    for (int e = 0; e < C; ++e) q[t][e] = acc[t][e] = 0.0f;
+    if (GRAD && (kept >> t & 1)) cols.template load<false>(a.Q + (int64_t)t * a.ldq, q[t]);
   }
   for (int c0 = first; c0 < last; c0 += CHUNK) {
     const int rows = min(CHUNK, last - c0);
@@ -104,14 +109,16 @@ __global__ void __launch_bounds__(kXentFewThreads) xent_few_down_kernel(XentFewA
     __syncthreads();
     const float* const b = a.B + (int64_t)c0 * a.ldb;
     float* const d = a.D + (int64_t)c0 * a.ldd;
-    auto load = [&](int r) { return cols.load<GRAD>(b + (int64_t)r * a.ldb); };
-    auto take = [&](int r, f32x4 v) {
-      f32x4 g = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto load = [&](int r, float (&v)[C]) {
+      cols.template load<GRAD>(b + (int64_t)r * a.ldb, v);
+    };
+    auto take = [&](int r, const float (&v)[C]) {
+      float g[C] = {};
 #pragma unroll
       for (int t = 0; t < R; ++t) {
         const float p = room[r * R + t];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < C; ++e) {
           acc[t][e] = fmaf(p, v[e], acc[t][e]);
           if (GRAD) g[e] = fmaf(p, q[t][e], g[e]);
         }
@@ -120,30 +127,44 @@ __global__ void __launch_bounds__(kXentFewThreads) xent_few_down_kernel(XentFewA
     };
     for (int r0 = wave * U; r0 < rows; r0 += 4 * U) {
       if (r0 + U <= rows) {
-        f32x4 v[U];
+        float v[U][C];
 #pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = load(r0 + u);
+        for (int u = 0; u < U; ++u) load(r0 + u, v[u]);
 #pragma unroll
         for (int u = 0; u < U; ++u) take(r0 + u, v[u]);
       } else {
-        for (int r = r0; r < rows; ++r) take(r, load(r));
+        for (int r = r0; r < rows; ++r) {
+          float v[C];
+          load(r, v);
+          take(r, v);
+        }
       }
     }
   }
   if (a.planes == nullptr) return;
   // The four waves' sums, by halves.
-  f32x4* const join = reinterpret_cast<f32x4*>(room);
+  typedef float part_t __attribute__((ext_vector_type(C)));
+  part_t* const join = reinterpret_cast<part_t*>(room);
 #pragma unroll
   for (int half = 2; half > 0; half /= 2) {
     __syncthreads();
     if (wave >= half && wave < 2 * half) {
 #pragma unroll
-      for (int t = 0; t < R; ++t) join[((wave - half) * R + t) * 64 + lane] = acc[t];
+      for (int t = 0; t < R; ++t) {
+        part_t p;
+#pragma unroll
+        for (int e = 0; e < C; ++e) p[e] = acc[t][e];
+        join[((wave - half) * R + t) * 64 + lane] = p;
+      }
     }
     __syncthreads();
     if (wave < half) {
 #pragma unroll
-      for (int t = 0; t < R; ++t) acc[t] += join[(wave * R + t) * 64 + lane];
+      for (int t = 0; t < R; ++t) {
+        const part_t p = join[(wave * R + t) * 64 + lane];
+#pragma unroll
+        for (int e = 0; e < C; ++e) acc[t][e] += p[e];
+      }
     }
   }
   if (wave > 0) return;
@@ -153,7 +174,8 @@ __global__ void __launch_bounds__(kXentFewThreads) xent_few_down_kernel(XentFewA
 }
 
 template <int R>
-__global__ void __launch_bounds__(kXentFewThreads, R <= 8 ? 4 : 2) xent_few_across_kernel(XentFewArgs a) {
+__global__ void __launch_bounds__(kXentFewThreads, R <= 8 ? 4 : 2)
+    xent_few_across_kernel(XentFewArgs a) {
   constexpr int U = R <= 4 ? 8 : 4;    // rows of B in flight
   constexpr int S = U * R;                   // sums over the lanes at once
   constexpr int ROWS = kXentFewAcross;

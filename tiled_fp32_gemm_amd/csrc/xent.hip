@@ -121,9 +121,9 @@ int choose_planes(const XentVariant* v, bool grouped, bool trans_b, int64_t T, i
   return 9e-6 + b / 5.0e12 < 0.95 * slow ? 1 : 0;
 }
 
-// A few rows: the logits in planes, their gradient, and both gradients in one reading of
-// B (kernel_xent_few.hpp).
-constexpr int64_t kFewDown = 8, kFewAcross = 16;
+// A few rows: the logits in planes and their gradient, or a product that ends in it, and
+// both gradients in one reading of B (kernel_xent_few.hpp).
+constexpr int64_t kFewRows = 16, kFewLogits = 8;   // of the gradients; of the logits
 
 // A launch over B as it is stored, rows x cols.
 struct FewGrid {
@@ -137,7 +137,7 @@ FewGrid few_grid(bool down, bool grad, int64_t T, int64_t rows, int64_t cols) {
   const int64_t groups = !down ? 2048
                          : grad ? (T <= 1 ? 1280 : T <= 2 ? 1024 : T <= 4 ? 768 : 512)
                                 : (T <= 4 ? 1280 : 768);
-  const int64_t blocks = cdiv(cols, down ? 256 : 1024);
+  const int64_t blocks = cdiv(cols, down ? 64 * sg::xent_few_cols((int)T) : 1024);
   int64_t part = round_up(cdiv(rows, at_least_one(groups / blocks)), down ? 32 : 8);
   if (!down && part > sg::kXentFewAcross) part = sg::kXentFewAcross;
   return {(int)part, (int)blocks, (int)cdiv(rows, part)};
@@ -145,7 +145,7 @@ FewGrid few_grid(bool down, bool grad, int64_t T, int64_t rows, int64_t cols) {
 
 // The logits that xent_few_down_kernel makes.
 bool few_logits(bool trans_b, int64_t T, int64_t V, int64_t H) {
-  return !trans_b && T > 0 && T <= kFewDown && V > 0 && H > 0 && 4 * T * V <= kPlanesOne;
+  return !trans_b && T > 0 && T <= kFewLogits && V > 0 && H > 0 && 4 * T * V <= kPlanesOne;
 }
 
 // Forward, where rows of B begin at any 4 bytes and B is beyond the caches (us, products /
@@ -198,16 +198,18 @@ int64_t piece_columns(int64_t T, int64_t V, int64_t bytes) {
 
 struct Few {
   bool possible;
-  FewGrid z, grad;   // z: B stored H x V
+  FewGrid z, grad;   // z: by xent_few_down_kernel; part 0: by a product
+  const XentVariant* v;   // that ends in dz; null: in planes
   int count;         // planes of dX
   int z_count;       // and of the logits
   float *z_planes, *planes;
+  sg::XentRow* row;
   int64_t bytes;
 };
 
 Few plan_few(bool trans_b, int64_t T, int64_t V, int64_t H, void* ws) {
   Few f = {};
-  if (T == 0 || T > (trans_b ? kFewDown : kFewAcross) || V == 0 || H == 0 || 4 * T * V > kPlanesOne) return f;
+  if (T == 0 || T > kFewRows || V == 0 || H == 0 || 4 * T * V > kPlanesOne) return f;
   const int64_t rows = trans_b ? V : H, cols = trans_b ? H : V;
   f.grad = few_grid(trans_b, true, T, rows, cols);
   f.count = trans_b ? f.grad.parts : f.grad.blocks;
@@ -215,14 +217,25 @@ Few plan_few(bool trans_b, int64_t T, int64_t V, int64_t H, void* ws) {
     f.z = few_grid(true, false, T, rows, cols);
     f.z_count = f.z.parts;
   } else {
-    const PlanesPlan z = plan_planes(false, trans_b, T, V, H, kPlanesAll);
-    if (!z.possible) return f;
-    f.z_count = z.count;
+    f.v = choose(trans_b, T, V, H);
+    if (f.v == nullptr) return f;
+    f.z_count = choose_planes(f.v, false, trans_b, T, V, H);
+    if (f.z_count == 0) {
+      // By rows, B read twice, where its tiles are too few (15, 4000, 600 V x H 30 us, tiles
+      // 70; 16, 64, 60000 53 and 31).
+      const PlanesPlan z = plan_planes(false, trans_b, T, V, H, kPlanesAll);
+      const int64_t tiles = cdiv(T, f.v->cost.tile_m) * cdiv(V, f.v->cost.tile_n);
+      if (z.possible && z.count == 1 && z.seconds < 0.5 * estimate_grid(f.v->cost, tiles, H))
+        f.z_count = 1;
+    }
+    if (f.z_count > 0) f.v = nullptr;
+    else f.z_count = 1;
   }
   if (!grid_fits((int64_t)f.grad.blocks * f.grad.parts, sg::kXentFewThreads)) return f;
   Room room = {static_cast<char*>(ws), 0};
   f.z_planes = room.take<float>(f.z_count * T * V);
   f.planes = room.take<float>(f.count * T * H);
+  if (f.v) f.row = room.take<sg::XentRow>(T);
   f.bytes = room.used;
   f.possible = true;
   return f;
@@ -338,14 +351,13 @@ enum class FewKernel { kLogits, kDown, kAcross };
 
 template <int R>
 const void* few_kernel(FewKernel which, int64_t T) {
-  if constexpr (R < kFewAcross)
+  if constexpr (R < kFewRows)
     if (T > R) return few_kernel<2 * R>(which, T);
-  if constexpr (R <= kFewDown) {
+  if constexpr (R <= kFewLogits)
     if (which == FewKernel::kLogits)
       return reinterpret_cast<const void*>(sg::xent_few_down_kernel<R, false>);
-    if (which == FewKernel::kDown)
-      return reinterpret_cast<const void*>(sg::xent_few_down_kernel<R, true>);
-  }
+  if (which == FewKernel::kDown)
+    return reinterpret_cast<const void*>(sg::xent_few_down_kernel<R, true>);
   return reinterpret_cast<const void*>(sg::xent_few_across_kernel<R>);
 }
 
@@ -535,27 +547,43 @@ int sgemm_linear_xent_backward(int trans_b, int64_t T, int64_t V, int64_t H, con
     a.rows = (int)br;
     a.cols = (int)bc;
     a.ldb = (int)ldb;
-    XentPlanesArgs p = {};
-    if (f.z.part == 0) {
-      st = launch_planes(trans_b, T, V, H, X, ldx, B, ldb, nullptr, f.z_planes, kPlanesAll, stream,
-                         p.count);
+    if (f.v) {
+      XentPlaceArgs p = {};
+      p.targets = t;
+      p.rows.row = f.row;
+      p.lse = lse;
+      p.dloss = dloss;
+      p.T = T;
+      st = launch(reinterpret_cast<const void*>(sg::xent_rows_kernel), 1, 64, &p, stream);
+      if (st != SGEMM_OK) return st;
+      XentProductArgs z = product_args(T, V, H, X, ldx, B, ldb, nullptr);
+      z.C = f.z_planes;
+      z.ldc = (int)V;
+      z.row = f.row;
+      st = launch_product(*f.v, z, true, stream);
     } else {
-      p.count = f.z_count;
-      a.P = X;
-      a.ldp = (int)ldx;
-      a.planes = f.z_planes;
-      st = launch_few(FewKernel::kLogits, f.z, a, stream);
+      XentPlanesArgs p = {};
+      if (f.z.part == 0) {
+        st = launch_planes(trans_b, T, V, H, X, ldx, B, ldb, nullptr, f.z_planes, kPlanesAll,
+                           stream, p.count);
+      } else {
+        p.count = f.z_count;
+        a.P = X;
+        a.ldp = (int)ldx;
+        a.planes = f.z_planes;
+        st = launch_few(FewKernel::kLogits, f.z, a, stream);
+      }
+      if (st != SGEMM_OK) return st;
+      p.planes = f.z_planes;
+      p.dZ = f.z_planes;
+      p.targets = t;
+      p.lse = lse;
+      p.dloss = dloss;
+      p.rows = (int)T;
+      p.N = (int)V;
+      st = launch(reinterpret_cast<const void*>(sg::xent_planes_grad_kernel),
+                  T * cdiv(V, sg::kXentPlanesCols), 256, &p, stream);
     }
-    if (st != SGEMM_OK) return st;
-    p.planes = f.z_planes;
-    p.dZ = f.z_planes;
-    p.targets = t;
-    p.lse = lse;
-    p.dloss = dloss;
-    p.rows = (int)T;
-    p.N = (int)V;
-    st = launch(reinterpret_cast<const void*>(sg::xent_planes_grad_kernel),
-                T * cdiv(V, sg::kXentPlanesCols), 256, &p, stream);
     if (st != SGEMM_OK) return st;
     a.P = trans_b ? f.z_planes : X;
     a.ldp = (int)(trans_b ? V : ldx);

@@ -268,6 +268,14 @@ def test_rows_without_a_target_reach_nothing(T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [17, 63, 64, 65, 256, 257, 511, 1023, 1024, 1025])
+def test_rows_are_numbered(T):
+    """Up to 1024 by a wave each."""
+    for H, ignored in ((1030, 0.5), (3, 0.9), (2049, 0.0)):
+        run(T, H, 60, H > 3, ignored=ignored, dtype=torch.int32 if H == 3 else torch.int64, seed=T)
+
+
+@pytest.mark.gpu
 def test_more_rows_than_one_workgroup_numbers_at_a_time():
     """Rows with a target in every pattern: 200000 tokens, 1024 a workgroup."""
     g = gen(55)

@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kXentPlaceThreads) xent_place_kernel(XentPlace
 }
 
 // Up to kXentGatherRows tokens: a wave numbers a token and copies 1024 columns of its row,
-// in one launch (place and copy in two: 9.4 us for 4.9, 104 tokens of H = 1399).
+// in one launch (two launches: 9.4 us for 4.9, 104 tokens of H = 1399).
 constexpr int kXentGatherRows = 1024, kXentGatherCols = 1024;
 
 __global__ void __launch_bounds__(256) xent_gather_kernel(XentPlaceArgs a) {
@@ -95,13 +95,20 @@ __global__ void __launch_bounds__(256) xent_gather_kernel(XentPlaceArgs a) {
       (int)(blockIdx.x * 4 + (threadIdx.x >> 6)));
   const int t = (int)(w / chunks), chunk = (int)(w % chunks);
   if (t >= (int)a.T) return;
-  int row = 0;
-#pragma unroll 4
-  for (int i0 = 0; i0 < t; i0 += 64) {
-    const int target = a.targets.of(min(i0 + lane, t - 1));
-    row += __popcll(__ballot(target >= 0 && i0 + lane < t));
-  }
   const int target = a.targets.of(t);
+  int row = 0;   // those before with a target; four rounds' loads, or all, in flight
+  auto count = [&](auto from, auto to) {
+    constexpr int I = decltype(from)::value, N = decltype(to)::value - I;
+    int before[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) before[i] = a.targets.of(min((I + i) * 64 + lane, t));
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      row += __popcll(__ballot(before[i] >= 0 && (I + i) * 64 + lane < t));
+  };
+  count(std::integral_constant<int, 0>(), std::integral_constant<int, 4>());
+  if (t > 256)
+    count(std::integral_constant<int, 4>(), std::integral_constant<int, kXentGatherRows / 64>());
   if (chunk == 0 && lane == 0) {
     a.rows.place[t] = target >= 0 ? row : -1;
     if (target >= 0) {

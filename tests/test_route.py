@@ -116,7 +116,9 @@ def test_route(T, E, top, scoring):
 @pytest.mark.parametrize("T,E,groups,top_groups,top", [
     (100, 8, 2, 1, 3), (77, 8, 8, 3, 3), (50, 12, 3, 2, 5), (300, 64, 4, 2, 8), (65, 96, 32, 5, 6),
     (400, 256, 8, 4, 8), (33, 160, 8, 3, 6), (40, 320, 16, 4, 12), (20, 1024, 32, 8, 32),
-    (20, 1022, 7, 6, 9), (64, 30, 15, 4, 4), (9, 16, 2, 2, 16)])
+    (20, 1022, 7, 6, 9), (64, 30, 15, 4, 4), (9, 16, 2, 2, 16), (60, 96, 6, 4, 8),
+    (31, 128, 32, 16, 20), (50, 512, 32, 1, 16), (45, 24, 6, 2, 8), (70, 64, 16, 1, 4),
+    (33, 256, 8, 4, 32), (40, 1024, 16, 8, 32), (20, 480, 12, 5, 8), (66, 256, 32, 16, 1)])
 @pytest.mark.parametrize("group_best", [1, 2])
 def test_groups(T, E, groups, top_groups, top, group_best):
     if E // groups < group_best:

@@ -17,12 +17,13 @@
 // computes the scores again in FP64, those that may be chosen (reorder), or all
 // where the groups are open or there are too many (refine).
 //
-// Bound by vector instructions, about 1610 a wave for eight tokens' best 8 of 256 in
+// Bound by vector instructions, about 1330 a wave for eight tokens' best 8 of 256 in
 // groups by sigmoid and bias, where the copies of 32768 such rows would take 7.3 us:
-// measured on MI355X 18.7 us, of which the last waves' FP64 takes 2.5; without bias and
-// groups 10.8, 8191 tokens of 64 experts 3.9.  Sixteen lanes a token instead of eight
-// (twice the waves, half the experts a lane) took 23.9 for 19.9, a branch for each
-// expert's special cases 37.  A batch of equal scores, all in FP64: 64 us.
+// measured on MI355X 17.3 us, of which the last waves' FP64 takes 2.5; without bias and
+// groups 10.8, 8191 tokens of 64 experts 3.8.  Where the groups that stay have at most half
+// of the experts, only those are sorted (all: 1612 instructions, 18.8 us).  Sixteen lanes
+// a token instead of eight (twice the waves, half the experts a lane) took 23.9 for 19.9, a
+// branch for each expert's special cases 37.  A batch of equal scores, all in FP64: 64 us.
 // The gradient is bound by HBM: 32768 x 256 (69 MB) in 13.2 to 14.3 us.
 #pragma once
 
@@ -312,7 +313,8 @@ __global__ void __launch_bounds__(256, K <= 8 ? 4 : 2) route_kernel(RouteArgs a)
   constexpr int TOKENS = 256 / G, N = 4 * V;
   // Each wave has its tokens' part of both.
   __shared__ __attribute__((aligned(16))) uint32_t keys[TOKENS * N * G];
-  __shared__ int ids[TOKENS][kRouteTop];
+  // Eight tokens' rows begin on different banks.
+  __shared__ __attribute__((aligned(16))) int ids[TOKENS][kRouteTop + 4];
   __shared__ int candidates[TOKENS];
   static_assert(64 / G * N * G * 4 >= N * G * 8, "a wave's keys hold one token's FP64 scores");
   const int lane = (int)threadIdx.x & 63, g = (int)threadIdx.x % G;
@@ -405,6 +407,13 @@ __global__ void __launch_bounds__(256, K <= 8 ? 4 : 2) route_kernel(RouteArgs a)
     for (int i = 0; i < N; ++i) key[i] = ordered(c[i]);
   }
   bool regroup = false, unsure = false;   // of the groups, of the experts
+  // Groups that stay of at most half of the experts: each lane takes quads of theirs
+  // alone, the first half of its keys, and the rest is not looked at again.
+  constexpr int HALF = V > 1 ? V / 2 : 1;
+  const bool fewer = V > 1 && a.size % 4 == 0 && 2 * a.top_groups * a.size <= N * G;
+  int quad[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) quad[i] = g + i * G;
 
   if (a.groups > 1) {
     // Lane g looks at groups g, g + G ..: the best and second best of each, then
@@ -453,22 +462,27 @@ __global__ void __launch_bounds__(256, K <= 8 ? 4 : 2) route_kernel(RouteArgs a)
                        ? ordered(unordered(best) + unordered(second)) : best;
       }
     }
-    wave_lds_fence();
+    uint32_t* const totals = reinterpret_cast<uint32_t*>(ids[sub]);
+    static_assert(kRouteTop >= SGEMM_MOE_MAX_GROUPS, "room for the groups' totals");
 #pragma unroll
     for (int r = 0; r < ROUNDS; ++r)
-      if (r * G < a.groups && r * G + g < a.groups) mine[r * G + g] = total[r];
+      if (r * G < a.groups) totals[r * G + g] = r * G + g < a.groups ? total[r] : 0u;
     wave_lds_fence();
     uint32_t stays = 0;
+    int rank_of[ROUNDS];
     uint32_t least = 0u, next = 0u;   // the last group that stays, the first that does not
 #pragma unroll
     for (int r = 0; r < ROUNDS; ++r) {
       if (r * G < a.groups) {
         const int q = r * G + g;
         int rank = q < a.groups ? 0 : a.groups;
-        for (int o = 0; o < a.groups; ++o) {
-          const uint32_t other = mine[o];
-          rank += other > total[r] || (other == total[r] && o < q) ? 1 : 0;
+        for (int o = 0; o < a.groups; o += 4) {   // past the last one, zeros
+          const u32x4 other = *reinterpret_cast<const u32x4*>(totals + o);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            rank += other[e] > total[r] || (other[e] == total[r] && o + e < q) ? 1 : 0;
         }
+        rank_of[r] = rank;
         if (rank == a.top_groups - 1) least = total[r];
         if (rank == a.top_groups) next = total[r];
         const uint64_t bits = __ballot(rank < a.top_groups) >> (lane - g);
@@ -486,7 +500,27 @@ __global__ void __launch_bounds__(256, K <= 8 ? 4 : 2) route_kernel(RouteArgs a)
         regroup = x - y <= 2.0f * off + 8.0f * kHalfStep * (fabsf(x) + fabsf(y));
       }
     }
-    if (size % 4 == 0) {
+    if (fewer) {
+      wave_lds_fence();
+#pragma unroll
+      for (int r = 0; r < ROUNDS; ++r)
+        if (r * G < a.groups && rank_of[r] < a.top_groups) ids[sub][rank_of[r]] = r * G + g;
+      wave_lds_fence();
+#pragma unroll
+      for (int i = 0; i < HALF; ++i) {
+        const int at = 4 * (g + i * G), n = group_of(a, at);   // of those that stay
+        u32x4 v = {kNever, kNever, kNever, kNever};
+        if (n < a.top_groups) {
+          const int first = ids[sub][n] * size + at - n * size;
+          quad[i] = first >> 2;
+          v = *reinterpret_cast<const u32x4*>(mine + first);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) key[4 * i + e] = v[e];
+      }
+#pragma unroll
+      for (int i = 4 * HALF; i < N; ++i) key[i] = kNever;
+    } else if (size % 4 == 0) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const bool gone = !(stays >> group_of(a, min(4 * (g + i * G), last)) & 1);
@@ -506,11 +540,12 @@ __global__ void __launch_bounds__(256, K <= 8 ? 4 : 2) route_kernel(RouteArgs a)
   double best[K];
 #pragma unroll
   for (int i0 = 0; i0 < N; i0 += K) {
+    if (i0 >= 4 * HALF && fewer) continue;
     double v[K];
 #pragma unroll
     for (int j = 0; j < K; ++j)
       v[j] = i0 + j < N ? packed(key[i0 + j < N ? i0 + j : 0],
-                                 4 * (g + ((i0 + j) >> 2) * G) + ((i0 + j) & 3))
+                                 4 * quad[(i0 + j < N ? i0 + j : 0) >> 2] + ((i0 + j) & 3))
                         : 0.0;
     sort_down(v);
     if (i0 == 0) {
@@ -562,7 +597,11 @@ __global__ void __launch_bounds__(256, K <= 8 ? 4 : 2) route_kernel(RouteArgs a)
     // No other may be within reach of the last one.
     int close = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) close += key[i] >= from ? 1 : 0;
+    for (int i = 0; i < 4 * HALF; ++i) close += key[i] >= from ? 1 : 0;
+    if (!fewer) {
+#pragma unroll
+      for (int i = 4 * HALF; i < N; ++i) close += key[i] >= from ? 1 : 0;
+    }
     close = group_sum<G>(close);
     unsure |= (chosen > kNever) & (close > a.top);
     // A token's lanes agree on both.
@@ -577,7 +616,7 @@ __global__ void __launch_bounds__(256, K <= 8 ? 4 : 2) route_kernel(RouteArgs a)
         for (int i = 0; i < N; ++i) {
           if (key[i] >= from && key[i] > kNever) {
             const int slot = atomicAdd(&candidates[sub], 1);
-            if (slot < MOST) list[slot] = 4 * (g + (i >> 2) * G) + (i & 3);
+            if (slot < MOST) list[slot] = 4 * quad[i >> 2] + (i & 3);
           }
         }
       }

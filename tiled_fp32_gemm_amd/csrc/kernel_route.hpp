@@ -19,7 +19,7 @@
 //
 // Bound by vector instructions, about 1330 a wave for eight tokens' best 8 of 256 in
 // groups by sigmoid and bias, where the copies of 32768 such rows would take 7.3 us:
-// measured on MI355X 17.3 us, of which the last waves' FP64 takes 2.5; without bias and
+// measured on MI355X 16.6 to 17.3 us, of which the last waves' FP64 takes 2.5; without bias and
 // groups 10.8, 8191 tokens of 64 experts 3.8.  Where the groups that stay have at most half
 // of the experts, only those are sorted (all: 1612 instructions, 18.8 us).  Sixteen lanes
 // a token instead of eight (twice the waves, half the experts a lane) took 23.9 for 19.9, a

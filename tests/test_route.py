@@ -164,6 +164,72 @@ def test_scores_that_fp32_cannot_tell_apart(E, top, scoring):
     check(x, top, scoring, b)
 
 
+def apart64(x, top, scoring, bias, groups, top_groups):
+    """The tokens whose choice 64 bits tell apart for certain, with groups of two
+    scores: the last group that stays and the first that does not, and each choice and
+    the next one.  A score is within 2^-48 of its value there, and c and a total of two
+    round by 2^-53 of the largest bias each: 8 such roundings lie below `least`."""
+    x, b = x.cpu().double(), bias.cpu().double()
+    T, E = x.shape
+    least = 1e-13 + 8 * 2.0 ** -53 * b.abs().max()
+    c = scores64(x, scoring) + b
+    total = c.reshape(T, groups, -1).sort(dim=2, descending=True).values[:, :, :2].sum(2)
+    total, order = total.sort(dim=1, descending=True, stable=True)
+    good = total[:, top_groups - 1] - total[:, top_groups] > least
+    stays = torch.zeros(T, groups, dtype=torch.bool)
+    stays.scatter_(1, order[:, :top_groups], True)
+    c[~stays.repeat_interleave(E // groups, 1)] = -INF
+    c = c.sort(dim=1, descending=True).values[:, :top + 1]
+    return (good & ((c[:, :-1] - c[:, 1:])[:, :top] > least).all(1)).nonzero().squeeze(1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,groups,top_groups,top", [(4, 2, 1, 2), (16, 8, 3, 4), (32, 4, 2, 8),
+                                                     (96, 16, 5, 6), (256, 8, 4, 8)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_two_scores_of_a_group_that_cancel(E, groups, top_groups, top, scoring):
+    """A group's best two have large biases of opposite signs: each was rounded at its
+    own size, and their sum, which decides, is far smaller.  Neighbouring groups have
+    nearly the same scores, so that the roundings would decide in FP32."""
+    g = gen(E + groups)
+    T, size = 4000, E // groups
+    kw = dict(groups=groups, top_groups=top_groups, group_best=2)
+    for X in (64.0, 1000.0, 1e4):
+        x = torch.randn(T, 1, size, device="cuda", generator=g).repeat(1, groups, 1)
+        # of a last place of X, once the scores' slope (at most 1/4) has made it smaller
+        near = X * 2.0 ** -22 * (1 if scoring == "sigmoid" else groups)
+        x = (x + near * torch.randn(x.shape, device="cuda", generator=g)).reshape(T, E)
+        b = torch.full((groups, size), -2 * X, device="cuda")
+        b[:, 0], b[:, 1] = X, -X
+        if X == 1e4:
+            b[::3, :2] = 0.0        # groups of both kinds
+        b = b.reshape(E)
+        rows = apart64(x, top, scoring, b, groups, top_groups)
+        assert rows.numel() >= T // 4
+        check(x[rows.cuda()].contiguous(), top, scoring, b, **kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_totals_of_a_group_past_fp32(scoring):
+    """The sums of two biases of some 3e38 are infinite in FP32, not in 64 bits; a
+    group of scores that are infinite themselves is larger than those."""
+    x = torch.randn(70, 12, device="cuda", generator=gen(3))
+    for rows in ([[3e38, 2e38], [3e38, 2.5e38], [2e38, 2e38]],
+                 [[-3e38, -3e38], [-3e38, -2e38], [-2e38, -3.3e38]],
+                 [[3e38, 3e38], [INF, -3e38], [3e38, 3.2e38]],
+                 [[-INF, -INF], [-3e38, -3e38], [-INF, -3.3e38]],
+                 [[1e9, -1e9], [1.0, 1.0], [-1e9, -1e9]]):
+        b = torch.full((3, 4), -3.4e38, device="cuda")
+        b[:, 1:3] = torch.tensor(rows, device="cuda")
+        for top_groups in (1, 2):
+            # one choice a group: the scores beside 3e38 are nothing in 64 bits either
+            ids, _ = sg.moe_route(x, top_groups, scoring, b.reshape(12), groups=3,
+                                  top_groups=top_groups, group_best=2)
+            assert torch.equal(ids.cpu(), choose64(x, top_groups, scoring, b.reshape(12), groups=3,
+                                                   top_groups=top_groups, group_best=2))
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("E,top", [(5, 2), (16, 4), (64, 8), (130, 31), (1024, 16)])
 def test_ties_go_to_the_lowest(E, top):

@@ -430,10 +430,12 @@ __global__ void __launch_bounds__(256, K <= 8 ? 4 : 2) route_kernel(RouteArgs a)
     wave_lds_fence();
     constexpr int ROUNDS = (SGEMM_MOE_MAX_GROUPS + G - 1) / G;
     uint32_t total[ROUNDS];
+    float wide[ROUNDS];   // how far off a total may be
 #pragma unroll
     for (int r = 0; r < ROUNDS; ++r) {
       const int q = r * G + g;
       total[r] = kNever;
+      wide[r] = 0.0f;
       if (r * G < a.groups && q < a.groups) {
         uint32_t best = kNever, second = kNever;
         // Neighbouring groups may begin on the same bank: lanes start apart.
@@ -458,8 +460,13 @@ __global__ void __launch_bounds__(256, K <= 8 ? 4 : 2) route_kernel(RouteArgs a)
             best = max(best, k);
           }
         }
-        total[r] = a.group_best == 2 && second != kNever
-                       ? ordered(unordered(best) + unordered(second)) : best;
+        const bool two = a.group_best == 2 && second != kNever;
+        const float x = unordered(best), y = two ? unordered(second) : 0.0f;
+        total[r] = two ? ordered(x + y) : best;
+        // Each score of a total is off by half of `off` and rounded at its own size, which
+        // may be far larger than their sum's: at most 2 half steps of |x| + |y| with the
+        // sum's own rounding, and two more for those of these bounds.
+        if (fabsf(x) < INFINITY) wide[r] = off + 4.0f * kHalfStep * (fabsf(x) + fabsf(y));
       }
     }
     uint32_t* const totals = reinterpret_cast<uint32_t*>(ids[sub]);
@@ -470,7 +477,8 @@ __global__ void __launch_bounds__(256, K <= 8 ? 4 : 2) route_kernel(RouteArgs a)
     wave_lds_fence();
     uint32_t stays = 0;
     int rank_of[ROUNDS];
-    uint32_t least = 0u, next = 0u;   // the last group that stays, the first that does not
+    // The least that one that stays may be, the most that one that does not may be.
+    float low = INFINITY, high = -INFINITY;
 #pragma unroll
     for (int r = 0; r < ROUNDS; ++r) {
       if (r * G < a.groups) {
@@ -483,22 +491,21 @@ __global__ void __launch_bounds__(256, K <= 8 ? 4 : 2) route_kernel(RouteArgs a)
             rank += other[e] > total[r] || (other[e] == total[r] && o + e < q) ? 1 : 0;
         }
         rank_of[r] = rank;
-        if (rank == a.top_groups - 1) least = total[r];
-        if (rank == a.top_groups) next = total[r];
+        // A total past FP32, or of scores with NaN, may be anything.
+        const float at = unordered(total[r]);
+        const bool known = wide[r] < INFINITY;
+        if (rank < a.top_groups) low = fminf(low, known ? at - wide[r] : -INFINITY);
+        else if (q < a.groups) high = fmaxf(high, known ? at + wide[r] : INFINITY);
         const uint64_t bits = __ballot(rank < a.top_groups) >> (lane - g);
         stays |= (uint32_t)(bits & ((uint64_t(1) << G) - 1)) << (r * G);
       }
     }
     if (by_score && a.top_groups < a.groups) {
       butterfly<G>([&](auto s) {
-        least = max(least, (uint32_t)exchanged<decltype(s)::value>((int)least));
-        next = max(next, (uint32_t)exchanged<decltype(s)::value>((int)next));
+        low = fminf(low, exchanged<decltype(s)::value>(low));
+        high = fmaxf(high, exchanged<decltype(s)::value>(high));
       });
-      // Two scores a group: twice the errors.
-      if (next > kNever) {
-        const float x = unordered(least), y = unordered(next);
-        regroup = x - y <= 2.0f * off + 8.0f * kHalfStep * (fabsf(x) + fabsf(y));
-      }
+      regroup = high > -INFINITY && low <= high;
     }
     if (fewer) {
       wave_lds_fence();

@@ -371,6 +371,64 @@ def test_infinite_and_nan_logits():
     assert loss[2].isnan() and torch.equal(loss[rows], base[rows])
 
 
+# Few rows, with their logits by tiles, by rows and in planes; a split K's planes; tiles.
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,V", [(6, 4, 300), (1, 1024, 32768), (8, 300, 2000), (15, 4000, 600),
+                                   (16, 256, 9001), (19, 2894, 3306), (200, 100, 3000),
+                                   (1500, 512, 2600)])
+@pytest.mark.parametrize("tb", [False, True])
+def test_gradients_of_rows_with_an_infinite_logit(T, H, V, tb):
+    """One infinite weight makes a logit of a row +inf (then lse is, p is 0 at the
+    others and NaN there) or -inf (p is 0 there).  dB is NaN in that weight's column
+    alone, dA in the rows whose p is, and where 0 meets the weight."""
+    inf, col = float("inf"), min(V - 1, 290)
+    g = gen(T + V)
+    A, B, targets, skip = make(T, H, V, tb, g, ignored=0.3 if T > 6 else 0.0)
+    targets[targets == col] = 0
+    A[:, 0] = torch.where(torch.arange(T, device="cuda") % 3 == 1, -1.0, 1.0) + 0.1 * A[:, 0]
+    (B[col] if tb else B[:, col])[0] = inf
+    lse, dloss = torch.empty(T, device="cuda"), torch.randn(T, device="cuda", generator=g)
+    sg.linear_cross_entropy(A, B, targets, transpose_b=tb, lse=lse)
+    up, kept = (A[:, 0] > 0) & ~skip, ~skip
+    assert (lse[up] == inf).all() and torch.isfinite(lse[~up]).all()
+
+    a = torch.where(kept[:, None], A, 0.0).double()
+    b = (B.t() if tb else B).double()
+    finite = b.clone()
+    finite[0, col] = 0.0
+    z = a @ finite
+    z[:, col] = torch.where(up, inf, -inf)
+    e = sum_tol(H) * (a.abs() @ finite.abs())
+    l, d = torch.where(kept, lse, 0.0).double()[:, None], torch.where(kept, dloss, 0.0).double()
+    p = torch.where(kept[:, None], torch.exp(z - l), 0.0)
+    hit = torch.zeros_like(p)
+    hit[kept, targets[kept].long()] = 1.0
+    dz = (p - hit) * d[:, None]
+    # as in grads64, where p is not 0
+    rel = torch.where(p > 0, e + 2.3 * U * (z - l).abs() + 10 * U, 0.0)
+    tiny = 2.0 ** -126
+    dtol = d.abs()[:, None] * (p * (rel + rel * rel) + 2 * U * (p + hit) + tiny) + tiny
+    wB, tB = a.t() @ dz, a.abs().t() @ dtol + sum_tol(T) * (a.abs().t() @ dz.abs()) + 2 * T * tiny
+    pieces = max(64, V // 256 + 1)
+    wA = dz @ finite.t()
+    tA = dtol @ finite.abs().t() + (sum_tol(V) + pieces * U) * (dz.abs() @ finite.abs().t())
+    tA = tA + 2 * V * tiny
+    wA[kept & ~up, 0] = float("nan")      # 0 times the weight
+    least = sg.sgemm_linear_xent_backward_least_bytes(tb, T, V, H)
+    for ws in (None, torch.empty(least // 4, device="cuda")):
+        dA, dB = sg.linear_cross_entropy_backward(dloss, A, B, targets, lse, transpose_b=tb,
+                                                  workspace=ws)
+        dB = dB.t() if tb else dB
+        assert (dA[skip] == 0).all()
+        assert torch.equal(dA.isnan(), wA.isnan()) and dA[up].isnan().all()
+        near(dA.nan_to_num(0), wA.nan_to_num(0), tA.nan_to_num(0), "dA")
+        here = torch.arange(V, device="cuda") == col
+        if up.any():
+            assert dB[:, here].isnan().all()
+        assert torch.isfinite(dB[:, ~here]).all()
+        near(dB[:, ~here], wB[:, ~here], tB[:, ~here], "dB")
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("tb", [False, True])
 def test_gradients_against_differences(tb):

@@ -29,7 +29,8 @@ struct Targets {
   }
 };
 
-// What the gradient needs of a row: one load (workspaces are aligned to 4 bytes).
+// What the gradient needs of a row: one load (workspaces are aligned to 4 bytes).  An
+// infinite lse leaves no rest, so that exp(z - lse) is 0 at every finite z.
 struct XentRow {
   int target;
   float ref, rest;   // lse times log2 e, rounded, and what that left
@@ -37,7 +38,7 @@ struct XentRow {
 };
 __device__ __forceinline__ XentRow xent_row(int target, float lse, float dloss) {
   const float ref = lse * kLog2e;
-  return {target, ref, fmaf(lse, kLog2e, -ref), dloss};
+  return {target, ref, fabsf(ref) < INFINITY ? fmaf(lse, kLog2e, -ref) : 0.0f, dloss};
 }
 
 // The rows with a target, one after another ("kept" rows), made on the device.

@@ -135,6 +135,16 @@ def test_many_rows_of_which_some_count(T, H, V, tb):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,H,V", [(1024, 512, 30000), (1000, 1030, 15001), (700, 1500, 15000)])
+@pytest.mark.parametrize("tb", [False, True])
+def test_up_to_1024_rows_gathered_for_the_loss(T, H, V, tb):
+    """One launch numbers and copies the rows, here for a product of over 200 us."""
+    assert 2 * T * H * V > 200e-6 * 150e12
+    run(T, H, V, tb, ignored=0.4, seed=T)
+    run(T, H, V, tb, pad=3, off=1, ignored=0.0, dtype=torch.int32, seed=V)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,H,V", [(19, 2894, 3306), (3, 2647, 111), (300, 4096, 500),
                                    (1, 1024, 32768), (8, 1030, 20001), (4, 1305, 142),
                                    (14, 1330, 2235), (1000, 4096, 300), (2, 5000, 3)])

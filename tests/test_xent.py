@@ -657,6 +657,39 @@ def test_workspaces_hold_no_logits(lib):
         assert backward(nb=least - 4, **args) == sg.ERR_INVALID_ARG
 
 
+ODD = [(17, 301, 64), (19, 333, 2894), (7, 1001, 30), (23, 517, 33), (1, 3, 5), (40, 263, 100)]
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are made up")
+@pytest.mark.parametrize("T,V,H", ODD)
+@pytest.mark.parametrize("tb", [0, 1])
+def test_every_workspace_from_the_least_on_is_enough(lib, T, V, H, tb):
+    """T V need not be a multiple of four floats.  (Accepted, a call fails at its launch.)"""
+    least = sg.sgemm_linear_xent_backward_least_bytes(tb, T, V, H)
+    most = sg.sgemm_linear_xent_backward_workspace_bytes(tb, T, V, H)
+    piece = 4 * T * V      # the whole vocabulary's, and each plane's
+    near = [n + d for n in range(least, most + 2 * piece, piece) for d in range(-64, 256, 4)]
+    sizes = near + [most + d for d in range(-64, 64, 4)] + list(range(least, most + 64, 116))
+    sizes += list(range(least, least + 40000, 4)) + [least + d for d in (1, 2, 3, 5, 17)]
+    assert backward(tb, T, V, H, nb=least - 1) == sg.ERR_INVALID_ARG
+    for nb in sizes:
+        if nb >= least:
+            assert backward(tb, T, V, H, nb=nb) == sg.ERR_LAUNCH, (nb, least, most)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,V,H", ODD)
+@pytest.mark.parametrize("tb", [False, True])
+def test_workspaces_around_a_whole_vocabulary(T, V, H, tb):
+    least = sg.sgemm_linear_xent_backward_least_bytes(tb, T, V, H)
+    whole = least + 4 * T * max(V - 256, 0)
+    for ws in range(max(least, whole - 16), whole + 36, 4):
+        run(T, H, V, tb, ignored=0.3, ws=ws, seed=T)
+    for planes in (2, 3):
+        for d in range(0, 16, 4):
+            run(T, H, V, tb, ws=whole + 4 * (planes - 1) * T * V + d, seed=V)
+
+
 def test_the_header_declares_the_binding_names(lib):
     import os
     import re

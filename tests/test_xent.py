@@ -690,6 +690,18 @@ def test_workspaces_around_a_whole_vocabulary(T, V, H, tb):
             run(T, H, V, tb, ws=whole + 4 * (planes - 1) * T * V + d, seed=V)
 
 
+@pytest.mark.parametrize("tb", [0, 1])
+def test_rows_that_no_launch_copies_stay_where_they_are(lib, tb):
+    """From 2^34 values on: the loss takes them without copying them together, the
+    gradients refuse them before any launch."""
+    T, V, H = 1 << 23, 1000, 2048
+    assert sg.sgemm_linear_xent_workspace_bytes(tb, T - 1, V, H) > 4 * (T - 1) * H     # copied
+    assert sg.sgemm_linear_xent_workspace_bytes(tb, T, V, H) < 4 * T * H // 20
+    far = dict(X=FAR * 5, B=FAR * 6, t=FAR * 7, nb=1 << 45)
+    assert backward(tb, T, V, H, lse=FAR * 8, d=FAR * 9, dX=FAR * 10, dB=FAR * 11, ws=FAR * 64,
+                    **far) == sg.ERR_UNSUPPORTED
+
+
 def test_the_header_declares_the_binding_names(lib):
     import os
     import re

@@ -93,6 +93,9 @@ XentRows take_rows(Room& room, int64_t T, int64_t H, bool backward) {
 // product that takes this long, and saves the products of the rows left out.
 constexpr double kGatherSeconds = 200e-6;
 
+// The copies' grid, four values a thread.
+bool rows_fit(int64_t T, int64_t H) { return grid_fits(cdiv(T * cdiv(H, 4), 256), 256); }
+
 constexpr int64_t kLossRowsFrom = 1024;   // tokens
 
 // How many planes (product_planes.hpp) T x V over H is best left in; 0: rather tiles
@@ -168,7 +171,7 @@ Forward plan_forward(bool trans_b, int64_t T, int64_t V, int64_t H, void* ws) {
   Forward f = {};
   f.v = choose(trans_b, T, V, H);
   if (f.v == nullptr) return f;
-  f.gathered = 2.0 * T * V * H / 150e12 > kGatherSeconds;
+  f.gathered = 2.0 * T * V * H / 150e12 > kGatherSeconds && rows_fit(T, H);
   f.planes = f.gathered ? 0 : choose_planes(f.v, false, trans_b, T, V, H);
   if (!f.gathered && few_logits(trans_b, T, V, H) && V % 4 != 0 && 4 * V * H >= kFewForward) {
     f.few = few_grid(true, false, T, H, V);
@@ -532,8 +535,7 @@ int sgemm_linear_xent_backward(int trans_b, int64_t T, int64_t V, int64_t H, con
   if (overlaps(out[0], out[1]) || overlaps(out[0], ws) || overlaps(out[1], ws))
     return SGEMM_ERR_INVALID_ARG;
   const XentVariant* v = V > 0 ? choose(trans_b, T, b.columns, H) : nullptr;
-  if ((V > 0 && v == nullptr) || !grid_fits(cdiv(T * cdiv(H, 4), 256), 256))
-    return SGEMM_ERR_UNSUPPORTED;
+  if ((V > 0 && v == nullptr) || !rows_fit(T, H)) return SGEMM_ERR_UNSUPPORTED;
 
   ldx = leading(T, H, ldx);
   ldb = leading(br, bc, ldb);

@@ -74,8 +74,10 @@ typedef struct sgemm_moe_router {
  * An expert whose logit or whose c is -infinity is never chosen: where fewer than
  * top remain, the rest of a token's choices are -1 with weight 0, which
  * sgemm_moe_sort drops.  A NaN score counts as infinite, and makes NaN weights.
- * The choice is that of the scores in exact arithmetic: what FP32 cannot tell apart
- * is computed again in FP64.  Experts over SGEMM_MOE_MAX_EXPERTS, top or groups over
+ * The choice is that of the scores in FP64: what FP32 cannot tell apart is computed
+ * again, and only what FP64 rounds to the same number is equal (two sigmoids next to
+ * 1 with a bias, say).  Without a bias, and without groups of two scores, the logits
+ * themselves decide, whose order is that of exact scores.  Experts over SGEMM_MOE_MAX_EXPERTS, top or groups over
  * their limits are SGEMM_ERR_UNSUPPORTED.  T == 0 is a no-op. */
 int sgemm_moe_route(int64_t T, int64_t E, int64_t top, const float *logits,
                     int64_t ldl, const sgemm_moe_router *router,

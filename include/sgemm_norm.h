@@ -19,9 +19,11 @@
  * layer), optional.
  *
  * Everything is summed in FP32: the mean first, then the squares of what is left
- * of it, so that a large mean costs no accuracy.  Squares past FP32 (|x - mean|
- * over about 1e19) give rstd = 0.  NaN and infinities give NaN in their row, and
- * in dweight and dbias of their columns.
+ * of it, which do not cancel however large the mean is.  The mean itself is an FP32
+ * sum, rounded: it is off by a few 2^-24 of the row's mean |x|, and that times rstd
+ * goes into every y of the row.  Squares past FP32 (|x - mean| over about 1e19) give
+ * rstd = 0, a row whose sum is past FP32 gives NaN.  NaN and infinities give NaN in
+ * their row, and in dweight and dbias of their columns.
  *
  * Contracts as for sgemm.h: device memory owned by the caller, 4-byte aligned,
  * any leading dimension; enqueued on stream without allocating or

@@ -29,8 +29,9 @@
  * allocating or synchronising; arguments checked before any HIP call; results the
  * same from run to run (no atomics).  Leading dimensions of X and B, V and H are
  * limited to SGEMM_XENT_MAX_LD; more is SGEMM_ERR_UNSUPPORTED.  Infinite and NaN
- * logits follow the formulas: a row with one of +infinity has lse = +infinity, one
- * with a NaN has NaN.  Finite ones are taken to be below 2e38 in size.
+ * logits follow the formulas: a row with one of +infinity has lse = +infinity and a dZ
+ * that is NaN there alone, one with a NaN has NaN.  Finite ones are taken to be below
+ * 2e38 in size.
  */
 #ifndef SGEMM_XENT_H
 #define SGEMM_XENT_H
@@ -69,7 +70,8 @@ int64_t sgemm_linear_xent_workspace_bytes(int trans_b, int64_t T, int64_t V, int
  *              vocabulary goes in more pieces, down to
  *              sgemm_linear_xent_backward_least_bytes, below which it is
  *              SGEMM_ERR_INVALID_ARG.
- * T == 0 sets dB to 0; H == 0 or V == 0 leaves nothing but dX = 0. */
+ * T == 0 sets dB to 0; H == 0 or V == 0 leaves nothing but dX = 0.  T H (H in fours)
+ * of 2^34 or more is SGEMM_ERR_UNSUPPORTED. */
 int sgemm_linear_xent_backward(int trans_b, int64_t T, int64_t V, int64_t H,
                                const float *X, int64_t ldx, const float *B,
                                int64_t ldb, const void *targets, int id_bytes,

@@ -15,10 +15,16 @@
 // kNormRun rows: the rounding errors grow with n / 256 + 256 rather than n.
 //
 // Bound by HBM: 8 bytes an element forward, 12 backward (16 with a residual).
-// Measured on MI355X: 32768 x 4096 forward 192 to 200 us (5.4 TB/s), 16 x 1024 3.5; the
-// gradients of 32768 x 1024 with a residual 84 + 5 us (6.0 TB/s), of 1000 x 777 6.3 + 3.8.
-// The wide kernels read a row from the caches for their second and third step: 4000 x
-// 16384 backward 309 us, 2.5 TB/s of what has to move.
+// Measured on MI355X (averages): 32768 x 4096 forward 201 us (5.3 TB/s), 4000 x 16384 103
+// (5.1), 16 x 1024 3.5; the gradients of 32768 x 1024 with a residual 84 + 5 us (6.0 TB/s), of
+// 4000 x 8192 70 + 8 (5.0), of 1000 x 777 6.3 + 3.8.
+//
+// A workgroup of 1024 has 128 registers a lane.  Forward, four groups of four columns
+// take 64 of them (a row, the next one, weight, bias): up to 16384 columns.  Backward, two
+// take 64 (dy, x and the next ones, weight, residual and both sums), four would take
+// all: up to 8192.  The wide kernels past that read a row from the caches for their
+// second and third step: 4000 x 20000 forward 175 us (3.7 TB/s of what has to move);
+// backward 4000 x 12288  139 + 92 + 9, 4000 x 16384  187 + 114 + 9 (2.5).
 #pragma once
 
 #include "lanes.hpp"

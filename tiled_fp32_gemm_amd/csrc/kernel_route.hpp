@@ -10,21 +10,25 @@
 // and the lanes' lists meet by a butterfly: the larger of A[i] and B[K-1-i] are
 // the best K of both, a bitonic sequence, which log2 K rounds sort.
 //
-// The choice is that of exact scores.  Without a bias, and without groups that
+// The choice is that of FP64 scores.  Without a bias, and without groups that
 // count two scores, it goes by the logits themselves, whose order is the scores'.
 // Otherwise FP32 scores decide unless two that matter are closer than their
-// errors (kSoftmaxOff below), as for one token in about a thousand; then the wave
+// errors (kSoftmaxOff below, and each score's rounding at its own size, also where a
+// group's two cancel), as for one token in about a thousand; then the wave
 // computes the scores again in FP64, those that may be chosen (reorder), or all
 // where the groups are open or there are too many (refine).
 //
-// Bound by vector instructions, about 1330 a wave for eight tokens' best 8 of 256 in
-// groups by sigmoid and bias, where the copies of 32768 such rows would take 7.3 us:
-// measured on MI355X 16.6 to 17.3 us, of which the last waves' FP64 takes 2.5; without bias and
-// groups 10.8, 8191 tokens of 64 experts 3.8.  Where the groups that stay have at most half
-// of the experts, only those are sorted (all: 1612 instructions, 18.8 us).  Sixteen lanes
-// a token instead of eight (twice the waves, half the experts a lane) took 23.9 for 19.9, a
-// branch for each expert's special cases 37.  A batch of equal scores, all in FP64: 64 us.
-// The gradient is bound by HBM: 32768 x 256 (69 MB) in 13.2 to 14.3 us.
+// Bound by vector instructions, 1357 a wave for eight tokens' best 8 of 256 in groups by
+// sigmoid and bias, where the copies of 32768 such rows would take 7.3 us.  Measured on
+// MI355X, calls one after another over several inputs: 16.3 to 19.5 us, by the inputs (2.5 of
+// it the FP64 of the last waves); without bias and groups 10 to 11.5, 8191 tokens of 64
+// experts 3.8.  Where the groups that stay have at most half of the experts, only those are sorted
+// (all: 300 instructions and 1.1 us more).  Sixteen lanes a token instead of eight (twice
+// the waves, half the experts a lane) took 23.9 for 19.9, a branch for each expert's special
+// cases 37.  A batch of equal scores, all in FP64: 64 us, 78 in groups.
+// The gradient is bound by HBM: 32768 x 256 (69 MB) with the whole softmax in 14.3 us (the
+// kernel 16.4 on average of forty under the profiler, 13.9 at least); renormalised 9.0, by
+// sigmoid 10.1 to 10.5 (33.6 MB to write, a cache line to read for each choice).
 #pragma once
 
 #include "../../include/sgemm_moe.h"

@@ -22,11 +22,12 @@
 // holds, reaches no gradient.
 //
 // Bound by the matrix pipe for many rows, by reading B for a few.  Measured on MI355X
-// with B stored V x H, H = 1024, V = 32768: 6144 rows forward 2807 us (147 TFLOP/s;
-// the product alone would take 2745), numbering and copying them 6 + 12, joining 512
-// strips of 8192 tokens 12; the gradient of half that vocabulary for 8192 rows 1912 us,
-// 97 more than a product, of which dz's 512 MiB are most; 16 rows forward 28 us (4.8
-// TB/s) and 4.6 for their 1024 strips.
+// with B stored V x H, H = 1024, V = 32768 (averages of forty passes over three states in
+// turn): 6144 rows forward 2910 us (142 TFLOP/s; 2823 at least, 146), numbering and copying
+// them 6 + 12, joining 512 strips of 8192 tokens 12; the gradient of half that vocabulary
+// for 8192 rows 1927 us, 95 more than a product, of which dz's 512 MiB are most; 16 rows
+// forward 28.8 us (4.7 TB/s) and 4.4 for their 1024 strips; 64 rows 43.8 + 5.4; 1000 rows
+// 545 (123 TFLOP/s), 6 for their copies and 6 for the strips.
 #pragma once
 
 #include <float.h>

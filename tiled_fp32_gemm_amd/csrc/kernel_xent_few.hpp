@@ -3,29 +3,33 @@
 //
 //   dB = sum over tokens of x by dz        dX = dz·op(B)'
 //
-// Each entry of B meets the entry of dB at its place: a lane holds four columns of the
+// Each entry of B meets the entry of dB at its place: a lane holds a few columns of the
 // rows of the one factor (X, or dz) in registers, goes down B's rows with the other
 // factor's numbers from LDS, and for each row stores dB and takes B into its part of
 // dX.  B is read and dB written once, which is what it is bound by; the parts of dX
 // are added up by xent_few_sum_kernel.  Rows without a target count as zeros, so
-// nothing has to be copied together for so few.
+// nothing has to be copied together for so few.  (dz comes from the logits, a launch
+// before this one that reads B too: twice in all.)
 //
-//   xent_few_down_kernel    B is V x H: a lane has four of H in each of four waves,
-//                           which take the rows by turns; dX's sums stay in registers.
+//   xent_few_down_kernel    B is V x H: a lane has four columns of H, two for sixteen rows,
+//                           in each of four waves, which take the rows by turns; dX's
+//                           sums stay in registers.
 //                           Without the gradients: the logits where B is H x V.
 //   xent_few_across_kernel  B is H x V: a wave has 256 of V, four waves side by side;
 //                           a row of B is summed over the lanes, several rows at once.
 //
-// Measured on MI355X (us; tokens, H, V):
-//   down    8, 3264, 7145  35.9 (5.2 TB/s), 8, 3271, 7145  40.1, 4, 1024, 33000  46.0
-//           (5.9), 4, 1030, 33000  57.5, 1, 2885, 29858  155 (4.4); the logits of 8, 1024,
-//           32768  29.7 (4.5) and 2, 2871, 34831  73.5 (5.4), where products by rows or
-//           tiles took 87 to 180
-//   across  8, 1024, 32768  47.8 (5.6), 2, 2871, 34831  163 (4.9)
-//   All of the gradients, against the rows' copies, three products and dX's scatter:
-//   down, sixteen rows 1024, 32768  91 for 111, 64, 60000  31 for 41 (four columns in a lane
-//   would spill: 185 for 113), 12, 2217, 5372  50 for 66; across, 9, 1030, 20001  64 for 96,
-//   sixteen rows 1024, 32768  89 for 114
+// Measured on MI355X (us; tokens, H, V; the kernel's average over thirty passes and three
+// weights in turn):
+//   down    8, 3264, 7145  35.9 (5.2 TB/s), 7, 3271, 7145  41, 4, 1024, 33000  46.0
+//           (5.9), 4, 1030, 33000  57.5, 1, 2885, 29858  155 (4.4), 16, 1024, 32768  61
+//           (4.4); the logits of 8, 1024, 32768  30.0 (4.5) and 2, 2871, 34831  74 (5.4),
+//           where products by rows or tiles took 87 to 180
+//   across  8, 1024, 32768  49.7 (5.4), 2, 2871, 34831  164 (4.9), 16, 1024, 32768  65 (4.2)
+//   All of the gradients, calls one after another with three weights in turn, against the
+//   rows' copies, three products and dX's scatter: down, sixteen rows 1024, 32768  92 for
+//   111, 64, 60000  30 for 41 (four columns in a lane would spill: 185 for 113), 12, 2217,
+//   5372  51 for 66; across, 9, 1030, 20001  64 for 96, sixteen rows 1024, 32768  92 for 114
+//   (85 with one weight, as some of it stays in the caches)
 //   Columns four together in a lane (16-byte accesses at any alignment) down: 3271 59.5,
 //   1030 87.  dB past the caches down: 49 and 76, as the ends of unaligned rows' pieces
 //   are then written in parts; across, where a workgroup's piece is 4 KB, in them: 149 for
